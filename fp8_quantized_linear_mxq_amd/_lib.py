@@ -15,7 +15,8 @@ LIB_PATH = os.path.join(PKG, "libmxq.so")
 
 MXFP4, MXFP8, NVFP4, INT4 = 1, 2, 3, 4
 BF16 = 5   # unquantized bf16 activations (GEMM operand only)
-FORMATS = {"MXFP4": MXFP4, "MXFP8": MXFP8, "NVFP4": NVFP4, "INT4": INT4}
+INT8 = 6   # row-wise int8, one fp32 scale per row
+FORMATS = {"MXFP4": MXFP4, "MXFP8": MXFP8, "NVFP4": NVFP4, "INT4": INT4, "INT8": INT8}
 FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 DT_F32, DT_BF16 = 1, 2
 OP_QUANTIZE, OP_GEMM, OP_SELECT, OP_QUANTIZE_MSE, OP_LOWRANK_SPLIT = 1, 2, 3, 4, 5
@@ -27,6 +28,7 @@ STATUS = {0: "MXQ_OK", 1: "MXQ_ERR_INVALID_ARG", 2: "MXQ_ERR_UNSUPPORTED",
 
 # Every symbol include/mxq.h declares.
 EXPORTS = ("mxq_quantize", "mxq_quantize_noalloc", "mxq_quantize_lrp", "mxq_pack_l1t", "mxq_gemm", "mxq_gemm_mixed", "mxq_conv3x3_gemm_mixed",
+           "mxq_gemm_grouped", "mxq_qk_norm_rope",
            "mxq_select_format", "mxq_quantize_mse", "mxq_lowrank_split",
            "mxq_act_format_for_step", "mxq_workspace_size", "mxq_storage",
            "mxq_status_string", "mxq_version")
@@ -76,6 +78,11 @@ def load():
     lib.mxq_gemm.restype = i32
     lib.mxq_gemm_mixed.argtypes = [qp, qp, i32, vp, vp, i64, vp, i32, vp, vp, i64, i64, vp, sz, vp]
     lib.mxq_gemm_mixed.restype = i32
+    lib.mxq_gemm_grouped.argtypes = [qp, qp, i32, vp, vp, vp, i64, vp]
+    lib.mxq_gemm_grouped.restype = i32
+    lib.mxq_qk_norm_rope.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, vp, C.c_float, vp, vp, i64,
+                                     i32, i32, vp, vp, i64, i64, vp, i64, i64, vp]
+    lib.mxq_qk_norm_rope.restype = i32
     lib.mxq_conv3x3_gemm_mixed.argtypes = [qp, i64, i64, qp, i32, vp, vp, vp, i64, i64, vp, sz,
                                            vp]
     lib.mxq_conv3x3_gemm_mixed.restype = i32
@@ -160,7 +167,9 @@ def empty_qtensor(fmt: int, rows: int, cols: int, device="cuda") -> QTensor:
     # row strides padded to the ABI's alignment (16 B codes; 4 B scales, 16 B
     # for INT4's fp32 scales)
     codes = torch.empty((rows, (cb + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    if fmt == INT4:
+    if fmt == INT8:
+        scales = torch.empty((rows, 1), dtype=torch.float32, device=device)
+    elif fmt == INT4:
         scales = torch.empty((rows, (sb // 4 + 3) // 4 * 4), dtype=torch.float32, device=device)
     else:
         scales = torch.empty((rows, (sb + 3) // 4 * 4), dtype=torch.uint8, device=device)
@@ -175,6 +184,18 @@ def bf16_operand(x) -> QTensor:
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("bf16_operand needs a row-major 2-D bfloat16 tensor")
     return QTensor(BF16, x.shape[0], x.shape[1], x, None)
+
+
+def int8_operand(codes, scales) -> QTensor:
+    """int8 codes [rows, K] (cuda, row-major) and one float32 scale per row
+    ([rows] or [rows, 1]) as a quantized operand."""
+    import torch
+    if codes.dim() != 2 or codes.element_size() != 1 or (codes.shape[1] > 1 and codes.stride(1) != 1):
+        raise ValueError("int8_operand needs row-major 2-D 8-bit codes")
+    rows, cols = codes.shape
+    if scales.dtype != torch.float32 or scales.shape not in ((rows,), (rows, 1)):
+        raise ValueError("int8_operand needs float32 scales of shape [rows] or [rows, 1]")
+    return QTensor(INT8, rows, cols, codes, scales)
 
 
 def pack_l1t(l1t, stream=None):
@@ -268,6 +289,71 @@ def gemm_mixed(a: QTensor, groups: list, w_perm, n_out: int, u=None, l2t=None, b
                             _ptr(out), out.stride(0), n_out, wsp, wsn, _stream(stream))
     _check("mxq_gemm_mixed", st)
     return out
+
+
+def gemm_grouped(a: QTensor, w: QTensor, offsets, bias=None, out=None, stream=None):
+    """mxq_gemm_grouped: rows of ``a`` sorted by expert, ``offsets`` (int32,
+    cuda, [experts + 1]) their groups, ``w`` the experts' weights one after
+    the other ([experts * N, K]), ``bias`` bf16 [experts, N]; returns the bf16
+    [rows, N] output tensor (rows of no group are left as they are in ``out``)."""
+    import torch
+    lib = load()
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
+        raise ValueError("gemm_grouped needs contiguous 1-D int32 offsets")
+    groups = offsets.shape[0] - 1
+    n = w.rows // groups if groups > 0 else 0
+    if out is None:
+        out = torch.empty((a.rows, n), dtype=torch.bfloat16, device=a.codes.device)
+    ac, wc = a.c(), w.c()
+    st = lib.mxq_gemm_grouped(C.byref(ac), C.byref(wc), groups, _ptr(offsets), _ptr(bias), _ptr(out),
+                              out.stride(0), _stream(stream))
+    _check("mxq_gemm_grouped", st)
+    return out
+
+
+def qk_norm_rope(x, n_q_heads: int, n_k_heads: int, head_dim: int, q_weight=None, k_weight=None,
+                 cos=None, sin=None, positions=None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, stream=None):
+    """mxq_qk_norm_rope on the 2-D output of a fused projection (float32 or
+    bfloat16, cuda): RMS norm of every query and key head and the position
+    rotation given by the float32 tables ``cos`` and ``sin`` [n_pos, rot/2].
+    Returns (q [tokens, n_q_heads, head_dim], k [tokens, n_k_heads, head_dim]);
+    ``q_out`` and ``k_out`` may be given with any token and head strides."""
+    import torch
+    lib = load()
+    if x.dtype not in (torch.bfloat16, torch.float32) or x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("qk_norm_rope needs a row-major 2-D float32 or bfloat16 tensor")
+    tokens = x.shape[0]
+    if x.shape[1] < (n_q_heads + n_k_heads) * head_dim:
+        raise ValueError("qk_norm_rope: x is narrower than its heads")
+    for g in (q_weight, k_weight):
+        if g is not None and (g.dtype != x.dtype or g.shape != (head_dim,) or not g.is_contiguous()):
+            raise ValueError("qk_norm_rope: weights are contiguous [head_dim] tensors of x's dtype")
+    rot = n_pos = 0
+    if cos is not None:
+        for t in (cos, sin):
+            if t is None or t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape \
+                    or not t.is_contiguous():
+                raise ValueError("qk_norm_rope: cos and sin are contiguous float32 [n_pos, rot / 2]")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if positions is not None and (positions.dtype != torch.int32 or positions.shape != (tokens,)
+                                      or not positions.is_contiguous()):
+            raise ValueError("qk_norm_rope: positions are contiguous int32 [tokens]")
+    outs = []
+    for t, heads in ((q_out, n_q_heads), (k_out, n_k_heads)):
+        if t is None:
+            t = torch.empty((tokens, heads, head_dim), dtype=x.dtype, device=x.device)
+        elif t.dtype != x.dtype or t.shape != (tokens, heads, head_dim) or t.stride(2) != 1:
+            raise ValueError("qk_norm_rope: outputs are [tokens, heads, head_dim] of x's dtype")
+        outs.append(t)
+    q, k = outs
+    st = lib.mxq_qk_norm_rope(_ptr(x), DT_BF16 if x.dtype == torch.bfloat16 else DT_F32, tokens,
+                              x.stride(0), n_q_heads, n_k_heads, head_dim, _ptr(q_weight),
+                              _ptr(k_weight), eps, _ptr(cos), _ptr(sin), n_pos, rot,
+                              int(interleaved), _ptr(positions), _ptr(q), q.stride(0), q.stride(1),
+                              _ptr(k), k.stride(0), k.stride(1), _stream(stream))
+    _check("mxq_qk_norm_rope", st)
+    return q, k
 
 
 def conv3x3_gemm_mixed(x: QTensor, height: int, width: int, groups: list, w_perm, n_out: int,

@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libmxq.so")
 PROBE_SRC = os.path.join(PKG, "probe", "mfma_probe.hip")
 PROBE_LIB = os.path.join(PKG, "probe", "libmxq_probe.so")
 SOURCES = ["api.cpp", "quantize.hip", "lowrank.hip", "gemm_mx.hip", "gemm_dq.hip", "gemm_dqp.hip",
-           "mse.hip", "lowrank_split.hip"]
+           "mse.hip", "lowrank_split.hip", "quantize_i8.hip", "gemm_i8.hip", "gemm_few.hip",
+           "qk_norm.hip"]
 ARCH = "gfx950"
 
 
@@ -51,7 +52,7 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(6, os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]

@@ -21,14 +21,18 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 int block_of(int fmt) { return fmt == MXQ_FMT_NVFP4 ? 16 : 32; }
 
 // The quantized formats (BF16, unquantized activations, is separate).
-bool known_fmt(int fmt) { return fmt >= MXQ_FMT_MXFP4 && fmt <= MXQ_FMT_INT4; }
+bool known_fmt(int fmt) {
+  return (fmt >= MXQ_FMT_MXFP4 && fmt <= MXQ_FMT_INT4) || fmt == MXQ_FMT_INT8;
+}
 
 int64_t code_bytes(int fmt, int64_t cols) {
-  return fmt == MXQ_FMT_BF16 ? 2 * cols : fmt == MXQ_FMT_MXFP8 ? cols : cols / 2;
+  if (fmt == MXQ_FMT_BF16) return 2 * cols;
+  return fmt == MXQ_FMT_MXFP8 || fmt == MXQ_FMT_INT8 ? cols : cols / 2;
 }
 
 int64_t scale_bytes(int fmt, int64_t cols) {
   if (fmt == MXQ_FMT_BF16) return 0;
+  if (fmt == MXQ_FMT_INT8) return 4;   // one fp32 per row
   const int64_t blocks = cols / block_of(fmt);
   return fmt == MXQ_FMT_INT4 ? blocks * 4 : blocks;
 }
@@ -59,6 +63,9 @@ mxq_status check_qtensor(const mxq_qtensor* t) {
     return MXQ_ERR_ALIGNMENT;
   return MXQ_OK;
 }
+
+constexpr int64_t kMaxKInt8 = 1 << 17;
+constexpr int32_t kMaxGroups = 1 << 16;
 
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
@@ -202,6 +209,9 @@ static mxq_status quantize_impl(const void* x, int32_t dtype, int64_t rows, int6
     if (!lr_l1t || !lr_u || ld_u < lr_rank) return MXQ_ERR_INVALID_ARG;
     if (!aligned(lr_l1t, 16) || !aligned(lr_u, 16) || ld_u % 4) return MXQ_ERR_ALIGNMENT;
   }
+  // the fused kernel that reads the packed L1 writes block formats
+  if (packed && out->fmt == MXQ_FMT_INT8) return MXQ_ERR_UNSUPPORTED;
+  if (out->fmt == MXQ_FMT_INT8 && (rows > INT32_MAX || cols > INT32_MAX)) return MXQ_ERR_SHAPE;
   const bool dynamic_nv = out->fmt == MXQ_FMT_NVFP4 && !static_tensor_scale;
   if (!noalloc && dynamic_nv && (!workspace || ws_bytes < (size_t)kAmaxPartials * 4))
     return MXQ_ERR_WORKSPACE;
@@ -248,7 +258,8 @@ static mxq_status quantize_impl(const void* x, int32_t dtype, int64_t rows, int6
     l.packed = packed;
     a.lr = &l;
   }
-  hipError_t e = launch_quantize(a, as_stream(stream));
+  hipError_t e = out->fmt == MXQ_FMT_INT8 ? launch_quantize_i8(a, as_stream(stream))
+                                          : launch_quantize(a, as_stream(stream));
   return from_hip(e);
 }
 
@@ -301,11 +312,15 @@ static mxq_status gemm_checks(const mxq_qtensor* a, const mxq_qtensor* w, const 
   if (st != MXQ_OK) return st;
   if (a->cols != w->cols) return MXQ_ERR_SHAPE;
   if (n_out < 0 || lr_rank < 0 || lr_rank > 128 || lr_rank % 16) return MXQ_ERR_INVALID_ARG;
-  // activations: MXFP4, MXFP8, NVFP4 or bf16; weights: MXFP4, NVFP4 or INT4
+  // activations: MXFP4, MXFP8, NVFP4 or bf16; weights: MXFP4, NVFP4 or INT4;
+  // INT8 only with INT8
   if (a->fmt == MXQ_FMT_INT4 || w->fmt == MXQ_FMT_MXFP8 || w->fmt == MXQ_FMT_BF16)
     return MXQ_ERR_UNSUPPORTED;
+  const bool i8 = a->fmt == MXQ_FMT_INT8;
+  if (i8 != (w->fmt == MXQ_FMT_INT8)) return MXQ_ERR_UNSUPPORTED;
   if (a->rows == 0 || w->rows == 0 || n_out == 0) return MXQ_OK;
-  if (a->cols % 128) return MXQ_ERR_SHAPE;
+  // int8 sums stay within int32 up to K = 2**17
+  if (i8 ? a->cols == 0 || a->cols > kMaxKInt8 : a->cols % 128 != 0) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX || w->rows > INT32_MAX || a->cols > INT32_MAX || n_out > INT32_MAX)
     return MXQ_ERR_SHAPE;
   if (!out || ld_out < n_out) return MXQ_ERR_INVALID_ARG;
@@ -317,18 +332,14 @@ static mxq_status gemm_checks(const mxq_qtensor* a, const mxq_qtensor* w, const 
   return MXQ_OK;
 }
 
-// One GEMM launch of the route for (a->fmt, w->fmt).  With cv_c > 0 the
-// activation operand is the implicit im2col of a 3x3 convolution over an
-// [images * cv_h * cv_w][cv_c] pixel-row input (K = w->cols = 9 * cv_c).
-static hipError_t gemm_launch(const mxq_qtensor* a, const mxq_qtensor* w, const int32_t* col_map,
-                              const float* lr_u, int64_t ld_u, const void* lr_l2t,
-                              int32_t lr_rank, const void* bias, void* out, int64_t ld_out,
-                              int64_t n_out, void* workspace, size_t ws_bytes, hipStream_t s,
-                              int64_t cv_h = 0, int64_t cv_w = 0, int64_t cv_c = 0) {
+static GemmArgs gemm_args(const mxq_qtensor* a, const mxq_qtensor* w, const int32_t* col_map,
+                          const float* lr_u, int64_t ld_u, const void* lr_l2t, int32_t lr_rank,
+                          const void* bias, void* out, int64_t ld_out, int64_t n_out,
+                          void* workspace, size_t ws_bytes) {
   GemmArgs g;
-  g.cv_h = cv_h;
-  g.cv_w = cv_w;
-  g.cv_c = cv_c;
+  g.cv_h = g.cv_w = g.cv_c = 0;
+  g.goff = nullptr;
+  g.groups = 0;
   g.ws = static_cast<float*>(workspace);
   g.ws_bytes = workspace ? (int64_t)ws_bytes : 0;
   g.a_fmt = a->fmt;
@@ -355,6 +366,23 @@ static hipError_t gemm_launch(const mxq_qtensor* a, const mxq_qtensor* w, const 
   g.out = static_cast<uint16_t*>(out);
   g.ld_out = ld_out;
   g.n_out = n_out;
+  return g;
+}
+
+// One GEMM launch of the route for (a->fmt, w->fmt).  With cv_c > 0 the
+// activation operand is the implicit im2col of a 3x3 convolution over an
+// [images * cv_h * cv_w][cv_c] pixel-row input (K = w->cols = 9 * cv_c).
+static hipError_t gemm_launch(const mxq_qtensor* a, const mxq_qtensor* w, const int32_t* col_map,
+                              const float* lr_u, int64_t ld_u, const void* lr_l2t,
+                              int32_t lr_rank, const void* bias, void* out, int64_t ld_out,
+                              int64_t n_out, void* workspace, size_t ws_bytes, hipStream_t s,
+                              int64_t cv_h = 0, int64_t cv_w = 0, int64_t cv_c = 0) {
+  GemmArgs g = gemm_args(a, w, col_map, lr_u, ld_u, lr_l2t, lr_rank, bias, out, ld_out, n_out,
+                         workspace, ws_bytes);
+  g.cv_h = cv_h;
+  g.cv_w = cv_w;
+  g.cv_c = cv_c;
+  if (a->fmt == MXQ_FMT_INT8) return few_rows(g) ? launch_gemm_few(g, s) : launch_gemm_i8(g, s);
   // E2M1 x E2M1 is exact on the scaled MFMA; every other pair is dequantized
   // exactly to 16-bit operands (E4M3 MFMA products are not summed to fp32
   // accuracy on this hardware)
@@ -410,6 +438,94 @@ mxq_status mxq_gemm_mixed(const mxq_qtensor* a, const mxq_qtensor* w_groups, int
   return MXQ_OK;
 }
 
+mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t n_groups,
+                            const int32_t* offsets, const void* bias, void* out, int64_t ld_out,
+                            void* stream) {
+  mxq_status st = check_qtensor(a);
+  if (st != MXQ_OK) return st;
+  st = check_qtensor(w);
+  if (st != MXQ_OK) return st;
+  if (n_groups < 1 || n_groups > kMaxGroups) return MXQ_ERR_INVALID_ARG;
+  if (a->cols != w->cols || w->rows % n_groups) return MXQ_ERR_SHAPE;
+  const bool i8 = a->fmt == MXQ_FMT_INT8 && w->fmt == MXQ_FMT_INT8;
+  const bool w4 = w->fmt == MXQ_FMT_MXFP4 && (a->fmt == MXQ_FMT_MXFP4 || a->fmt == MXQ_FMT_BF16);
+  if (!i8 && !w4) return MXQ_ERR_UNSUPPORTED;
+  const int64_t n = w->rows / n_groups;
+  if (a->rows == 0 || n == 0) return MXQ_OK;
+  if (a->cols == 0 || (i8 ? a->cols > kMaxKInt8 : a->cols % 128 != 0)) return MXQ_ERR_SHAPE;
+  if (a->rows > INT32_MAX / 2 || w->rows > INT32_MAX || a->cols > INT32_MAX) return MXQ_ERR_SHAPE;
+  if (!offsets || !out || ld_out < n) return MXQ_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4) || !aligned(out, 2)) return MXQ_ERR_ALIGNMENT;
+  unsigned* dbg = nullptr;
+  st = device_entry(&dbg);
+  if (st != MXQ_OK) return st;
+  GemmArgs g = gemm_args(a, w, nullptr, nullptr, 0, nullptr, 0, bias, out, ld_out, n, nullptr, 0);
+  g.N = n;
+  g.goff = offsets;
+  g.groups = n_groups;
+  const hipStream_t s = as_stream(stream);
+  if (few_rows(g)) return from_hip(launch_gemm_few(g, s));
+  if (i8) return from_hip(launch_gemm_i8(g, s));
+  return from_hip(a->fmt == MXQ_FMT_MXFP4 ? launch_gemm_mx(g, s) : launch_gemm_dqp(g, s));
+}
+
+mxq_status mxq_qk_norm_rope(const void* x, int32_t dtype, int64_t tokens, int64_t ldx,
+                            int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+                            const void* q_weight, const void* k_weight, float eps,
+                            const float* cos, const float* sin, int64_t n_pos, int32_t rot_dim,
+                            int32_t interleaved, const int32_t* positions,
+                            void* q_out, int64_t q_token_stride, int64_t q_head_stride,
+                            void* k_out, int64_t k_token_stride, int64_t k_head_stride,
+                            void* stream) {
+  if ((dtype != MXQ_DT_F32 && dtype != MXQ_DT_BF16) || tokens < 0 || n_q_heads < 0 ||
+      n_k_heads < 0 || head_dim <= 0 || rot_dim < 0 || rot_dim > head_dim || n_pos < 0 ||
+      (interleaved != 0 && interleaved != 1) || !(eps >= 0.f))
+    return MXQ_ERR_INVALID_ARG;
+  if (head_dim % 8 || head_dim > 512 || rot_dim % 8) return MXQ_ERR_SHAPE;
+  const int64_t heads = (int64_t)n_q_heads + n_k_heads;
+  if (tokens == 0 || heads == 0) return MXQ_OK;
+  if (heads > (1 << 20) || tokens > INT32_MAX) return MXQ_ERR_SHAPE;
+  if (!x || ldx < heads * head_dim) return MXQ_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!cos || !sin)) return MXQ_ERR_INVALID_ARG;
+  // without positions token t is at position t
+  if (rot_dim > 0 && !positions && tokens > n_pos) return MXQ_ERR_SHAPE;
+  if ((n_q_heads > 0 && !q_out) || (n_k_heads > 0 && !k_out)) return MXQ_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || ldx % 8 || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+      (rot_dim > 0 && (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4))))
+    return MXQ_ERR_ALIGNMENT;
+  if (n_q_heads > 0 && (!aligned(q_out, 16) || q_token_stride % 8 || q_head_stride % 8))
+    return MXQ_ERR_ALIGNMENT;
+  if (n_k_heads > 0 && (!aligned(k_out, 16) || k_token_stride % 8 || k_head_stride % 8))
+    return MXQ_ERR_ALIGNMENT;
+  unsigned* dbg = nullptr;
+  const mxq_status st = device_entry(&dbg);
+  if (st != MXQ_OK) return st;
+  QkNormArgs a;
+  a.x = x;
+  a.dtype = dtype;
+  a.tokens = tokens;
+  a.ldx = ldx;
+  a.n_q = n_q_heads;
+  a.n_k = n_k_heads;
+  a.head_dim = head_dim;
+  a.wq = q_weight;
+  a.wk = k_weight;
+  a.eps = eps;
+  a.cos = cos;
+  a.sin = sin;
+  a.n_pos = n_pos;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.pos = positions;
+  a.q = q_out;
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
+  a.k = k_out;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  return from_hip(launch_qk_norm_rope(a, as_stream(stream)));
+}
+
 mxq_status mxq_conv3x3_gemm_mixed(const mxq_qtensor* x, int64_t height, int64_t width,
                                   const mxq_qtensor* w_groups, int32_t n_groups,
                                   const int32_t* w_perm, const void* bias, void* out,
@@ -419,7 +535,8 @@ mxq_status mxq_conv3x3_gemm_mixed(const mxq_qtensor* x, int64_t height, int64_t 
   mxq_status st = check_qtensor(x);
   if (st != MXQ_OK) return st;
   if (height <= 0 || width <= 0 || n_out < 0) return MXQ_ERR_INVALID_ARG;
-  if (x->fmt == MXQ_FMT_INT4 || x->fmt == MXQ_FMT_BF16) return MXQ_ERR_UNSUPPORTED;
+  if (x->fmt == MXQ_FMT_INT4 || x->fmt == MXQ_FMT_BF16 || x->fmt == MXQ_FMT_INT8)
+    return MXQ_ERR_UNSUPPORTED;
   if (workspace && !aligned(workspace, 16)) return MXQ_ERR_ALIGNMENT;
   if (height > INT32_MAX / width) return MXQ_ERR_SHAPE;
   const int64_t C = x->cols, hw = height * width;
@@ -432,7 +549,8 @@ mxq_status mxq_conv3x3_gemm_mixed(const mxq_qtensor* x, int64_t height, int64_t 
     const mxq_qtensor* w = &w_groups[g];
     st = check_qtensor(w);
     if (st != MXQ_OK) return st;
-    if (w->fmt == MXQ_FMT_MXFP8 || w->fmt == MXQ_FMT_BF16) return MXQ_ERR_UNSUPPORTED;
+    if (w->fmt == MXQ_FMT_MXFP8 || w->fmt == MXQ_FMT_BF16 || w->fmt == MXQ_FMT_INT8)
+      return MXQ_ERR_UNSUPPORTED;
     // the scaled-MFMA route (MXFP4 x MXFP4) reads no implicit im2col
     if (x->fmt == MXQ_FMT_MXFP4 && w->fmt == MXQ_FMT_MXFP4 && w->rows > 0)
       return MXQ_ERR_UNSUPPORTED;

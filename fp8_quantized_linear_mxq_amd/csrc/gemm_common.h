@@ -3,6 +3,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "kernels.h"
 
 namespace mxq {
 
@@ -34,7 +35,26 @@ struct GemmP {
   // x + kx - 1), zero outside the image.  cv_c is a multiple of the K-tile,
   // so a K-tile never spans two taps.
   int cv_h, cv_w, cv_c;
+  // Rows grouped by expert (kernels with a GRP form): offsets of the groups'
+  // rows [groups + 1], W holds groups * N rows, bias groups * N entries.
+  const int32_t* goff;
+  int groups;
 };
+
+inline GemmP gemm_params(const GemmArgs& a) {
+  GemmP p;
+  p.a = a.a_codes; p.lda = a.lda; p.as = a.a_scales; p.ldas = a.ld_as;
+  p.w = a.w_codes; p.ldw = a.ldw; p.ws = a.w_scales; p.ldws = a.ld_ws;
+  p.M = (int)a.M; p.N = (int)a.N; p.K = (int)a.K;
+  p.tiles_m = p.tiles_n = 0;
+  p.col_map = a.col_map;
+  p.u = a.u; p.ld_u = a.ld_u; p.l2t = a.l2t; p.rank = a.rank;
+  p.bias = a.bias;
+  p.out = a.out; p.ld_out = a.ld_out; p.n_out = (int)a.n_out;
+  p.cv_h = (int)a.cv_h; p.cv_w = (int)a.cv_w; p.cv_c = (int)a.cv_c;
+  p.goff = a.goff; p.groups = (int)a.groups;
+  return p;
+}
 
 // K-tiles per tap (cv_c / bk) and ceil(2**32 / tiles): floor(kt / tiles) is
 // then one multiply, exact while kt * tiles < 2**32, which holds for every

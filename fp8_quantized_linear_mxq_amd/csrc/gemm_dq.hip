@@ -586,16 +586,9 @@ int64_t gemm_dq_workspace(int64_t M, int64_t N) {
 hipError_t launch_gemm_dq(const GemmArgs& a, hipStream_t s) {
   DqParams dp;
   GemmP& p = dp.g;
-  p.a = a.a_codes; p.lda = a.lda; p.as = a.a_scales; p.ldas = a.ld_as;
-  p.w = a.w_codes; p.ldw = a.ldw; p.ws = a.w_scales; p.ldws = a.ld_ws;
-  p.M = (int)a.M; p.N = (int)a.N; p.K = (int)a.K;
+  p = gemm_params(a);
   p.tiles_m = (int)((a.M + BM - 1) / BM);
   p.tiles_n = (int)((a.N + BN - 1) / BN);
-  p.col_map = a.col_map;
-  p.u = a.u; p.ld_u = a.ld_u; p.l2t = a.l2t; p.rank = a.rank;
-  p.bias = a.bias;
-  p.out = a.out; p.ld_out = a.ld_out; p.n_out = (int)a.n_out;
-  p.cv_h = (int)a.cv_h; p.cv_w = (int)a.cv_w; p.cv_c = (int)a.cv_c;
   dp.a_gp = a.a_g;
   dp.w_gp = a.w_g;
   dp.part = nullptr;

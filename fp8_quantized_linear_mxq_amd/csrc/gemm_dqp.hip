@@ -40,7 +40,10 @@
 #include "device_common.h"
 #include "gemm_common.h"
 #include "gemm_pipe.h"
+#include "grouped.h"
 #include "kernels.h"
+
+#include <type_traits>
 
 namespace mxq {
 namespace {
@@ -157,9 +160,10 @@ __device__ __forceinline__ uint4 dq(const uint32_t* raw, int ks, const Scales<K,
   }
 }
 
-template <int AK, int WK, int TM, int TN, int WGM, bool SLAB, bool LR, bool CONV, int WGN>
+template <int AK, int WK, int TM, int TN, int WGM, bool SLAB, bool LR, bool CONV, int WGN, bool GRP = false>
 __device__ __forceinline__ void dqp_body(const DqpParams& dp) {
-  const GemmP& p = dp.g;
+  // a grouped product narrows its own copy to the tile's group
+  std::conditional_t<GRP, GemmP, const GemmP&> p = dp.g;
   constexpr bool FP16 = (AK == K_NV && WK == K_NV);
   constexpr int NW = WGM * WGN;   // waves: WGM (rows) x WGN (columns)
   constexpr int TBM = 32 * TM * WGM, TBN = 32 * TN * WGN;
@@ -180,9 +184,18 @@ __device__ __forceinline__ void dqp_body(const DqpParams& dp) {
   __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t st2[STAGE];
 
-  int tm, tn;
-  tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, dp.gm, tm, tn);
-  const int m0 = tm * TBM, n0 = tn * TBN;
+  int tm, tn, m0;
+  if constexpr (GRP) {
+    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TBM);
+    if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
+    tile_coords(blockIdx.x, tiles_m, p.tiles_n, dp.gm, tm, tn);
+    m0 = enter_group(p, TBM, tm);
+    if (m0 < 0) return;
+  } else {
+    tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, dp.gm, tm, tn);
+    m0 = tm * TBM;
+  }
+  const int n0 = tn * TBN;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WGN, wn = wave % WGN;
   const int l32 = lane & 31, half = lane >> 5;
@@ -448,6 +461,12 @@ __global__ __launch_bounds__(64 * WGM * WGN, (SLAB && AK != K_BF) ? 2 : 1) void 
   dqp_body<AK, WK, TM, TN, WGM, SLAB, LR, false, WGN>(dp);
 }
 
+// The same GEMM with the rows grouped by expert (no low-rank branch).
+template <int AK, int WK, int TM, int TN, int WGM, bool SLAB, int WGN>
+__global__ __launch_bounds__(64 * WGM * WGN, 1) void grouped_dqp_kernel(DqpParams dp) {
+  dqp_body<AK, WK, TM, TN, WGM, SLAB, false, false, WGN, true>(dp);
+}
+
 // The same GEMM with the activation operand read as the implicit im2col of a
 // 3x3 convolution (128x128 tiles, two workgroups per compute unit).
 template <int AK, int WK, bool SLAB>
@@ -483,6 +502,19 @@ template <int AK, int WK>
 hipError_t launch_256(bool lr, const DqpParams& dp, hipStream_t s) {
   if constexpr (tall_waves<AK, WK>()) return launch_cfg<AK, WK, 4, 2, false, 2, 4>(lr, dp, s);
   else return launch_cfg<AK, WK, 2, 4, false, 4>(lr, dp, s);
+}
+
+template <int AK, int WK, int TM, int TN, bool SLAB, int WGM, int WGN>
+hipError_t launch_grouped(DqpParams dp, hipStream_t s) {
+  constexpr int TBM = 32 * TM * WGM, TBN = 32 * TN * WGN;
+  dp.g.tiles_m = (int)group_tiles_bound(dp.g.M, dp.g.groups, TBM);
+  dp.g.tiles_n = (dp.g.N + TBN - 1) / TBN;
+  const int64_t tiles = (int64_t)dp.g.tiles_m * dp.g.tiles_n;
+  if (tiles > INT32_MAX) return hipErrorInvalidValue;
+  dp.gm = 1;
+  while (dp.gm * 2 <= dp.g.tiles_m && (int64_t)dp.gm * 2 * dp.gm * 2 <= (tiles + 7) / 8) dp.gm *= 2;
+  grouped_dqp_kernel<AK, WK, TM, TN, WGM, SLAB, WGN><<<(unsigned)tiles, 64 * WGM * WGN, 0, s>>>(dp);
+  return hipGetLastError();
 }
 
 template <int AK, int WK>
@@ -559,20 +591,17 @@ hipError_t launch_w(int w_fmt, bool lr, const DqpParams& dp, hipStream_t s) {
 
 hipError_t launch_gemm_dqp(const GemmArgs& a, hipStream_t s) {
   DqpParams dp;
-  GemmP& p = dp.g;
-  p.a = a.a_codes; p.lda = a.lda; p.as = a.a_scales; p.ldas = a.ld_as;
-  p.w = a.w_codes; p.ldw = a.ldw; p.ws = a.w_scales; p.ldws = a.ld_ws;
-  p.M = (int)a.M; p.N = (int)a.N; p.K = (int)a.K;
-  p.tiles_m = p.tiles_n = 0;
-  p.col_map = a.col_map;
-  p.u = a.u; p.ld_u = a.ld_u; p.l2t = a.l2t; p.rank = a.rank;
-  p.bias = a.bias;
-  p.out = a.out; p.ld_out = a.ld_out; p.n_out = (int)a.n_out;
-  p.cv_h = (int)a.cv_h; p.cv_w = (int)a.cv_w; p.cv_c = (int)a.cv_c;
+  dp.g = gemm_params(a);
   dp.a_gp = a.a_g;
   dp.w_gp = a.w_g;
   const bool lr = a.rank > 0;
   if (a.w_fmt != FMT_NVFP4 && a.w_fmt != FMT_MXFP4) return hipErrorInvalidValue;
+  if (a.goff) {
+    // the plain GEMM's tiles for this pair: 64x128, slabbed 128x128 past 32 K-tiles
+    if (a.a_fmt != FMT_BF16 || a.w_fmt != FMT_MXFP4) return hipErrorInvalidValue;
+    if (a.K / BK > 32) return launch_grouped<K_BF, K_MX4, 2, 2, true, 2, 2>(dp, s);
+    return launch_grouped<K_BF, K_MX4, 2, 1, false, 1, 4>(dp, s);
+  }
   switch (a.a_fmt) {
     case FMT_NVFP4: return launch_w<K_NV>(a.w_fmt, lr, dp, s);
     case FMT_MXFP8: return launch_w<K_MX8>(a.w_fmt, lr, dp, s);

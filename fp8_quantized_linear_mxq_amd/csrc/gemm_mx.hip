@@ -40,6 +40,7 @@
 #include "device_common.h"
 #include "gemm_common.h"
 #include "gemm_pipe.h"
+#include "grouped.h"
 #include "kernels.h"
 
 namespace mxq {
@@ -52,60 +53,7 @@ constexpr int KS = BK / 64;       // MFMA K-steps per K-tile
 constexpr int SB = BK / 32;       // scale bytes per row per K-tile
 constexpr int kSlab = 8;          // K-tiles per fp32 slab when slabbing
 
-// Whole-tile staged epilogue (no column map; 16-byte aligned output rows):
-// each wave writes its accumulators (+ bias, bf16) into the LDS image of the
-// workgroup tile -- rows [0, TBM/2) in `lo`, the rest in `hi` -- then every
-// thread stores 16-byte pieces of whole tile rows with non-temporal stores.
-// Accumulator layout (D^T = W A^T): lane l of MFMA tile (i, j) holds row
-// i*32 + l%32 and columns j*32 + 8g + 4(l/32) + [0, 4) at acc[i][j][4g..4g+3].
-template <int TM, int TN, int WGM, int STAGE>
-__device__ __forceinline__ void epilogue_wg(const GemmP& p, v16f (&acc)[TM][TN], int m0, int n0,
-                                            int wm, int wn, int lane, uint8_t* lo, uint8_t* hi) {
-  constexpr int TBM = 32 * TM * WGM, TBN = 64 * TN, NT = 128 * WGM;
-  constexpr int WRS = TBN * 2 + 16, CPR = TBN / 8;   // row stride; 16-byte pieces per row
-  const int l32 = lane & 31, half = lane >> 5;
-  const int n_lim = p.N < p.n_out ? p.N : p.n_out;
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = wm * 32 * TM + i * 32 + l32;
-    uint8_t* row = (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS);
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int c = wn * 32 * TN + j * 32 + 8 * g + 4 * half;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int nn = n0 + c + e;
-          v[e] = acc[i][j][4 * g + e] + ((p.bias && nn < n_lim) ? bf16_bits_to_f32(p.bias[nn]) : 0.f);
-        }
-        uint2 pk;
-        pk.x = pack_bf16_rne(v[0], v[1]);
-        pk.y = pack_bf16_rne(v[2], v[3]);
-        *reinterpret_cast<uint2*>(row + c * 2) = pk;
-      }
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < TBM * CPR; idx += NT) {
-    const int r = idx / CPR, ch = idx % CPR;
-    const uint8_t* src = (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS) + ch * 16;
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
-    const int row = m0 + r, n = n0 + ch * 8;
-    if (row >= p.M) continue;
-    uint16_t* o = p.out + (int64_t)row * p.ld_out + n;
-    if (n + 8 <= n_lim) {
-      __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(o));
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n + e < n_lim) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
-  }
-}
-
-template <int TM, int TN, int WGM, bool SLAB, bool LR, bool VSC>
+template <int TM, int TN, int WGM, bool SLAB, bool LR, bool VSC, bool GRP = false>
 __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) {
   constexpr int NW = 2 * WGM;                      // waves: WGM (rows) x 2 (columns)
   constexpr int TBM = 32 * TM * WGM, TBN = 64 * TN;
@@ -124,9 +72,18 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
   __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t scl[2 * SGRP + 1024];   // + spare-load pad
 
-  int tm, tn;
-  tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, gm, tm, tn);
-  const int m0 = tm * TBM, n0 = tn * TBN;
+  int tm, tn, m0;
+  if constexpr (GRP) {   // rows grouped by expert: the tile's group, then as one product
+    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TBM);
+    if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
+    tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
+    m0 = enter_group(p, TBM, tm);
+    if (m0 < 0) return;
+  } else {
+    tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, gm, tm, tn);
+    m0 = tm * TBM;
+  }
+  const int n0 = tn * TBN;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
   const int l32 = lane & 31, half = lane >> 5;
@@ -361,7 +318,8 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
 
 template <int TM, int TN, int WGM, bool SLAB>
 hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
-  p.tiles_m = (p.M + 32 * TM * WGM - 1) / (32 * TM * WGM);
+  p.tiles_m = p.goff ? (int)group_tiles_bound(p.M, p.groups, 32 * TM * WGM)
+                     : (p.M + 32 * TM * WGM - 1) / (32 * TM * WGM);
   p.tiles_n = (p.N + 64 * TN - 1) / (64 * TN);
   const int tiles = p.tiles_m * p.tiles_n;
   // tile-rows per group: one XCD's share (tiles / 8) as a near-square block
@@ -373,6 +331,11 @@ hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
                    reinterpret_cast<uintptr_t>(p.as) % 16 == 0 &&
                    reinterpret_cast<uintptr_t>(p.ws) % 16 == 0 && p.K % (2 * BK) == 0;
   const dim3 grid(tiles);
+  if (p.goff) {
+    if (vsc) gemm_mx_kernel<TM, TN, WGM, SLAB, false, true, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
+    else gemm_mx_kernel<TM, TN, WGM, SLAB, false, false, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
+    return hipGetLastError();
+  }
   if (lr && vsc) gemm_mx_kernel<TM, TN, WGM, SLAB, true, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
   else if (lr) gemm_mx_kernel<TM, TN, WGM, SLAB, true, false><<<grid, 128 * WGM, 0, s>>>(p, gm);
   else if (vsc) gemm_mx_kernel<TM, TN, WGM, SLAB, false, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
@@ -383,17 +346,14 @@ hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_gemm_mx(const GemmArgs& a, hipStream_t s) {
-  GemmP p;
-  p.a = a.a_codes; p.lda = a.lda; p.as = a.a_scales; p.ldas = a.ld_as;
-  p.w = a.w_codes; p.ldw = a.ldw; p.ws = a.w_scales; p.ldws = a.ld_ws;
-  p.M = (int)a.M; p.N = (int)a.N; p.K = (int)a.K;
-  p.col_map = a.col_map;
-  p.u = a.u; p.ld_u = a.ld_u; p.l2t = a.l2t; p.rank = a.rank;
-  p.bias = a.bias;
-  p.out = a.out; p.ld_out = a.ld_out; p.n_out = (int)a.n_out;
-  p.cv_h = (int)a.cv_h; p.cv_w = (int)a.cv_w; p.cv_c = (int)a.cv_c;
+  const GemmP p = gemm_params(a);
   const bool lr = a.rank > 0;
   if (a.K > 4096) return launch_cfg<2, 2, 2, true>(lr, p, s);
+  if (a.goff) {
+    // 256-row tiles once the groups fill most of one on average
+    if (a.M >= 192 * a.groups) return launch_cfg<2, 4, 4, false>(lr, p, s);
+    return launch_cfg<2, 2, 2, false>(lr, p, s);
+  }
   // Large tiles move the fewest bytes per MFMA; pick the one whose tile count
   // fills the 256 compute units in the fewest rounds, per unit of tile work.
   const int64_t cu = 256;

@@ -343,4 +343,57 @@ __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN],
   }
 }
 
+// Whole-tile staged epilogue (no column map; 16-byte aligned output rows):
+// each wave writes its accumulators (+ bias, bf16) into the LDS image of the
+// workgroup tile -- rows [0, TBM/2) in `lo`, the rest in `hi` -- then every
+// thread stores 16-byte pieces of whole tile rows with non-temporal stores.
+// Accumulator layout (D^T = W A^T): lane l of MFMA tile (i, j) holds row
+// i*32 + l%32 and columns j*32 + 8g + 4(l/32) + [0, 4) at acc[i][j][4g..4g+3].
+template <int TM, int TN, int WGM, int STAGE>
+__device__ __forceinline__ void epilogue_wg(const GemmP& p, v16f (&acc)[TM][TN], int m0, int n0,
+                                            int wm, int wn, int lane, uint8_t* lo, uint8_t* hi) {
+  constexpr int TBM = 32 * TM * WGM, TBN = 64 * TN, NT = 128 * WGM;
+  constexpr int WRS = TBN * 2 + 16, CPR = TBN / 8;   // row stride; 16-byte pieces per row
+  const int l32 = lane & 31, half = lane >> 5;
+  const int n_lim = p.N < p.n_out ? p.N : p.n_out;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int r = wm * 32 * TM + i * 32 + l32;
+    uint8_t* row = (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = wn * 32 * TN + j * 32 + 8 * g + 4 * half;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int nn = n0 + c + e;
+          v[e] = acc[i][j][4 * g + e] + ((p.bias && nn < n_lim) ? bf16_bits_to_f32(p.bias[nn]) : 0.f);
+        }
+        uint2 pk;
+        pk.x = pack_bf16_rne(v[0], v[1]);
+        pk.y = pack_bf16_rne(v[2], v[3]);
+        *reinterpret_cast<uint2*>(row + c * 2) = pk;
+      }
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < TBM * CPR; idx += NT) {
+    const int r = idx / CPR, ch = idx % CPR;
+    const uint8_t* src = (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS) + ch * 16;
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    const int row = m0 + r, n = n0 + ch * 8;
+    if (row >= p.M) continue;
+    uint16_t* o = p.out + (int64_t)row * p.ld_out + n;
+    if (n + 8 <= n_lim) {
+      __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(o));
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < n_lim) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
 }  // namespace mxq

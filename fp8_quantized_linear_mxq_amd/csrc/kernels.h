@@ -42,6 +42,9 @@ struct QuantizeArgs {
   bool nv_two_pass;                 // dynamic NVFP4: skip the one-pass kernel
 };
 
+// INT8 rows (one scale per row); scales of ld_scales bytes between rows.
+hipError_t launch_quantize_i8(const QuantizeArgs& a, hipStream_t s);
+
 constexpr int kAmaxPartials = 1024;  // NVFP4 phase-1 grid (workspace floats)
 
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
@@ -75,7 +78,16 @@ struct GemmArgs {
   // implicit im2col of a 3x3 convolution (0 = plain GEMM): A is the input's
   // [images * cv_h * cv_w][cv_c] pixel rows and K = 9 * cv_c
   int64_t cv_h, cv_w, cv_c;
+  // rows grouped by expert (null = plain GEMM): offsets [groups + 1] on the
+  // device; N = output columns per group, W and bias hold groups * N rows
+  const int32_t* goff;
+  int64_t groups;
 };
+hipError_t launch_gemm_i8(const GemmArgs& a, hipStream_t s);
+// Products with few rows (or few per group): INT8 x INT8, MXFP4 x MXFP4 and
+// bf16 x MXFP4; see few_rows().
+bool few_rows(const GemmArgs& a);
+hipError_t launch_gemm_few(const GemmArgs& a, hipStream_t s);
 hipError_t launch_gemm_mx(const GemmArgs& a, hipStream_t s);
 // INT4-row route: K splits for an M x N x K problem (1 = none) and the
 // workspace bytes that cover the splits of any K.
@@ -83,6 +95,21 @@ int dq_splits(int64_t M, int64_t N, int64_t K);
 int64_t gemm_dq_workspace(int64_t M, int64_t N);
 hipError_t launch_gemm_dq(const GemmArgs& a, hipStream_t s);
 hipError_t launch_gemm_dqp(const GemmArgs& a, hipStream_t s);
+
+// Per-head RMS norm of queries and keys with the position rotation.
+struct QkNormArgs {
+  const void* x; int dtype;
+  int64_t tokens, ldx;
+  int n_q, n_k, head_dim;
+  const void* wq; const void* wk;          // [head_dim] of dtype, may be null
+  float eps;
+  const float* cos; const float* sin;      // [n_pos][rot_dim / 2]
+  int64_t n_pos; int rot_dim; bool interleaved;
+  const int32_t* pos;                      // [tokens], null = token index
+  void* q; int64_t q_token, q_head;        // element strides
+  void* k; int64_t k_token, k_head;
+};
+hipError_t launch_qk_norm_rope(const QkNormArgs& a, hipStream_t s);
 
 struct SelectArgs {
   const void* w; int dtype;

@@ -31,18 +31,22 @@
  *   MXFP8  E4M3 elements, one E8M0 scale per 32
  *   NVFP4  E2M1 elements, one E4M3 scale per 16, one fp32 tensor scale g
  *   INT4   symmetric two's-complement int4, one fp32 scale per 32 (weights)
+ *   INT8   symmetric two's-complement int8, one fp32 scale per row (activations
+ *          and weights of the 8-bit layer)
  * Rounding: nearest, ties to even, saturating at the largest finite value,
  * decided on the exact real quotient.  Scale rules:
  *   MX     e = clamp(floor(log2 amax) - emax_elem, -127, 127), code e + 127,
  *          emax_elem = 2 (E2M1) or 8 (E4M3); amax = 0 gives code 0.
  *   NVFP4  g = RN_fp32(A / 2688), A = tensor amax; s = RN_E4M3(amax / (6 g)).
  *   INT4   s = RN_fp32(amax / 7); q = clamp(RNE(x / s), -7, 7).
+ *   INT8   s = RN_fp32(row amax / 127); q = clamp(RNE(x / s), -127, 127);
+ *          s = 0 gives q = 0.
  *
  * Storage (all device memory, row-major, K contiguous):
  *   codes   4-bit formats: [rows][K/2] bytes, element 2i in the low nibble
- *           of byte i; MXFP8: [rows][K] bytes.
+ *           of byte i; MXFP8, INT8: [rows][K] bytes.
  *   scales  MX: [rows][K/32] E8M0 bytes; NVFP4: [rows][K/16] E4M3 bytes;
- *           INT4: [rows][K/32] fp32.
+ *           INT4: [rows][K/32] fp32; INT8: [rows][1] fp32.
  *   tensor_scale  NVFP4 only: one fp32 in device memory.
  * Weights, like nn.Linear, are stored [out][in] with the reduction index
  * contiguous: W [N][K], the low-rank factors as L1^T [r][K] and L2^T [N][r].
@@ -110,7 +114,10 @@ typedef enum mxq_format {
    * Only as mxq_gemm / mxq_gemm_mixed's `a`: codes holds the bf16 values
    * [rows][ld_codes bytes] (16-byte aligned, ld_codes a multiple of 16),
    * scales and tensor_scale are unused.  Not a quantize target. */
-  MXQ_FMT_BF16 = 5
+  MXQ_FMT_BF16 = 5,
+  /* Row-wise int8: two's-complement codes in [-127, 127], one fp32 scale per
+   * row (an activation token, or a weight's output channel). */
+  MXQ_FMT_INT8 = 6
 } mxq_format;
 
 typedef enum mxq_dtype { MXQ_DT_F32 = 1, MXQ_DT_BF16 = 2 } mxq_dtype;
@@ -129,7 +136,8 @@ typedef struct mxq_qtensor {
 } mxq_qtensor;
 
 /*
- * mxq_quantize -- rotate (optional) and block-quantize a [rows, cols] tensor.
+ * mxq_quantize -- rotate (optional) and block-quantize a [rows, cols] tensor
+ * (MXQ_FMT_INT8: row-quantize it).
  *
  * Computes the scale and element rules above (Microscaling FP4 summary, the
  * two reasons FP4 fails) on r = x, or on r = x H_bd when hadamard_n > 0
@@ -196,7 +204,7 @@ mxq_status mxq_pack_l1t(const void* l1t, int32_t rank, int64_t cols, void* l1p, 
  * unpacked L1^T); the projection's factor reads are whole contiguous
  * kilobytes.  It takes the fused quantize + projection path only: lr_rank a
  * multiple of 16 in [16, 128] (0 is MXQ_ERR_INVALID_ARG), bf16 x and
- * hadamard_n 0 (else MXQ_ERR_UNSUPPORTED), cols a multiple of 128 (else
+ * hadamard_n 0 (else MXQ_ERR_UNSUPPORTED; so is MXQ_FMT_INT8), cols a multiple of 128 (else
  * MXQ_ERR_SHAPE); like the other low-rank conditions these are checked for
  * non-empty inputs.  Other arguments, workspace and errors as mxq_quantize.
  */
@@ -234,8 +242,11 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  * low-rank branch added in the same output).
  *
  *  a           quantized activations [M, K]: MXFP4, MXFP8 or NVFP4; or
- *              unquantized bf16 activations (MXQ_FMT_BF16), taken exactly.
- *  w           quantized weights [N, K]: MXFP4, NVFP4 or INT4.  Every pair
+ *              unquantized bf16 activations (MXQ_FMT_BF16), taken exactly; or
+ *              INT8 (with INT8 weights only).
+ *  w           quantized weights [N, K]: MXFP4, NVFP4 or INT4; or INT8 with
+ *              INT8 activations (one scale per token and per output channel;
+ *              the integer sum is exact).  Every other pair
  *              is supported: MXFP4 x MXFP4 on the scaled MFMA; the others
  *              dequantize exactly to fp16 (NVFP4 x NVFP4) or bf16 operands;
  *              INT4 rows sum each 32-block and apply its fp32 scale.
@@ -269,7 +280,8 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  *              size; they may differ from the unsplit sum by fp32 rounding,
  *              within the same error bound).  Otherwise, and for every other
  *              route and with a low-rank branch, it is unused.
- * Requirements: a->cols == w->cols == K, K a multiple of 128.
+ * Requirements: a->cols == w->cols == K, K a multiple of 128; INT8: K a
+ * multiple of 32, 32 .. 2**17.
  * M or N of 0 is a no-op.  Accumulation is fp32; long K is summed in slabs.
  */
 mxq_status mxq_gemm(const mxq_qtensor* a, const mxq_qtensor* w, const int32_t* w_out_col,
@@ -292,6 +304,68 @@ mxq_status mxq_gemm_mixed(const mxq_qtensor* a, const mxq_qtensor* w_groups, int
                           const float* lr_u, int64_t ld_u, const void* lr_l2t, int32_t lr_rank,
                           const void* bias, void* out, int64_t ld_out, int64_t n_out,
                           void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * mxq_gemm_grouped -- the product of a layer of experts: rows of a sorted by
+ * expert, each group of rows multiplied by its own weights,
+ *   out[m] = RN_bf16(Q(a_m) Q(W_e)^T + bias_e)  for offsets[e] <= m < offsets[e+1].
+ *
+ *  a           activations [M, K]: INT8, MXFP4 or bf16 (MXQ_FMT_BF16).
+ *  w           weights [n_groups * N, K], expert e in rows [e N, (e + 1) N):
+ *              INT8 with INT8 activations, else MXFP4.  Other pairs are
+ *              MXQ_ERR_UNSUPPORTED.  The domain of bf16 x MXFP4 is mxq_gemm's.
+ *  n_groups    1 .. 65536; must divide w->rows (else MXQ_ERR_SHAPE).
+ *  offsets     device int32 [n_groups + 1], non-decreasing, in [0, M]; read on
+ *              the device, so a router on the GPU needs no host round trip.
+ *              Groups may be empty; rows outside [offsets[0],
+ *              offsets[n_groups]) are not written.  Values outside [0, M] are
+ *              clamped; offsets that decrease leave rows unspecified, without
+ *              access outside the operands.
+ *  bias        optional device bf16 [n_groups][N].
+ *  out         device bf16 [M][ld_out], N columns; 2-byte aligned.
+ * K as in mxq_gemm, not 0.  M = 0 or N = 0 is a no-op.  Error bound as in mxq_gemm.
+ * The kernel is chosen by M / n_groups (few rows per expert: one that streams
+ * the weights of the experts hit), never by what offsets holds.
+ */
+mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t n_groups,
+                            const int32_t* offsets, const void* bias, void* out, int64_t ld_out,
+                            void* stream);
+
+/*
+ * mxq_qk_norm_rope -- RMS norm of every query and key head with the position
+ * rotation, in one pass over the output of a fused projection:
+ *   v = x[t][h], n = v / sqrt(mean(v^2) + eps) * weight  (all in fp32)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)  for each pair of n's first
+ *   rot_dim elements; the rest pass; one rounding to dtype at the end.
+ * Pairs: (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved, i < rot_dim/2,
+ * with cos and sin [position][i].
+ *
+ *  x           device, dtype elements, token stride ldx (elements, a multiple
+ *              of 8): n_q_heads query heads, then n_k_heads key heads, of
+ *              head_dim elements each (what follows, values, is not read).
+ *  head_dim    a multiple of 8, at most 512.   rot_dim  a multiple of 8, 0 ..
+ *              head_dim (0: no rotation; cos, sin and positions are unused).
+ *  q_weight, k_weight  device [head_dim] of dtype, or NULL for ones.
+ *  eps         >= 0.
+ *  cos, sin    device fp32 [n_pos][rot_dim / 2].
+ *  positions   device int32 [tokens], or NULL: token t is at position t (then
+ *              n_pos >= tokens).  A token whose position lies outside
+ *              [0, n_pos) is skipped: its outputs are not written.
+ *  q_out, k_out  device, dtype; element strides between tokens and heads
+ *              (multiples of 8; head elements contiguous), so a caller can
+ *              have [token][head] or [head][token] order.  They may be x
+ *              itself with x's strides; any other overlap is unspecified.
+ * x, the weights, the tables and the outputs are 16-byte aligned.
+ * tokens = 0 or no heads is a no-op.
+ */
+mxq_status mxq_qk_norm_rope(const void* x, int32_t dtype, int64_t tokens, int64_t ldx,
+                            int32_t n_q_heads, int32_t n_k_heads, int32_t head_dim,
+                            const void* q_weight, const void* k_weight, float eps,
+                            const float* cos, const float* sin, int64_t n_pos, int32_t rot_dim,
+                            int32_t interleaved, const int32_t* positions,
+                            void* q_out, int64_t q_token_stride, int64_t q_head_stride,
+                            void* k_out, int64_t k_token_stride, int64_t k_head_stride,
+                            void* stream);
 
 /*
  * mxq_conv3x3_gemm_mixed -- a 3x3, stride-1, zero-padding-1 convolution as the

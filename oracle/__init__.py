@@ -31,6 +31,8 @@ Module map:
   quantize  MXFP4, MXFP8, NVFP4, INT4 block quantizers and their dequantizers
   hadamard  Sylvester block-diagonal Hadamard rotation
   gemm      dequantized fp64 linear layer (+ low-rank branch) and its tolerance
+  int8      row-wise int8 quantizer
+  heads     per-head RMS norm with the position rotation
   select    per-output-channel format choice by minimum reconstruction error
   mse_scales  least-squared-error block (and NVFP4 tensor) scales for weights
   lowrank   offline SVDQuant split W ~= (L1 L2)^T + R (truncated SVD)
