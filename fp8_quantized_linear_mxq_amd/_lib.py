@@ -113,13 +113,16 @@ def _check(fn: str, status: int):
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()   # ctypes takes the integer
 
 
 def _stream(stream):
+    """The given stream's handle, or the current device's current stream (read
+    as a handle: building the Stream object takes 3 us of a small call's 12)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def storage(fmt: int, cols: int):
@@ -152,24 +155,26 @@ class QTensor:
     tensor_scale: "object" = None
 
     def c(self) -> QTensorC:
+        codes, scales, ts = self.codes, self.scales, self.tensor_scale
         return QTensorC(self.fmt, 0, self.rows, self.cols,
-                        self.codes.data_ptr() if self.codes is not None else None,
-                        self.codes.stride(0) * self.codes.element_size() if self.codes is not None else 0,
-                        self.scales.data_ptr() if self.scales is not None else None,
-                        self.scales.stride(0) * self.scales.element_size() if self.scales is not None else 0,
-                        self.tensor_scale.data_ptr() if self.tensor_scale is not None else None)
+                        codes.data_ptr() if codes is not None else None,
+                        codes.stride(0) * codes.element_size() if codes is not None else 0,
+                        scales.data_ptr() if scales is not None else None,
+                        scales.stride(0) * scales.element_size() if scales is not None else 0,
+                        ts.data_ptr() if ts is not None else None)
 
 
 def empty_qtensor(fmt: int, rows: int, cols: int, device="cuda") -> QTensor:
     """Allocates (torch) the buffers of a quantized operand."""
     import torch
+    if fmt == INT8 and cols % 32 == 0:
+        return QTensor(fmt, rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                       torch.empty((rows, 1), dtype=torch.float32, device=device))
     cb, sb = storage(fmt, cols)
     # row strides padded to the ABI's alignment (16 B codes; 4 B scales, 16 B
     # for INT4's fp32 scales)
     codes = torch.empty((rows, (cb + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    if fmt == INT8:
-        scales = torch.empty((rows, 1), dtype=torch.float32, device=device)
-    elif fmt == INT4:
+    if fmt == INT4:
         scales = torch.empty((rows, (sb // 4 + 3) // 4 * 4), dtype=torch.float32, device=device)
     else:
         scales = torch.empty((rows, (sb + 3) // 4 * 4), dtype=torch.uint8, device=device)
@@ -221,21 +226,21 @@ def quantize(x, fmt: int, hadamard: int = 0, static_tensor_scale=None, l1t=None,
     if out is None:
         out = empty_qtensor(fmt, rows, cols, x.device)
     if workspace is None:
-        n = workspace_size(OP_QUANTIZE, rows, cols, fmt)
-        workspace = torch.empty((max(n, 16),), dtype=torch.uint8, device=x.device)
+        n = workspace_size(OP_QUANTIZE, rows, cols, fmt) if fmt != INT8 else 0
+        if n > 0:
+            workspace = torch.empty((n,), dtype=torch.uint8, device=x.device)
+    wsp, wsn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
     qc = out.c()
     if l1p is not None:
         st = lib.mxq_quantize_lrp(_ptr(x), dt, rows, cols, x.stride(0), hadamard,
                                   _ptr(static_tensor_scale), _ptr(l1p), l1p.shape[0], _ptr(u),
-                                  0 if u is None else u.stride(0), C.byref(qc), _ptr(workspace),
-                                  workspace.numel(), _stream(stream))
+                                  0 if u is None else u.stride(0), C.byref(qc), wsp, wsn, _stream(stream))
         _check("mxq_quantize_lrp", st)
         return out
     rank = 0 if l1t is None else l1t.shape[0]
     st = lib.mxq_quantize(_ptr(x), dt, rows, cols, x.stride(0), hadamard,
                           _ptr(static_tensor_scale), _ptr(l1t), rank, _ptr(u),
-                          0 if u is None else u.stride(0), C.byref(qc), _ptr(workspace),
-                          workspace.numel(), _stream(stream))
+                          0 if u is None else u.stride(0), C.byref(qc), wsp, wsn, _stream(stream))
     _check("mxq_quantize", st)
     return out
 
@@ -247,6 +252,9 @@ def _gemm_workspace(a: QTensor, ws: list, workspace):
     if workspace is False:
         return None, 0
     if workspace is None:
+        # only INT4 weights can use one
+        if all(w.fmt != INT4 for w in ws):
+            return None, 0
         n = max([workspace_size(OP_GEMM, a.rows, w.rows, w.fmt) for w in ws] + [0])
         if n <= 0:
             return None, 0
