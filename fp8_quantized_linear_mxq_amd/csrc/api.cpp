@@ -64,7 +64,7 @@ mxq_status check_qtensor(const mxq_qtensor* t) {
   return MXQ_OK;
 }
 
-constexpr int64_t kMaxKInt8 = 1 << 17;
+constexpr int64_t kMaxKInt8 = 1 << 17, kMaxLdInt8 = 1 << 24;
 constexpr int32_t kMaxGroups = 1 << 16;
 
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -321,6 +321,7 @@ static mxq_status gemm_checks(const mxq_qtensor* a, const mxq_qtensor* w, const 
   if (a->rows == 0 || w->rows == 0 || n_out == 0) return MXQ_OK;
   // int8 sums stay within int32 up to K = 2**17
   if (i8 ? a->cols == 0 || a->cols > kMaxKInt8 : a->cols % 128 != 0) return MXQ_ERR_SHAPE;
+  if (i8 && (a->ld_codes > kMaxLdInt8 || w->ld_codes > kMaxLdInt8)) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX || w->rows > INT32_MAX || a->cols > INT32_MAX || n_out > INT32_MAX)
     return MXQ_ERR_SHAPE;
   if (!out || ld_out < n_out) return MXQ_ERR_INVALID_ARG;
@@ -453,6 +454,7 @@ mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t 
   const int64_t n = w->rows / n_groups;
   if (a->rows == 0 || n == 0) return MXQ_OK;
   if (a->cols == 0 || (i8 ? a->cols > kMaxKInt8 : a->cols % 128 != 0)) return MXQ_ERR_SHAPE;
+  if (i8 && (a->ld_codes > kMaxLdInt8 || w->ld_codes > kMaxLdInt8)) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX / 2 || w->rows > INT32_MAX || a->cols > INT32_MAX) return MXQ_ERR_SHAPE;
   if (!offsets || !out || ld_out < n) return MXQ_ERR_INVALID_ARG;
   if (!aligned(offsets, 4) || !aligned(out, 2)) return MXQ_ERR_ALIGNMENT;

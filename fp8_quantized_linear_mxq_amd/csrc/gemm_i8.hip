@@ -8,22 +8,28 @@
 // by the two scales in turn, (acc * sa) * sw: the product of the scales alone
 // could underflow where the result does not.
 //
-// Organisation (the pipeline of the MXFP4 kernel without its block scales):
-//  * workgroup tile (32*TM*WGM) x (64*TN), waves in a WGM x 2 grid, each wave
-//    (32*TM) x (32*TN); K-tile 128, so every row of a tile contributes one
-//    whole 128-byte line per K-tile;
-//  * code tiles stream into a 2-stage LDS ring with direct global->LDS loads
-//    one K-tile ahead of the MFMAs, landing in the XOR-swizzled slots the
-//    fragment reads expect;
-//  * lane l of a 32x32x32 step supplies row l % 32 and the 16 codes K =
-//    16 * (l / 32) + [0, 16);
-//  * the MFMAs compute D^T = W A^T, so each lane holds four consecutive output
-//    columns of one row, and the output leaves through LDS as whole rows.
+// Organisation: workgroup tiles of 64 T x 64 T for T = 1, 2 or 4, four waves of
+// 32 T x 32 T each; K-tile 128, so every row of a tile contributes one whole
+// 128-byte line per K-tile.  Code tiles stream into LDS with direct
+// global->LDS loads, landing in XOR-swizzled slots; lane l of a 32x32x32 step
+// supplies row l % 32 and the 16 codes K = 16 * (l / 32) + [0, 16) of it; the
+// MFMAs compute D^T = W A^T, so a lane holds four consecutive output columns of
+// one row, and the output leaves through LDS as whole rows.
+//
+// What bounds it: on random codes a stream of these MFMAs from registers
+// reaches 2.9 Pop/s with one wave per SIMD (3.4 with two; 4.5 and 4.8 on
+// zeros: the clock drops under the switching power).  8192^3 runs at 2.54
+// Pop/s (432 us), 1.51 us per K-tile and round of 256 tiles (2.84 Pop/s) plus
+// some 10 us a round to fill the pipeline and write the output.
 #include "device_common.h"
 #include "gemm_common.h"
 #include "gemm_pipe.h"
 #include "grouped.h"
 #include "kernels.h"
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 namespace mxq {
 namespace {
@@ -33,191 +39,328 @@ constexpr int RB = BK;
 constexpr int CH = RB / 16;       // 16-byte chunks per row
 constexpr int KS = BK / 32;       // MFMA K-steps per K-tile
 
-template <int TM, int TN, int WGM, bool LR, bool GRP>
-__global__ __launch_bounds__(128 * WGM, 1) void gemm_i8_kernel(GemmP p, int gm) {
-  constexpr int NW = 2 * WGM;                      // waves: WGM (rows) x 2 (columns)
-  constexpr int TBM = 32 * TM * WGM, TBN = 64 * TN, NTHR = 64 * NW;
-  constexpr int A_STAGE = TBM * RB, W_STAGE = TBN * RB, STAGE = A_STAGE + W_STAGE;
-  static_assert((TBM * CH / 64) % NW == 0 && (TBN * CH / 64) % NW == 0, "every wave the same loads");
-  // two separate stages: reads of one are visibly independent of the loads in
-  // flight into the other, so the compiler adds no wait for them
-  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
-  __shared__ __attribute__((aligned(16))) float scl[TBM + TBN];
+// The pipeline.  A T = 4 wave (128 x 128) reads 8 KB of fragments from LDS for
+// 16 MFMAs, a 64 x 128 one 6 KB for 8, which with the loads' own LDS writes
+// would keep the LDS as busy as the matrix cores; its accumulators take 256 of
+// the 512 registers that one wave per SIMD has.
+//
+// Two stages of whole K-tiles leave the loads one K-tile of MFMAs to arrive,
+// less than their latency plus 64 KB (T = 4) at the rate one compute unit
+// streams: 2.06 us per K-tile, against 1.51 now.  So the LDS is a ring of five
+// slots, each the A or the W half of a K-tile: K-tile t has A in slot 2t % 5
+// and W in slot (2t + 1) % 5, A is loaded two K-tiles ahead and W one.  Each
+// wave holds the fragments of one K-step in registers while it reads those of
+// the next, so by the last K-step of K-tile t every wave has read all of it:
+// one barrier there releases its slots and, with the loads of K-tile t+1 waited
+// for, opens the next K-tile, whose first fragments are read under the MFMAs
+// of the last K-step.  The slots are five arrays and the loop has five
+// K-tiles, so every read is visibly independent of the loads in flight and the
+// compiler adds no wait; the K-tiles left over follow it in line (leaving the
+// loop from its middle instead costs 80 spilled registers).
+template <int T, bool LR, bool GRP>
+__global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring_kernel(GemmP p, int gm) {
+  constexpr int TB = 64 * T, HB = 32 * T;   // workgroup and wave tile
+  constexpr int LD = TB * CH / 64 / 4;      // loads per wave per slot
+  constexpr int kSlot = TB * RB;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[kSlot], s1[kSlot], s2[kSlot], s3[kSlot], s4[kSlot];
+  uint8_t* const slots[5] = {s0, s1, s2, s3, s4};
 
   int tm, tn, m0;
   if constexpr (GRP) {
-    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TBM);
+    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TB);
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
-    m0 = enter_group(p, TBM, tm);
+    m0 = enter_group(p, TB, tm);
     if (m0 < 0) return;
   } else {
     tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, gm, tm, tn);
-    m0 = tm * TBM;
+    m0 = tm * TB;
   }
-  const int n0 = tn * TBN;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n0 = tn * TB;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int l32 = lane & 31, half = lane >> 5;
-  const int KT = (p.K + BK - 1) / BK;
-  const int last_ch = (p.K % BK) ? (p.K % BK) / 16 : CH;   // chunks of the last K-tile
+  const int KF = p.K / BK, rest = (p.K % BK) / 32;   // whole K-tiles, K-steps of a last one
+  const int KT = KF + (rest > 0);
 
-  // the tile's scales, on their way while the first K-tiles load
-  constexpr int NSC = (TBM + TBN + NTHR - 1) / NTHR;
-  float my_scale[NSC];
+  // Load t of a wave covers rows 8 (4t + wave) + lane / 8; the lane's chunk of
+  // its row is the same for every t.  Offsets from the tile's first row stay
+  // within 32 bits (row strides are at most 2**24, checked by the host); rows past the end re-read the last.
+  const int lr = 8 * wave + (lane >> 3);
+  const int lc = ((lane & 7) ^ swz<CH>(lr)) * 16;
+  uint32_t va[LD], vw[LD];
 #pragma unroll
-  for (int t = 0; t < NSC; ++t) {
-    const int i = t * NTHR + tid;
-    const int ra = min(m0 + i, p.M - 1), rw = max(min(n0 + i - TBM, p.N - 1), 0);
-    const uint8_t* pa = p.as + (int64_t)ra * p.ldas;
-    const uint8_t* pw = p.ws + (int64_t)rw * p.ldws;
-    my_scale[t] = *reinterpret_cast<const float*>(i < TBM ? pa : pw);
+  for (int t = 0; t < LD; ++t) {
+    va[t] = (uint32_t)(min(m0 + 32 * t + lr, p.M - 1) - m0) * (uint32_t)p.lda + lc;
+    vw[t] = (uint32_t)(min(n0 + 32 * t + lr, p.N - 1) - n0) * (uint32_t)p.ldw + lc;
   }
+  const uint8_t* const abase = p.a + (int64_t)m0 * p.lda;
+  const uint8_t* const wbase = p.w + (int64_t)n0 * p.ldw;
+  // Half a K-tile into a slot.  K-tiles past the end re-read the last one;
+  // chunks past the end of K re-read the row's first chunk of the K-tile (the
+  // K-steps that hold them are not multiplied).
+  auto issue = [&](const uint8_t* base, const uint32_t (&v)[LD], int kt, uint8_t* slot) __attribute__((always_inline)) {
+    kt = kt < KT ? kt : KT - 1;
+    const uint32_t back = kt == KF && lc >= rest * 32 ? lc : 0;
+    const uint8_t* b = base + (int64_t)kt * RB;
+#pragma unroll
+    for (int t = 0; t < LD; ++t)
+      __builtin_amdgcn_global_load_lds(b + (uint64_t)(v[t] - back),
+                                       (lds_void_t*)(slot + (4 * t + wave) * 1024), 16, 0, 0);
+  };
 
-  const uint8_t* zsrc = zero_src();
+  // the scales and bias this thread brings to the epilogue
+  float sa[T], sw, bs = 0.f;
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+    sa[i] = *reinterpret_cast<const float*>(p.as + (int64_t)min(m0 + wm * HB + i * 32 + l32, p.M - 1) * p.ldas);
+  sw = *reinterpret_cast<const float*>(p.ws + (int64_t)min(n0 + tid % TB, p.N - 1) * p.ldws);
+  int my_col = -1;   // output column of this thread's weight row
+  if (tid < TB && n0 + tid < p.N) my_col = p.col_map ? p.col_map[n0 + tid] : n0 + tid;
+  if (my_col >= p.n_out) my_col = -1;
+  if (p.bias && my_col >= 0) bs = bf16_bits_to_f32(p.bias[my_col]);
+
   const int swl = swz<CH>(l32);
-  uint32_t a_base[KS], w_base[KS];
+  uint32_t a_off[KS], w_off[KS];
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     const uint32_t c = ((2 * s + half) ^ swl) * 16;
-    a_base[s] = (wm * 32 * TM + l32) * RB + c;
-    w_base[s] = A_STAGE + (wn * 32 * TN + l32) * RB + c;
+    a_off[s] = (wm * HB + l32) * RB + c;
+    w_off[s] = (wn * HB + l32) * RB + c;
   }
-
-  auto issue = [&](int kt, uint8_t* st) __attribute__((always_inline)) {
-    const bool past = kt >= KT;   // past the end of K: a tile of zeros
-    kt = past ? KT - 1 : kt;
-    const int lim = kt == KT - 1 ? last_ch : CH;
-    issue_tile<TBM, RB, NW>(p.a, p.lda, m0, p.M, kt, st, wave, lane, zsrc, past, nullptr, lim);
-    issue_tile<TBN, RB, NW>(p.w, p.ldw, n0, p.N, kt, st + A_STAGE, wave, lane, zsrc, past, nullptr, lim);
-  };
-
-  v16i acc[TM][TN];
+  v16i acc[T][T];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < T; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v16i{};
-
-  auto compute = [&](const uint8_t* st) __attribute__((always_inline)) {
-    v4i fa[2][TM], fw[2][TN];
-    auto frag = [&](int s, int b) __attribute__((always_inline)) {
+    for (int j = 0; j < T; ++j) acc[i][j] = v16i{};
+  v4i fa[2][T], fw[2][T];
+  auto read = [&](const uint8_t* A, const uint8_t* W, int s, int b) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fw[b][j] = *reinterpret_cast<const v4i*>(st + w_base[s] + j * 32 * RB);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-        fa[b][i] = *reinterpret_cast<const v4i*>(st + a_base[s] + i * 32 * RB);
-    };
-    frag(0, 0);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      if (s + 1 < KS) frag(s + 1, (s + 1) & 1);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s & 1][j], fa[s & 1][i], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < T; ++i) {
+      fw[b][i] = *reinterpret_cast<const v4i*>(W + w_off[s] + i * 32 * RB);
+      fa[b][i] = *reinterpret_cast<const v4i*>(A + a_off[s] + i * 32 * RB);
     }
   };
-
-  // One K-tile (tile t lives in stage t % 2): wait until K-tile kt has landed,
-  // barrier (every wave is done reading the other stage), load K-tile kt+1
-  // into that stage and multiply K-tile kt.  Whole 2-step groups, no branch
-  // around the MFMAs; K-tiles past the end are loaded as zeros.
-  constexpr int NT = tile_loads<TBM, RB, NW>() + tile_loads<TBN, RB, NW>();   // per wave per K-tile
-  constexpr int N_MFMA = KS * TM * TN, N_DS0 = TM + TN, N_DS1 = (KS - 1) * (TM + TN);
-  auto step = [&](int kt, const uint8_t* st_cur, uint8_t* st_nxt, bool first) __attribute__((always_inline)) {
-    __builtin_amdgcn_sched_barrier(0);   // nothing of the previous step sinks below the wait
-    if (first) wait_vmcnt<NT>();
-    else wait_vmcnt<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");   // no LDS read moves above the barrier
-    if (!first) issue(kt + 1, st_nxt);
-    compute(st_cur);
-    __builtin_amdgcn_sched_group_barrier(0x100, N_DS0, 0);
+  auto mma = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < N_MFMA; ++k) {
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+      for (int j = 0; j < T; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[b][j], fa[b][i], acc[i][j], 0, 0, 0);
+  };
+  // a K-step's T*T MFMAs with the 2T fragment reads of the next and, where
+  // there are any, 2T loads
+  auto interleave = [&](bool loads) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 2 * T; ++k) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (k < N_DS1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (k < NT) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (T == 4) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   };
-  issue(0, st0);
-  issue(1, st1);
-  step(0, st0, st1, true);
-  step(1, st1, st0, false);
-  for (int kt = 2; kt < KT; kt += 2) {
-    step(kt, st0, st1, false);
-    step(kt + 1, st1, st0, false);
+  auto step = [&](auto slot_of, int kt) __attribute__((always_inline)) {
+    constexpr int I = decltype(slot_of)::value;
+    uint8_t* const A = slots[(2 * I) % 5];
+    uint8_t* const W = slots[(2 * I + 1) % 5];
+    uint8_t* const A1 = slots[(2 * I + 2) % 5];
+    uint8_t* const W1 = slots[(2 * I + 3) % 5];
+    uint8_t* const A2 = slots[(2 * I + 4) % 5];
+    read(A, W, 1, 1);
+    issue(abase, va, kt + 2, A2);
+    mma(0);
+    interleave(true);
+    __builtin_amdgcn_sched_barrier(0);
+    read(A, W, 2, 0);
+    mma(1);
+    interleave(false);
+    __builtin_amdgcn_sched_barrier(0);
+    read(A, W, 3, 1);
+    mma(0);
+    interleave(false);
+    __builtin_amdgcn_sched_barrier(0);
+    // every fragment of K-tile kt is read and K-tile kt+1 has landed (A of
+    // K-tile kt+2 may still be in flight)
+    wait_lgkmcnt0();
+    wait_vmcnt<LD>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    issue(wbase, vw, kt + 2, A);   // (2I + 5) % 5: the slot that A of K-tile kt leaves
+    read(A1, W1, 0, 0);
+    mma(1);
+    interleave(true);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  issue(abase, va, 0, s0);
+  issue(wbase, vw, 0, s1);
+  issue(abase, va, 1, s2);
+  issue(wbase, vw, 1, s3);
+  if (KF > 0) {
+    wait_vmcnt<2 * LD>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(s0, s1, 0, 0);
+    int kt = 0;
+    for (; kt + 5 <= KF; kt += 5) {
+      step(std::integral_constant<int, 0>{}, kt);
+      step(std::integral_constant<int, 1>{}, kt + 1);
+      step(std::integral_constant<int, 2>{}, kt + 2);
+      step(std::integral_constant<int, 3>{}, kt + 3);
+      step(std::integral_constant<int, 4>{}, kt + 4);
+    }
+    if (kt < KF) step(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < KF) step(std::integral_constant<int, 1>{}, kt + 1);
+    if (kt + 2 < KF) step(std::integral_constant<int, 2>{}, kt + 2);
+    if (kt + 3 < KF) step(std::integral_constant<int, 3>{}, kt + 3);
   }
-  wait_vmcnt<0>();   // the zero loads issued past the end
-#pragma unroll
-  for (int t = 0; t < NSC; ++t)
-    if (t * NTHR + tid < TBM + TBN) scl[t * NTHR + tid] = my_scale[t];
+  wait_vmcnt<0>();
   wait_lgkmcnt0();
   __syncthreads();
+  if (rest > 0) {   // the K-steps of a last, partial K-tile
+    const int ia = (2 * KF) % 5, iw = (2 * KF + 1) % 5;
+    const uint8_t* A = ia == 0 ? s0 : ia == 1 ? s1 : ia == 2 ? s2 : ia == 3 ? s3 : s4;
+    const uint8_t* W = iw == 0 ? s0 : iw == 1 ? s1 : iw == 2 ? s2 : iw == 3 ? s3 : s4;
+#pragma unroll
+    for (int s = 0; s < KS - 1; ++s)
+      if (s < rest) {
+        read(A, W, s, 0);
+        mma(0);
+      }
+    __syncthreads();
+  }
 
-  v16f out[TM][TN];
+  // Epilogue: the tile in bf16 through slots 0-3 (64 rows of 512 bytes each,
+  // 16-byte chunks swizzled by the row), the columns' scales and bias in slot
+  // 4; it leaves as whole rows.
+  float* const col = reinterpret_cast<float*>(s4);
+  if (tid < TB) {
+    col[tid] = sw;
+    col[TB + tid] = bs;
+  }
+  __syncthreads();
+  constexpr int ROW = 2 * TB;   // bytes of a staged row: a slot holds 64 of them
+  constexpr int SWM = TB / 8 < 16 ? TB / 8 - 1 : 15;   // chunk swizzle: the row's low bits
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const float sa = scl[wm * 32 * TM + i * 32 + l32];
+  for (int i = 0; i < T; ++i) {
+    v16f o[1][T];
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < T; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const v4f sw = *reinterpret_cast<const v4f*>(&scl[TBM + wn * 32 * TN + j * 32 + 8 * g + 4 * half]);
+        const v4f w4 = *reinterpret_cast<const v4f*>(col + wn * HB + j * 32 + 8 * g + 4 * half);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[i][j][4 * g + e] = ((float)acc[i][j][4 * g + e] * sa) * sw[e];
+        for (int e = 0; e < 4; ++e) o[0][j][4 * g + e] = ((float)acc[i][j][4 * g + e] * sa[i]) * w4[e];
+      }
+    if constexpr (LR) add_lowrank<1, T>(p, o, m0 + wm * HB + i * 32, n0 + wn * HB, lane);
+    // rows wm*HB + i*32 + l32 of the tile, 64 to a slot
+    uint8_t* const slot = T == 1 ? s0 + wm * 32 * ROW : wm ? slots[T / 2 + i / 2] : slots[i / 2];
+    uint8_t* const row = slot + ((i & 1) * 32 + l32) * ROW;
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = wn * HB + j * 32 + 8 * g + 4 * half;
+        const v4f b4 = *reinterpret_cast<const v4f*>(col + TB + c);
+        *reinterpret_cast<uint2*>(row + (((c >> 3) ^ (l32 & SWM)) * 16) + half * 8) =
+            make_uint2(pack_bf16_rne(o[0][j][4 * g] + b4[0], o[0][j][4 * g + 1] + b4[1]),
+                       pack_bf16_rne(o[0][j][4 * g + 2] + b4[2], o[0][j][4 * g + 3] + b4[3]));
       }
   }
-  const int row0 = m0 + wm * 32 * TM, col0 = n0 + wn * 32 * TN;
-  if constexpr (LR) add_lowrank<TM, TN>(p, out, row0, col0, lane);
-  // the whole output tile through LDS when its rows can leave as 16-byte
-  // pieces (no column map, aligned rows), else each wave by itself
-  constexpr int WRS = TBN * 2 + 16;
-  if constexpr ((TBM / 2) * WRS <= STAGE) {
-    if (!p.col_map && (p.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0) {
-      epilogue_wg<TM, TN, WGM, STAGE>(p, out, m0, n0, wm, wn, lane, st0, st1);
-      return;
+  __syncthreads();
+  if (!p.col_map && (p.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0) {
+    const int n_lim = p.N < p.n_out ? p.N : p.n_out;
+    constexpr int CPR = TB / 8;   // 16-byte pieces per row
+#pragma unroll
+    for (int q = 0; q < T; ++q) {
+#pragma unroll
+      for (int t = 0; t < 64 * CPR / 256; ++t) {
+        const int r = (256 / CPR) * t + tid / CPR, ch = tid % CPR, row = m0 + q * 64 + r, n = n0 + ch * 8;
+        const v4u v = *reinterpret_cast<const v4u*>(slots[q] + r * ROW + ((ch ^ (r & SWM)) * 16));
+        if (row >= p.M) continue;
+        uint16_t* const o = p.out + (int64_t)row * p.ld_out + n;
+        if (n + 8 <= n_lim) {
+          __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(o));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < n_lim) o[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
+      }
     }
+    return;
   }
-  epilogue_tr<false, TM, TN>(p, out, 1.0f, row0, col0, lane);
+  // a column map, or rows that are not 16-byte aligned: one column per thread,
+  // so a wave stores 64 neighbours of a row at a time
+  int* const map = reinterpret_cast<int*>(col);
+  __syncthreads();
+  if (tid < TB) map[tid] = my_col;
+  __syncthreads();
+  const int c = tid % TB, mc = map[c];
+  if (mc < 0) return;
+#pragma unroll
+  for (int q = 0; q < T; ++q) {
+    const int rows = min(64, p.M - (m0 + q * 64));
+#pragma unroll 8
+    for (int r = tid / TB; r < rows; r += 256 / TB)
+      p.out[(int64_t)(m0 + q * 64 + r) * p.ld_out + mc] =
+          *reinterpret_cast<const uint16_t*>(slots[q] + r * ROW + (((c >> 3) ^ (r & SWM)) * 16) + (c & 7) * 2);
+  }
 }
 
-template <int TM, int TN, int WGM>
-hipError_t launch_cfg(GemmP p, hipStream_t s) {
-  constexpr int TBM = 32 * TM * WGM, TBN = 64 * TN;
+template <int T>
+hipError_t launch_ring(GemmP p, hipStream_t s) {
+  constexpr int TB = 64 * T;
   const bool grp = p.goff != nullptr;
-  p.tiles_m = grp ? (int)group_tiles_bound(p.M, p.groups, TBM) : (p.M + TBM - 1) / TBM;
-  p.tiles_n = (p.N + TBN - 1) / TBN;
+  p.tiles_m = grp ? (int)group_tiles_bound(p.M, p.groups, TB) : (p.M + TB - 1) / TB;
+  p.tiles_n = (p.N + TB - 1) / TB;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  // tile-rows per group: one XCD's share (tiles / 8) as a near-square block
   int gm = 1;
   while (gm * 2 <= p.tiles_m && (int64_t)gm * 2 * gm * 2 <= (tiles + 7) / 8) gm *= 2;
   const dim3 grid((unsigned)tiles);
-  if (grp) gemm_i8_kernel<TM, TN, WGM, false, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
-  else if (p.rank > 0) gemm_i8_kernel<TM, TN, WGM, true, false><<<grid, 128 * WGM, 0, s>>>(p, gm);
-  else gemm_i8_kernel<TM, TN, WGM, false, false><<<grid, 128 * WGM, 0, s>>>(p, gm);
+  if (grp) gemm_i8_ring_kernel<T, false, true><<<grid, 256, 0, s>>>(p, gm);
+  else if (p.rank == 0) gemm_i8_ring_kernel<T, false, false><<<grid, 256, 0, s>>>(p, gm);
+  else if constexpr (T < 4) gemm_i8_ring_kernel<T, true, false><<<grid, 256, 0, s>>>(p, gm);
+  else return hipErrorInvalidValue;   // not launched: no registers left for the branch
   return hipGetLastError();
+}
+
+// Estimated time (us) of a product of about t tiles of 64 T x 64 T with kt
+// K-tiles: the latency of one workgroup, or the rounds of the workgroups that
+// fit the 256 compute units (four of T = 1, two of T = 2, one of T = 4; large
+// workgroups come in whole rounds).  The constants are fits to
+// 64 .. 8192 rows and columns and K = 128 .. 8192, within some 15%.
+template <int T>
+double cost(double t, double kt) {
+  constexpr double lat0 = T == 1 ? 1.6 : T == 2 ? 4.2 : 10.0, lat1 = T == 1 ? 0.38 : T == 2 ? 0.43 : 0.94;
+  constexpr double fix = T == 1 ? 2.5 : T == 2 ? 4.5 : 10.5, per = T == 1 ? 0.85 : T == 2 ? 0.97 : 1.51;
+  const double slots = 256.0 * (4 / T);
+  const double rounds = T == 4 ? std::ceil(t / slots) : t / slots;
+  return std::max(lat0 + lat1 * kt, 2.5 + rounds * (fix + per * kt));
 }
 
 }  // namespace
 
 hipError_t launch_gemm_i8(const GemmArgs& a, hipStream_t s) {
-  GemmP p = gemm_params(a);
-  // rows a tile can fill: all of them, or a group's share
-  const int64_t m = a.goff ? (a.M + a.groups - 1) / a.groups : a.M;
-  const int64_t cu = 256;
-  auto rounds = [&](int tbm, int tbn) {
-    const int64_t t = ((m + tbm - 1) / tbm) * ((a.N + tbn - 1) / tbn) * (a.goff ? a.groups : 1);
-    return (t + cu - 1) / cu;
+  const GemmP p = gemm_params(a);
+  // the tile sizes trade reuse (a T = 4 tile loads a quarter of the bytes per
+  // MFMA of a T = 1 tile) against how many workgroups there are to fill the
+  // GPU: 8192^3 2543 / 2154 Top/s with T = 4 / 2, 4096 x 4608 x 1152 46 / 32 /
+  // 42 us, 777 x 1001 x 1184 34 / 10.4 / 6.2 us with T = 4 / 2 / 1.  Groups
+  // leave half a tile empty each, on average.
+  auto tiles = [&](int tb) {
+    const double m = a.goff ? (double)a.M / tb + 0.5 * std::min<int64_t>(a.groups, a.M)
+                            : (double)((a.M + tb - 1) / tb);
+    return m * (double)((a.N + tb - 1) / tb);
   };
-  const int64_t c44 = rounds(256, 256) * 16 * 10, c22 = rounds(128, 128) * 4 * 16;
-  if (c44 <= c22) return launch_cfg<2, 4, 4>(p, s);
-  if (((m + 127) / 128) * ((a.N + 127) / 128) * (a.goff ? a.groups : 1) < 128) return launch_cfg<1, 1, 2>(p, s);
-  return launch_cfg<2, 2, 2>(p, s);
+  const double kt = (double)((a.K + BK - 1) / BK);
+  const double c1 = cost<1>(tiles(64), kt), c2 = cost<2>(tiles(128), kt), c4 = cost<4>(tiles(256), kt);
+  // T = 4 has no registers left for the low-rank branch
+  if (a.rank == 0 && c4 < c2 && c4 < c1) return launch_ring<4>(p, s);
+  return c2 < c1 ? launch_ring<2>(p, s) : launch_ring<1>(p, s);
 }
 
 }  // namespace mxq

@@ -63,6 +63,7 @@ def test_gemm_refusals(lib):
     assert call(i8(8, 0), i8(8, 0)) == SHAPE
     big = (1 << 17) + 32                                     # sums would leave int32
     assert call(i8(8, big), i8(8, big)) == SHAPE
+    assert call(i8(8, 96, ld=(1 << 24) + 16), i8(8, 96)) == SHAPE
     assert call(i8(8, 96), i8(8, 96), ld=7) == INV
     assert call(i8(8, 96), i8(9, 96)) == SHAPE               # more rows than columns out, no map
     assert call(i8(0, 96), i8(8, 96)) == 0
