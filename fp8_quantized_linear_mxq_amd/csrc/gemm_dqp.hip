@@ -597,10 +597,26 @@ hipError_t launch_gemm_dqp(const GemmArgs& a, hipStream_t s) {
   const bool lr = a.rank > 0;
   if (a.w_fmt != FMT_NVFP4 && a.w_fmt != FMT_MXFP4) return hipErrorInvalidValue;
   if (a.goff) {
-    // the plain GEMM's tiles for this pair: 64x128, slabbed 128x128 past 32 K-tiles
+    // Tiles by the rows per group, on average (times for 32 groups, K = 4096, N =
+    // 2048, weights from HBM): 32-row tiles while the weights' traffic decides,
+    // 32 x 256 where those fill the GPU (32 x 256 / 32 x 128 / 64 x 128: 16 rows
+    // 26.3 / 20.2 / 25.2 us, 64 rows 33.5 / 37.1 / 42.8, 256 rows 39 / 43 / 47,
+    // 1024 rows 63 / 59 / 68); 64 x 128 beyond, 64 x 256 once there are three
+    // rounds of those (64 x 128 / 64 x 256: 2048 rows 76 / 82, 8192 rows 221 /
+    // 190; 32 x 128 92 / 259).  Past 32 K-tiles the fp32 chains are slabbed.
     if (a.a_fmt != FMT_BF16 || a.w_fmt != FMT_MXFP4) return hipErrorInvalidValue;
-    if (a.K / BK > 32) return launch_grouped<K_BF, K_MX4, 2, 2, true, 2, 2>(dp, s);
-    return launch_grouped<K_BF, K_MX4, 2, 1, false, 1, 4>(dp, s);
+    const bool slab = a.K / BK > 32;
+    if (a.M > 40 * a.groups) {
+      if (slab) return launch_grouped<K_BF, K_MX4, 2, 2, true, 2, 2>(dp, s);
+      const double tiles = ((double)a.M / 64 + 0.5 * (double)a.groups) * (double)((a.N + 255) / 256);
+      if (tiles >= 3 * 256) return launch_grouped<K_BF, K_MX4, 2, 2, false, 1, 4>(dp, s);
+      return launch_grouped<K_BF, K_MX4, 2, 1, false, 1, 4>(dp, s);
+    }
+    if (slab) return launch_grouped<K_BF, K_MX4, 1, 1, true, 1, 4>(dp, s);
+    const int64_t hit = a.M < a.groups ? a.M : a.groups;
+    if (a.M <= 16 * a.groups && hit * ((a.N + 255) / 256) >= 192)
+      return launch_grouped<K_BF, K_MX4, 1, 2, false, 1, 4>(dp, s);
+    return launch_grouped<K_BF, K_MX4, 1, 1, false, 1, 4>(dp, s);
   }
   switch (a.a_fmt) {
     case FMT_NVFP4: return launch_w<K_NV>(a.w_fmt, lr, dp, s);

@@ -31,19 +31,20 @@ enum : int { P_I8 = 0, P_MX4 = 1, P_BF4 = 2 };
 constexpr int kWaves = 4;
 constexpr int kPairs = 4;    // step pairs in flight per wave
 
-// NT weight tiles and RT activation tiles of 16 rows per workgroup.
-template <int P, int NT, int RT, bool GRP>
+// NT weight tiles and one activation tile of 16 rows per workgroup.
+template <int P, int NT, bool GRP>
 __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
   using Acc = std::conditional_t<P == P_I8, v4i, v4f>;
   constexpr int S = 2 * kPairs;                      // steps per round
   constexpr int AV = P == P_BF4 ? 4 : 1;             // 16-byte pieces of a per step
-  __shared__ Acc part[kWaves][NT * RT][64];
+  static_assert(NT <= kWaves, "an output quad per thread");
+  __shared__ Acc part[kWaves][NT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
   const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
-  int m0 = tm * 16 * RT;
+  int m0 = tm * 16;
   if constexpr (GRP) {
-    m0 = enter_group(p, 16 * RT, tm);
+    m0 = enter_group(p, 16, tm);
     if (m0 < 0) return;
   }
   const int n0 = tn * 16 * NT;
@@ -58,24 +59,36 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
     wrow[j] = p.w + n * p.ldw + 16 * q;
     wscl[j] = p.ws + n * p.ldws;
   }
-  const uint8_t* arow[RT];
-  const uint8_t* ascl[RT];
+  const int64_t mr = min(m0 + r16, p.M - 1);
+  const uint8_t* const arow = p.a + mr * p.lda + (P == P_BF4 ? 64 : 16) * q;
+  const uint8_t* const ascl = p.as + mr * p.ldas;
+
+  // The output quad this thread finishes: lane l of weight tile `wave` holds
+  // activation row l % 16 and weight rows 4 (l / 16) + [0, 4).  Its scales, bias
+  // and columns are on their way while the weights stream.
+  const int m = m0 + r16, n = n0 + wave * 16 + 4 * q;
+  const bool mine = wave < NT && m < p.M;
+  float sa = 0.f, sw[4], bs[4];
+  int col[4];
+  if (mine) {
+    if constexpr (P == P_I8) sa = *reinterpret_cast<const float*>(p.as + (int64_t)m * p.ldas);
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int64_t m = min(m0 + i * 16 + r16, p.M - 1);
-    arow[i] = p.a + m * p.lda + (P == P_BF4 ? 64 : 16) * q;
-    ascl[i] = p.as + m * p.ldas;
+    for (int e = 0; e < 4; ++e) {
+      const int ne = min(n + e, p.N - 1);
+      if constexpr (P == P_I8) sw[e] = *reinterpret_cast<const float*>(p.ws + (int64_t)ne * p.ldws);
+      col[e] = p.col_map ? p.col_map[ne] : ne;
+      if (n + e >= p.N || col[e] >= p.n_out) col[e] = -1;
+      bs[e] = p.bias && col[e] >= 0 ? bf16_bits_to_f32(p.bias[col[e]]) : 0.f;
+    }
   }
 
-  Acc acc[NT][RT];
+  Acc acc[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < RT; ++i) acc[j][i] = Acc{};
+  for (int j = 0; j < NT; ++j) acc[j] = Acc{};
 
   for (int s0 = 2 * wave; s0 < steps; s0 += 2 * kPairs * kWaves) {
-    v4i wf[S][NT], af[S][RT][AV];
-    uint32_t wd[S][NT], ad[S][RT];
+    v4i wf[S][NT], af[S][AV];
+    uint32_t wd[S][NT], ad[S];
 #pragma unroll
     for (int t = 0; t < S; ++t) {
       const int s = s0 + (t >> 1) * 2 * kWaves + (t & 1);
@@ -91,16 +104,13 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-#pragma unroll
-        for (int v = 0; v < AV; ++v) {
-          af[t][i][v] = v4i{};
-          if (in) af[t][i][v] = *reinterpret_cast<const v4i*>(arow[i] + (P == P_BF4 ? 256 : 64) * s + 16 * v);
-        }
-        if constexpr (P == P_MX4) {
-          ad[t][i] = 0;
-          if (in) ad[t][i] = *reinterpret_cast<const uint32_t*>(ascl[i] + 4 * s);
-        }
+      for (int v = 0; v < AV; ++v) {
+        af[t][v] = v4i{};
+        if (in) af[t][v] = *reinterpret_cast<const v4i*>(arow + (P == P_BF4 ? 256 : 64) * s + 16 * v);
+      }
+      if constexpr (P == P_MX4) {
+        ad[t] = 0;
+        if (in) ad[t] = *reinterpret_cast<const uint32_t*>(ascl + 4 * s);
       }
     }
 #pragma unroll
@@ -108,20 +118,13 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if constexpr (P == P_I8) {
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-            acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[t][j], af[t][i][0], acc[j][i], 0, 0, 0);
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[t][j], af[t][0], acc[j], 0, 0, 0);
         } else if constexpr (P == P_MX4) {
-          const v4i& w4 = wf[t][j];
+          const v4i &w4 = wf[t][j], &a4 = af[t][0];
           const v8i wv = __builtin_shufflevector(w4, w4, 0, 1, 2, 3, -1, -1, -1, -1);
-          const int sw = (int)(wd[t][j] >> (8 * q));
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const v4i& a4 = af[t][i][0];
-            const v8i av = __builtin_shufflevector(a4, a4, 0, 1, 2, 3, -1, -1, -1, -1);
-            acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wv, av, acc[j][i], 4, 4, 0, sw, 0, (int)(ad[t][i] >> (8 * q)));
-          }
+          const v8i av = __builtin_shufflevector(a4, a4, 0, 1, 2, 3, -1, -1, -1, -1);
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              wv, av, acc[j], 4, 4, 0, (int)(wd[t][j] >> (8 * q)), 0, (int)(ad[t] >> (8 * q)));
         } else {
           // the block scale with its exponent raised by 2 (undone below), so
           // that code 0 is a normal fp32 scale for the converts
@@ -134,88 +137,72 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 1)),
                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 2)),
                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, sc, 3))));
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-              acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  wv, __builtin_bit_cast(v8bf, af[t][i][v]), acc[j][i], 0, 0, 0);
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(v8bf, af[t][v]), acc[j], 0, 0, 0);
           }
         }
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < RT; ++i) part[wave][j * RT + i][lane] = acc[j][i];
+  for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
   __syncthreads();
+  if (!mine) return;
 
-  // lane l of a tile holds activation row l % 16 and weight rows 4 (l / 16) + [0, 4)
-  for (int idx = threadIdx.x; idx < NT * RT * 64; idx += 64 * kWaves) {
-    const int tile = idx >> 6, l = idx & 63;
-    Acc sum = part[0][tile][l];
+  Acc sum = part[0][wave][lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += part[w][tile][l];
-    const int m = m0 + (tile % RT) * 16 + (l & 15);
-    const int n = n0 + (tile / RT) * 16 + 4 * (l >> 4);
-    if (m >= p.M) continue;
-    uint16_t* orow = p.out + (int64_t)m * p.ld_out;
-    float sa = 0.f;
-    if constexpr (P == P_I8) sa = *reinterpret_cast<const float*>(p.as + (int64_t)m * p.ldas);
+  for (int w = 1; w < kWaves; ++w) sum += part[w][wave][lane];
+  uint16_t* const orow = p.out + (int64_t)m * p.ld_out;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (n + e >= p.N) break;
-      const int c = p.col_map ? p.col_map[n + e] : n + e;
-      if (c < 0 || c >= p.n_out) continue;
-      float v;
-      if constexpr (P == P_I8) {
-        const float sw = *reinterpret_cast<const float*>(p.ws + (int64_t)(n + e) * p.ldws);
-        v = ((float)sum[e] * sa) * sw;
-        if constexpr (!GRP) {
-          const float* u = p.u + (int64_t)m * p.ld_u;
-          const uint16_t* l2 = p.l2t + (int64_t)c * p.rank;
-          for (int r = 0; r < p.rank; ++r) v = fmaf(u[r], bf16_bits_to_f32(l2[r]), v);
-        }
-      } else {
-        v = P == P_BF4 ? sum[e] * 0.25f : sum[e];
+  for (int e = 0; e < 4; ++e) {
+    if (col[e] < 0) continue;
+    float v;
+    if constexpr (P == P_I8) {
+      v = ((float)sum[e] * sa) * sw[e];
+      if constexpr (!GRP) {
+        const float* u = p.u + (int64_t)m * p.ld_u;
+        const uint16_t* l2 = p.l2t + (int64_t)col[e] * p.rank;
+        for (int r = 0; r < p.rank; ++r) v = fmaf(u[r], bf16_bits_to_f32(l2[r]), v);
       }
-      if (p.bias) v += bf16_bits_to_f32(p.bias[c]);
-      orow[c] = (uint16_t)f32_to_bf16_bits(v);
+    } else {
+      v = P == P_BF4 ? sum[e] * 0.25f : sum[e];
     }
+    orow[col[e]] = (uint16_t)f32_to_bf16_bits(v + bs[e]);
   }
 }
 
-template <int P, int NT, int RT, bool GRP>
+template <int P, int NT, bool GRP>
 hipError_t go(GemmP p, hipStream_t s) {
-  p.tiles_m = GRP ? (int)group_tiles_bound(p.M, p.groups, 16 * RT) : (p.M + 16 * RT - 1) / (16 * RT);
+  p.tiles_m = GRP ? (int)group_tiles_bound(p.M, p.groups, 16) : (p.M + 15) / 16;
   p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  gemm_few_kernel<P, NT, RT, GRP><<<(unsigned)tiles, 64 * kWaves, 0, s>>>(p);
+  gemm_few_kernel<P, NT, GRP><<<(unsigned)tiles, 64 * kWaves, 0, s>>>(p);
   return hipGetLastError();
-}
-
-template <int P, int NT>
-hipError_t by_rows(const GemmP& p, hipStream_t s) {
-  if ((int64_t)p.M <= (int64_t)16 * p.groups) return go<P, NT, 1, true>(p, s);
-  return go<P, NT, 2, true>(p, s);
 }
 
 }  // namespace
 
-// Where this kernel is the faster one: up to 16 rows of a plain product (16 x
-// 4096 x 4096 7.3 us against 8.9 with 64 x 64 tiles; 32 rows 9.2 against 8.8),
-// up to 32 on average per group.
+// Where this kernel is the faster one, against the tiled kernels.  A plain
+// product: up to 16 rows (int8 16 x 4096 x 4096 7.3 us against 8.9, 32 rows 9.2 /
+// 8.8).  By expert, weights from HBM: int8 up to four rows per group on average
+// (64 groups, N = 1536, K = 2048: 8 rows 8.1 / 10.7, 128 rows 35 / 42, 512 rows 52
+// / 45); 4-bit weights while the experts hit have too few 64-row pieces of
+// weights to fill the GPU with tiles (N = 2048, K = 4096, 4 / 8 / 14 experts:
+// MXFP4 7.6 / 11.4 / 18.7 us against 10.2 / 12.3 / 15.5, bf16 x MXFP4 9.4 / 13.7 /
+// 23.0 against 19.6 / 19.2 / 20.2).
 bool few_rows(const GemmArgs& a) {
   if (!a.goff) return a.M <= 16;
-  return a.M <= 32 * a.groups;
+  if (a.a_fmt == FMT_INT8) return a.M <= 4 * a.groups;
+  const int64_t hit = a.M < a.groups ? a.M : a.groups, pieces = hit * ((a.N + 63) / 64);
+  return a.M <= 16 * a.groups && pieces < (a.a_fmt == FMT_MXFP4 ? 320 : 384);
 }
 
 hipError_t launch_gemm_few(const GemmArgs& a, hipStream_t s) {
   const GemmP p = gemm_params(a);
-  if (!a.goff) return go<P_I8, 1, 1, false>(p, s);
-  if (a.a_fmt == FMT_INT8) return by_rows<P_I8, 1>(p, s);
-  if (a.a_fmt == FMT_MXFP4) return by_rows<P_MX4, 1>(p, s);
-  return by_rows<P_BF4, 2>(p, s);
+  if (!a.goff) return go<P_I8, 1, false>(p, s);
+  if (a.a_fmt == FMT_INT8) return go<P_I8, 1, true>(p, s);
+  if (a.a_fmt == FMT_MXFP4) return go<P_MX4, 2, true>(p, s);
+  return go<P_BF4, 2, true>(p, s);
 }
 
 }  // namespace mxq

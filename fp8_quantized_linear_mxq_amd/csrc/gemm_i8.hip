@@ -352,8 +352,8 @@ hipError_t launch_gemm_i8(const GemmArgs& a, hipStream_t s) {
   // 42 us, 777 x 1001 x 1184 34 / 10.4 / 6.2 us with T = 4 / 2 / 1.  Groups
   // leave half a tile empty each, on average.
   auto tiles = [&](int tb) {
-    const double m = a.goff ? (double)a.M / tb + 0.5 * std::min<int64_t>(a.groups, a.M)
-                            : (double)((a.M + tb - 1) / tb);
+    const double m = a.groups > 1 ? (double)a.M / tb + 0.5 * std::min<int64_t>(a.groups, a.M)
+                                  : (double)((a.M + tb - 1) / tb);
     return m * (double)((a.N + tb - 1) / tb);
   };
   const double kt = (double)((a.K + BK - 1) / BK);

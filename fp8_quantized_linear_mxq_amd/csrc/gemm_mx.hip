@@ -348,11 +348,24 @@ hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
 hipError_t launch_gemm_mx(const GemmArgs& a, hipStream_t s) {
   const GemmP p = gemm_params(a);
   const bool lr = a.rank > 0;
+  // Rows grouped by expert: the tile by the rows per group, on average (times
+  // for 32 groups, K = 4096, N = 2048, weights from HBM).
+  if (a.goff && a.M <= 16 * a.groups) {
+    // the weights' traffic decides; four workgroups' loads in flight per compute
+    // unit: 64 rows 26.5 us against 31.1 with 128 x 128, 256 rows 30.7 / 32.6,
+    // 1024 rows 44 / 35
+    if (a.K > 4096) return launch_cfg<1, 1, 2, true>(lr, p, s);
+    return launch_cfg<1, 1, 2, false>(lr, p, s);
+  }
   if (a.K > 4096) return launch_cfg<2, 2, 2, true>(lr, p, s);
   if (a.goff) {
-    // 256-row tiles once the groups fill most of one on average
-    if (a.M >= 192 * a.groups) return launch_cfg<2, 4, 4, false>(lr, p, s);
-    return launch_cfg<2, 2, 2, false>(lr, p, s);
+    // 128 x 128, 256 x 192, 256 x 256: 4096 rows 62 / 69 / 80 us, 8192 rows 91 /
+    // 74 / 84, 16384 rows 142 / 133 / 125 (the last pays with 2.5 rounds of tiles,
+    // half of one empty per group)
+    if (a.M < 192 * a.groups) return launch_cfg<2, 2, 2, false>(lr, p, s);
+    const double tiles = ((double)a.M / 256 + 0.5 * (double)a.groups) * (double)((a.N + 255) / 256);
+    if (tiles >= 2.5 * 256) return launch_cfg<2, 4, 4, false>(lr, p, s);
+    return launch_cfg<2, 3, 4, false>(lr, p, s);
   }
   // Large tiles move the fewest bytes per MFMA; pick the one whose tile count
   // fills the 256 compute units in the fewest rounds, per unit of tile work.
