@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -48,19 +49,25 @@ class QTensorC(C.Structure):
                 ("tensor_scale", C.c_void_p)]
 
 
+# The same layout as bytes: a read-only operand is passed as one of these (a
+# tenth of the time of building the Structure).
+_QTENSOR = struct.Struct("iiqqQqQqQ")
+
 _lib = None
+_torch = None   # the torch module, bound by load(): an import statement costs 0.2 us a call
 
 
 def load():
     """Load libmxq.so (built in-tree by ``build.py``); raises if absent."""
-    global _lib
+    global _lib, _torch
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"libmxq is not built ({LIB_PATH} missing); run "
                            "python -m fp8_quantized_linear_mxq_amd.build")
     try:  # share the HIP runtime torch already mapped (same soname)
-        import torch  # noqa: F401
+        import torch
+        _torch = torch
     except ImportError:
         pass
     lib = C.CDLL(LIB_PATH)
@@ -103,6 +110,12 @@ def load():
     lib.mxq_status_string.restype = C.c_char_p
     lib.mxq_version.argtypes = []
     lib.mxq_version.restype = i32
+    # entry points whose operands the binding passes as bytes
+    b = C.c_char_p
+    lib.gemm = C.CFUNCTYPE(i32, b, b, vp, vp, i64, vp, i32, vp, vp, i64, i64, vp, sz, vp)(("mxq_gemm", lib))
+    lib.gemm_grouped = C.CFUNCTYPE(i32, b, b, i32, vp, vp, vp, i64, vp)(("mxq_gemm_grouped", lib))
+    lib.quantize = C.CFUNCTYPE(i32, vp, i32, i64, i64, i64, i32, vp, vp, i32, vp, i64, b, vp, sz,
+                               vp)(("mxq_quantize", lib))
     _lib = lib
     return lib
 
@@ -121,8 +134,9 @@ def _stream(stream):
     as a handle: building the Stream object takes 3 us of a small call's 12)."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _torch.cuda.is_initialized():
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+    return _torch.cuda.current_stream().cuda_stream
 
 
 def storage(fmt: int, cols: int):
@@ -163,10 +177,21 @@ class QTensor:
                         scales.stride(0) * scales.element_size() if scales is not None else 0,
                         ts.data_ptr() if ts is not None else None)
 
+    def packed(self) -> bytes:
+        """c() as bytes, for the entry points that only read the operand."""
+        codes, scales, ts = self.codes, self.scales, self.tensor_scale
+        return _QTENSOR.pack(self.fmt, 0, self.rows, self.cols,
+                             0 if codes is None else codes.data_ptr(),
+                             0 if codes is None else codes.stride(0) * codes.element_size(),
+                             0 if scales is None else scales.data_ptr(),
+                             0 if scales is None else scales.stride(0) * scales.element_size(),
+                             0 if ts is None else ts.data_ptr())
+
 
 def empty_qtensor(fmt: int, rows: int, cols: int, device="cuda") -> QTensor:
     """Allocates (torch) the buffers of a quantized operand."""
-    import torch
+    load()
+    torch = _torch
     if fmt == INT8 and cols % 32 == 0:
         return QTensor(fmt, rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
                        torch.empty((rows, 1), dtype=torch.float32, device=device))
@@ -194,11 +219,13 @@ def bf16_operand(x) -> QTensor:
 def int8_operand(codes, scales) -> QTensor:
     """int8 codes [rows, K] (cuda, row-major) and one float32 scale per row
     ([rows] or [rows, 1]) as a quantized operand."""
-    import torch
-    if codes.dim() != 2 or codes.element_size() != 1 or (codes.shape[1] > 1 and codes.stride(1) != 1):
+    shape = codes.shape
+    if len(shape) != 2 or codes.element_size() != 1 or (codes.stride(1) != 1 and shape[1] > 1):
         raise ValueError("int8_operand needs row-major 2-D 8-bit codes")
-    rows, cols = codes.shape
-    if scales.dtype != torch.float32 or scales.shape not in ((rows,), (rows, 1)):
+    rows, cols = shape
+    sshape = scales.shape
+    if scales.element_size() != 4 or not scales.is_floating_point() or sshape[0] != rows or \
+            not (len(sshape) == 1 or (len(sshape) == 2 and sshape[1] == 1)):
         raise ValueError("int8_operand needs float32 scales of shape [rows] or [rows, 1]")
     return QTensor(INT8, rows, cols, codes, scales)
 
@@ -219,8 +246,8 @@ def quantize(x, fmt: int, hadamard: int = 0, static_tensor_scale=None, l1t=None,
              out: QTensor | None = None, workspace=None, stream=None, l1p=None) -> QTensor:
     """mxq_quantize on a 2-D torch tensor (float32 or bfloat16, cuda); with
     ``l1p`` (L1 from pack_l1t) instead of ``l1t``, mxq_quantize_lrp."""
-    import torch
     lib = load()
+    torch = _torch
     rows, cols = x.shape
     dt = DT_BF16 if x.dtype == torch.bfloat16 else DT_F32
     if out is None:
@@ -230,18 +257,19 @@ def quantize(x, fmt: int, hadamard: int = 0, static_tensor_scale=None, l1t=None,
         if n > 0:
             workspace = torch.empty((n,), dtype=torch.uint8, device=x.device)
     wsp, wsn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
-    qc = out.c()
     if l1p is not None:
+        qc = out.c()
         st = lib.mxq_quantize_lrp(_ptr(x), dt, rows, cols, x.stride(0), hadamard,
                                   _ptr(static_tensor_scale), _ptr(l1p), l1p.shape[0], _ptr(u),
                                   0 if u is None else u.stride(0), C.byref(qc), wsp, wsn, _stream(stream))
         _check("mxq_quantize_lrp", st)
         return out
     rank = 0 if l1t is None else l1t.shape[0]
-    st = lib.mxq_quantize(_ptr(x), dt, rows, cols, x.stride(0), hadamard,
-                          _ptr(static_tensor_scale), _ptr(l1t), rank, _ptr(u),
-                          0 if u is None else u.stride(0), C.byref(qc), wsp, wsn, _stream(stream))
-    _check("mxq_quantize", st)
+    st = lib.quantize(x.data_ptr(), dt, rows, cols, x.stride(0), hadamard,
+                      _ptr(static_tensor_scale), _ptr(l1t), rank, _ptr(u),
+                      0 if u is None else u.stride(0), out.packed(), wsp, wsn, _stream(stream))
+    if st != 0:
+        raise MxqError("mxq_quantize", st)
     return out
 
 
@@ -266,18 +294,17 @@ def gemm(a: QTensor, w: QTensor, n_out: int | None = None, w_out_col=None, u=Non
          bias=None, out=None, stream=None, workspace=None):
     """mxq_gemm; returns the bf16 [M, n_out] output tensor.  ``workspace``:
     a device tensor, None (allocated when the route can use one) or False."""
-    import torch
     lib = load()
     n_out = w.rows if n_out is None else n_out
     if out is None:
-        out = torch.empty((a.rows, n_out), dtype=torch.bfloat16, device=a.codes.device)
-    ac, wc = a.c(), w.c()
+        out = a.codes.new_empty((a.rows, n_out), dtype=_torch.bfloat16)
     rank = 0 if l2t is None else l2t.shape[1]
-    wsp, wsn = _gemm_workspace(a, [w], workspace)
-    st = lib.mxq_gemm(C.byref(ac), C.byref(wc), _ptr(w_out_col), _ptr(u),
-                      0 if u is None else u.stride(0), _ptr(l2t), rank, _ptr(bias), _ptr(out),
-                      out.stride(0), n_out, wsp, wsn, _stream(stream))
-    _check("mxq_gemm", st)
+    wsp, wsn = (None, 0) if workspace is None and w.fmt != INT4 else _gemm_workspace(a, [w], workspace)
+    st = lib.gemm(a.packed(), w.packed(), _ptr(w_out_col), _ptr(u), 0 if u is None else u.stride(0),
+                  _ptr(l2t), rank, _ptr(bias), out.data_ptr(), out.stride(0), n_out, wsp, wsn,
+                  _stream(stream))
+    if st != 0:
+        raise MxqError("mxq_gemm", st)
     return out
 
 
@@ -304,18 +331,16 @@ def gemm_grouped(a: QTensor, w: QTensor, offsets, bias=None, out=None, stream=No
     cuda, [experts + 1]) their groups, ``w`` the experts' weights one after
     the other ([experts * N, K]), ``bias`` bf16 [experts, N]; returns the bf16
     [rows, N] output tensor (rows of no group are left as they are in ``out``)."""
-    import torch
     lib = load()
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
+    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("gemm_grouped needs contiguous 1-D int32 offsets")
     groups = offsets.shape[0] - 1
-    n = w.rows // groups if groups > 0 else 0
     if out is None:
-        out = torch.empty((a.rows, n), dtype=torch.bfloat16, device=a.codes.device)
-    ac, wc = a.c(), w.c()
-    st = lib.mxq_gemm_grouped(C.byref(ac), C.byref(wc), groups, _ptr(offsets), _ptr(bias), _ptr(out),
-                              out.stride(0), _stream(stream))
-    _check("mxq_gemm_grouped", st)
+        out = a.codes.new_empty((a.rows, w.rows // groups if groups > 0 else 0), dtype=_torch.bfloat16)
+    st = lib.gemm_grouped(a.packed(), w.packed(), groups, offsets.data_ptr(), _ptr(bias), out.data_ptr(),
+                          out.stride(0), _stream(stream))
+    if st != 0:
+        raise MxqError("mxq_gemm_grouped", st)
     return out
 
 
@@ -327,41 +352,43 @@ def qk_norm_rope(x, n_q_heads: int, n_k_heads: int, head_dim: int, q_weight=None
     rotation given by the float32 tables ``cos`` and ``sin`` [n_pos, rot/2].
     Returns (q [tokens, n_q_heads, head_dim], k [tokens, n_k_heads, head_dim]);
     ``q_out`` and ``k_out`` may be given with any token and head strides."""
-    import torch
     lib = load()
-    if x.dtype not in (torch.bfloat16, torch.float32) or x.dim() != 2 or x.stride(1) != 1:
+    torch = _torch
+    dt = x.dtype
+    if dt not in (torch.bfloat16, torch.float32) or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("qk_norm_rope needs a row-major 2-D float32 or bfloat16 tensor")
-    tokens = x.shape[0]
-    if x.shape[1] < (n_q_heads + n_k_heads) * head_dim:
+    tokens, width = x.shape
+    if width < (n_q_heads + n_k_heads) * head_dim:
         raise ValueError("qk_norm_rope: x is narrower than its heads")
     for g in (q_weight, k_weight):
-        if g is not None and (g.dtype != x.dtype or g.shape != (head_dim,) or not g.is_contiguous()):
+        if g is not None and (g.dtype != dt or g.shape != (head_dim,) or g.stride(0) != 1):
             raise ValueError("qk_norm_rope: weights are contiguous [head_dim] tensors of x's dtype")
     rot = n_pos = 0
     if cos is not None:
-        for t in (cos, sin):
-            if t is None or t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape \
-                    or not t.is_contiguous():
-                raise ValueError("qk_norm_rope: cos and sin are contiguous float32 [n_pos, rot / 2]")
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        shape = cos.shape
+        if (sin is None or cos.dtype != torch.float32 or sin.dtype != torch.float32 or len(shape) != 2
+                or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous()):
+            raise ValueError("qk_norm_rope: cos and sin are contiguous float32 [n_pos, rot / 2]")
+        n_pos, rot = shape[0], 2 * shape[1]
         if positions is not None and (positions.dtype != torch.int32 or positions.shape != (tokens,)
                                       or not positions.is_contiguous()):
             raise ValueError("qk_norm_rope: positions are contiguous int32 [tokens]")
-    outs = []
+    if q_out is None:
+        q_out = x.new_empty((tokens, n_q_heads, head_dim))
+    if k_out is None:
+        k_out = x.new_empty((tokens, n_k_heads, head_dim))
     for t, heads in ((q_out, n_q_heads), (k_out, n_k_heads)):
-        if t is None:
-            t = torch.empty((tokens, heads, head_dim), dtype=x.dtype, device=x.device)
-        elif t.dtype != x.dtype or t.shape != (tokens, heads, head_dim) or t.stride(2) != 1:
+        if t.dtype != dt or t.shape != (tokens, heads, head_dim) or t.stride(2) != 1:
             raise ValueError("qk_norm_rope: outputs are [tokens, heads, head_dim] of x's dtype")
-        outs.append(t)
-    q, k = outs
-    st = lib.mxq_qk_norm_rope(_ptr(x), DT_BF16 if x.dtype == torch.bfloat16 else DT_F32, tokens,
+    st = lib.mxq_qk_norm_rope(x.data_ptr(), DT_BF16 if dt == torch.bfloat16 else DT_F32, tokens,
                               x.stride(0), n_q_heads, n_k_heads, head_dim, _ptr(q_weight),
                               _ptr(k_weight), eps, _ptr(cos), _ptr(sin), n_pos, rot,
-                              int(interleaved), _ptr(positions), _ptr(q), q.stride(0), q.stride(1),
-                              _ptr(k), k.stride(0), k.stride(1), _stream(stream))
-    _check("mxq_qk_norm_rope", st)
-    return q, k
+                              int(interleaved), _ptr(positions), q_out.data_ptr(), q_out.stride(0),
+                              q_out.stride(1), k_out.data_ptr(), k_out.stride(0), k_out.stride(1),
+                              _stream(stream))
+    if st != 0:
+        raise MxqError("mxq_qk_norm_rope", st)
+    return q_out, k_out
 
 
 def conv3x3_gemm_mixed(x: QTensor, height: int, width: int, groups: list, w_perm, n_out: int,
