@@ -11,6 +11,13 @@
 // power of two at or above D / 8) take a head, a wave 64 / LPH heads of one
 // token at a time, kHeads times, with all loads issued first; the token's
 // cosines and sines and both gains stay in registers meanwhile.
+//
+// 16384 tokens x (32 + 8) heads x 128 in bf16: 69 us, 5.0 TB/s (a plain copy of a
+// gigabyte runs at 5.2): one wave per workgroup (256 threads 75 us), streaming
+// stores (cached ones 75 us: a sequence's heads are more than the L2s hold),
+// four heads per lane (two 74 us, eight 94 us).  72-wide heads use 9 of 16
+// lanes: 16384 x 32 heads 43 us, 3.6 TB/s (seven heads packed into a wave, with
+// the sum by lane shifts: 41 us, not kept).
 #include "device_common.h"
 #include "gemm_pipe.h"
 #include "kernels.h"
@@ -18,7 +25,7 @@
 namespace mxq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;   // one wave: no wave waits for another
 constexpr int kHeads = 4;   // heads per lane
 
 struct QkParams {
@@ -44,11 +51,29 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, float (&f)[4]) {
 template <int DT>
 __device__ __forceinline__ void store4(void* p, int64_t i, const float (&f)[4]) {
   if constexpr (DT == DT_BF16) {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-        make_uint2(pack_bf16_rne(f[0], f[1]), pack_bf16_rne(f[2], f[3]));
+    typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+    const v2u v = {pack_bf16_rne(f[0], f[1]), pack_bf16_rne(f[2], f[3])};
+    __builtin_nontemporal_store(v, reinterpret_cast<v2u*>(static_cast<uint16_t*>(p) + i));
   } else {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
   }
+}
+
+// 8 consecutive bf16 elements in one access.
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&f)[2][4]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[e >> 1][2 * (e & 1)] = __uint_as_float(d[e] << 16);
+    f[e >> 1][2 * (e & 1) + 1] = __uint_as_float(d[e] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[2][4]) {
+  const v4u v = {pack_bf16_rne(f[0][0], f[0][1]), pack_bf16_rne(f[0][2], f[0][3]),
+                 pack_bf16_rne(f[1][0], f[1][1]), pack_bf16_rne(f[1][2], f[1][3])};
+  __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(static_cast<uint16_t*>(p) + i));
 }
 
 template <int LPH>
@@ -85,8 +110,12 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkParams p) {
     for (int e = 0; e < 4; ++e) x[i][0][e] = x[i][1][e] = 0.f;
     if (act && h < heads) {
       const int64_t at = tok * a.ldx + (int64_t)h * D;
-      load4<DT>(a.x, at + lo, x[i][0]);
-      load4<DT>(a.x, at + hi, x[i][1]);
+      if constexpr (INTER && DT == DT_BF16) {
+        load8(a.x, at + lo, x[i]);
+      } else {
+        load4<DT>(a.x, at + lo, x[i][0]);
+        load4<DT>(a.x, at + hi, x[i][1]);
+      }
     }
   }
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -146,8 +175,12 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkParams p) {
       void* out = is_q ? a.q : a.k;
       const int64_t at = is_q ? tok * a.q_token + (int64_t)h * a.q_head
                               : tok * a.k_token + (int64_t)(h - a.n_q) * a.k_head;
-      store4<DT>(out, at + lo, o[0]);
-      store4<DT>(out, at + hi, o[1]);
+      if constexpr (INTER && DT == DT_BF16) {
+        store8(out, at + lo, o);
+      } else {
+        store4<DT>(out, at + lo, o[0]);
+        store4<DT>(out, at + hi, o[1]);
+      }
     }
   }
 }
