@@ -6,18 +6,23 @@
 //
 // decided on the exact real quotient like every other format (s = 0 gives
 // q = 0).  The quotient is formed as t = r * (1 / s): both roundings move it
-// by less than 2**-16, so RNE(t) is RNE(r / s) unless t lies that close to a
-// half-integer.  A lane keeps its smallest distance to one, and only lanes
-// inside the window (a few in 10000) redo their values with the float64
-// quotient, which is exact enough to decide every case (r / s differs from a
-// half-integer by 2**-25 at least, or is one).
+// by less than 2**-16, so q = RNE(t) is RNE(r / s) unless t lies that close to
+// a half-integer.  A lane keeps its smallest distance to one, and only lanes
+// inside the window (one in 2000) look at the remainder r - q s: near a tie it
+// is exact in fp32 (a multiple of the smaller of r's and s's last places, and
+// at most about s / 2), so comparing it with s / 2 decides.  Deciding there by
+// float64 quotients instead cost a fifth of the kernel: 25% of the waves hold
+// such a lane.  Scales below 2**-120, whose reciprocal nears overflow, take
+// float64 quotients (r / s is 2**-25 away from a half-integer at least, or is one).
 //
 // Bound by memory: 2 (bf16) or 4 (fp32) bytes read and one written per
 // element.  A row is held in registers between the amax and the encoding, so
-// x is read once (rows of up to 16384 columns; longer rows are read twice).
-// A lane takes 8 consecutive elements at a time, so a wave's load is one
-// contiguous kilobyte of bf16; a row belongs to one wave when there are rows
-// enough to fill the GPU, else to the four waves of a workgroup.
+// x is read once (rows of up to 32768 columns, 16384 rotated; longer rows are
+// read twice).  A lane takes 8 consecutive elements at a time, so a wave's load
+// is one contiguous kilobyte of bf16; a row belongs to one wave up to 2048
+// columns, else to the four waves of a workgroup.  16384 x 4608 bf16: 41 us, 5.5
+// TB/s (a plain copy of a gigabyte runs at 5.2), with the 16-point rotation 56
+// us (float64 butterflies); 4096 x 4096 fp32 14 us.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -37,37 +42,38 @@ struct I8Params {
   unsigned* dbg;
 };
 
-// A lane's 8 consecutive values as loaded (bf16 pairs stay packed).
-template <int DT> struct Raw { uint4 v[DT == DT_F32 ? 2 : 1]; };
+// A lane's 8 consecutive values as loaded: two fp32 quads, or one quad of
+// packed bf16 pairs.
+template <int DT> struct Raw { uint4 lo, hi; };
+template <> struct Raw<DT_BF16> { uint4 lo; };
 
 template <int DT>
-__device__ __forceinline__ void load8(const I8Params& p, int64_t row, int col, Raw<DT>& r) {
-  const bool act = col < p.cols;
+__device__ __forceinline__ Raw<DT> load8(const I8Params& p, int64_t row, int col) {
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
   if constexpr (DT == DT_BF16) {
-    r.v[0] = make_uint4(0, 0, 0, 0);
-    if (act) r.v[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.ldx + col);
+    if (col < p.cols) lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + row * p.ldx + col);
+    return {lo};
   } else {
-    r.v[0] = r.v[1] = make_uint4(0, 0, 0, 0);
-    if (act) {
+    if (col < p.cols) {
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p.x) + row * p.ldx + col);
-      r.v[0] = q[0];
-      r.v[1] = q[1];
+      lo = q[0];
+      hi = q[1];
     }
+    return {lo, hi};
   }
 }
 
 template <int DT>
 __device__ __forceinline__ void unpack8(const Raw<DT>& r, float (&f)[8]) {
   if constexpr (DT == DT_BF16) {
-    const uint32_t d[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+    const uint32_t d[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[2 * i] = __uint_as_float(d[i] << 16);
       f[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
     }
   } else {
-    const uint32_t d[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w,
-                           r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+    const uint32_t d[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(d[i]);
   }
@@ -132,11 +138,19 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv
     u[e] = __float_as_uint(a);
     near = fminf(near, fabsf(fabsf(t - (a - kMagic)) - 0.5f));
   }
-  if (!fast || near < 0x1p-15f) {
+  if (!fast) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double q = s == 0.f ? 0.0 : rint((double)f[e] / (double)s);
       u[e] = (uint32_t)(int)fmin(127.0, fmax(-127.0, q));
+    }
+  } else if (near < 0x1p-15f) {
+    const float h = 0.5f * s;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float r = __builtin_fmaf(-(__uint_as_float(u[e]) - kMagic), s, f[e]);
+      const bool past = fabsf(r) > h || (fabsf(r) == h && (u[e] & 1u));
+      u[e] += past ? (r > 0.f ? 1u : ~0u) : 0u;
     }
   }
   // low bytes of four words into one
@@ -177,8 +191,8 @@ __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(I8Params p) {
     Raw<DT> in[HAD > 0 ? J : 1];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      if constexpr (HAD > 0) load8<DT>(p, row, c0 + j * STEP, in[j]);
-      else load8<DT>(p, row, c0 + j * STEP, raw[j]);
+      if constexpr (HAD > 0) in[j] = load8<DT>(p, row, c0 + j * STEP);
+      else raw[j] = load8<DT>(p, row, c0 + j * STEP);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -196,10 +210,8 @@ __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(I8Params p) {
     }
   } else {
     for (int c = c0; c - lane * 8 < p.cols; c += STEP) {   // whole waves stay in the loop
-      Raw<DT> r;
       float f[8];
-      load8<DT>(p, row, c, r);
-      unpack8<DT>(r, f);
+      unpack8<DT>(load8<DT>(p, row, c), f);
       flag_nonfinite(f, p.dbg);
       if constexpr (HAD > 0) hadamard8<HAD>(f, lane);
       m = fmaxf(m, amax8(f));
@@ -236,10 +248,8 @@ __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(I8Params p) {
     }
   } else {
     for (int c = c0; c - lane * 8 < p.cols; c += STEP) {
-      Raw<DT> r;
       float f[8];
-      load8<DT>(p, row, c, r);
-      unpack8<DT>(r, f);
+      unpack8<DT>(load8<DT>(p, row, c), f);
       if constexpr (HAD > 0) hadamard8<HAD>(f, lane);
       if (c < p.cols) *reinterpret_cast<uint2*>(out + c) = encode8(f, s, inv, fast);
     }
@@ -260,16 +270,24 @@ hipError_t by_pieces(const I8Params& p, hipStream_t s) {
   if (j <= 2) return go<DT, HAD, 2, WPR>(p, s);
   if (j <= 3) return go<DT, HAD, 3, WPR>(p, s);
   if (j <= 4) return go<DT, HAD, 4, WPR>(p, s);
-  if (j <= 6) return go<DT, HAD, 6, WPR>(p, s);
-  if (j <= 8) return go<DT, HAD, 8, WPR>(p, s);
-  if constexpr (WPR == 4) return go<DT, HAD, 0, WPR>(p, s);
-  return hipErrorInvalidValue;
+  if constexpr (WPR > 1) {
+    if (j <= 6) return go<DT, HAD, 6, WPR>(p, s);
+    if (j <= 8) return go<DT, HAD, 8, WPR>(p, s);
+    if constexpr (HAD == 0) {   // rotated rows are held as fp32 values: no registers for more
+      if (j <= 12) return go<DT, HAD, 12, WPR>(p, s);
+      if (j <= 16) return go<DT, HAD, 16, WPR>(p, s);
+    }
+    return go<DT, HAD, 0, WPR>(p, s);
+  }
+  return hipErrorInvalidValue;   // not reached: one wave takes up to 2048 columns
 }
 
 template <int DT, int HAD>
 hipError_t by_rows(const I8Params& p, hipStream_t s) {
-  // a wave per row needs rows for every compute unit's waves
-  if (p.rows >= 2048 && p.cols <= 4096) return by_pieces<DT, HAD, 1>(p, s);
+  // narrow rows leave most of four waves idle (bf16 4096 x 1152 5.8 us with one
+  // wave per row, 10.3 with four), wide ones too few waves per compute unit
+  // (2048 x 4096 10.4 / 7.7)
+  if (p.cols <= 2048) return by_pieces<DT, HAD, 1>(p, s);
   return by_pieces<DT, HAD, 4>(p, s);
 }
 

@@ -32,10 +32,11 @@ def _check_codes(got, vals, tag):
     assert np.array_equal(codes, q), f"{tag}: {np.sum(codes != q)} codes differ"
 
 
-# one wave per row (2048 rows and more, up to 4096 columns: 1 .. 8 pieces), a
-# workgroup per row, and rows too long to hold in registers
+# one wave per row (up to 2048 columns: 1 .. 4 pieces), a workgroup per row (2 ..
+# 16 pieces), and rows too long to hold in registers
 QSHAPES = [(1, 32), (3, 1152), (5, 4128), (1, 8160), (2, 16384), (3, 16416), (2049, 96), (2050, 1152),
-           (2048, 2400), (2051, 4096)]
+           (2048, 2400), (2051, 4096), (7, 640), (6, 2048), (4, 2080), (3, 11264), (2, 24608), (2, 32768),
+           (3, 32800)]
 
 
 @pytest.mark.parametrize("rows,cols", QSHAPES)
@@ -48,7 +49,7 @@ def test_quantize(rows, cols, dtype):
     _check_codes(got, gu.act_values(x, dtype), f"{rows}x{cols}")
 
 
-@pytest.mark.parametrize("rows,cols", [(3, 128), (7, 1152), (2, 16512), (2049, 1536)])
+@pytest.mark.parametrize("rows,cols", [(3, 128), (7, 1152), (2, 16512), (2049, 1536), (5, 512), (3, 3200), (2, 8192), (3, 12288)])
 @pytest.mark.parametrize("had", [16, 32, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_quantize_rotated(rows, cols, had, dtype):
