@@ -186,10 +186,11 @@ __device__ __forceinline__ void dqp_body(const DqpParams& dp) {
 
   int tm, tn, m0;
   if constexpr (GRP) {
-    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TBM);
+    const GroupScan gs(p.goff, p.groups, p.M, TBM);
+    const int tiles_m = gs.tiles();
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, dp.gm, tm, tn);
-    m0 = enter_group(p, TBM, tm);
+    m0 = enter_group(p, gs, tm);
     if (m0 < 0) return;
   } else {
     tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, dp.gm, tm, tn);

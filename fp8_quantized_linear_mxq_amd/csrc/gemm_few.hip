@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
   const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
   int m0 = tm * 16;
   if constexpr (GRP) {
-    m0 = enter_group(p, 16, tm);
+    m0 = enter_group(p, GroupScan(p.goff, p.groups, p.M, 16), tm);
     if (m0 < 0) return;
   }
   const int n0 = tn * 16 * NT;

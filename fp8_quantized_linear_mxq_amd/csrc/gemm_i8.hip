@@ -67,10 +67,11 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring
 
   int tm, tn, m0;
   if constexpr (GRP) {
-    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TB);
+    const GroupScan gs(p.goff, p.groups, p.M, TB);
+    const int tiles_m = gs.tiles();
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
-    m0 = enter_group(p, TB, tm);
+    m0 = enter_group(p, gs, tm);
     if (m0 < 0) return;
   } else {
     tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, gm, tm, tn);

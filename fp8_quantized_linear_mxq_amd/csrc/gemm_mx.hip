@@ -74,10 +74,11 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
 
   int tm, tn, m0;
   if constexpr (GRP) {   // rows grouped by expert: the tile's group, then as one product
-    const int tiles_m = group_tiles(p.goff, p.groups, p.M, TBM);
+    const GroupScan gs(p.goff, p.groups, p.M, TBM);
+    const int tiles_m = gs.tiles();
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
-    m0 = enter_group(p, TBM, tm);
+    m0 = enter_group(p, gs, tm);
     if (m0 < 0) return;
   } else {
     tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, gm, tm, tn);

@@ -41,50 +41,62 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive sum
   return v;
 }
 
-// All row tiles of `rows` rows.  Every lane of the wave takes part.
-__device__ __forceinline__ int group_tiles(const int32_t* off, int groups, int M, int rows) {
-  const int lane = threadIdx.x & 63;
-  int total = 0;
-  for (int c = 0; c < groups; c += 64) {
-    int o0;
-    const int n = group_rows(off, groups, M, c + lane, o0);
-    total += __shfl(wave_scan((n + rows - 1) / rows, lane), 63);
-  }
-  return __builtin_amdgcn_readfirstlane(total);
-}
+// The row tiles of all groups.  Every lane of the wave takes part; up to 64
+// groups are loaded and scanned once.
+struct GroupScan {
+  const int32_t* off;
+  int groups, M, rows;
+  int o0, n, upto;   // of group `lane` of the first 64: first row, rows, tiles up to its end
 
-// The group and rows of tile t (tiles of a group are consecutive); false when
-// there are fewer tiles.
-__device__ __forceinline__ bool group_tile(const int32_t* off, int groups, int M, int rows, int t,
-                                           GroupTile& out) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int c = 0; c < groups; c += 64) {
-    int o0;
-    const int n = group_rows(off, groups, M, c + lane, o0);
-    const int tiles = (n + rows - 1) / rows;
-    const int upto = before + wave_scan(tiles, lane);
-    const uint64_t past = __ballot(upto > t);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int first = __builtin_amdgcn_readlane(upto - tiles, l);
-      const int start = __builtin_amdgcn_readlane(o0, l), len = __builtin_amdgcn_readlane(n, l);
-      out.g = c + l;
-      out.row0 = start + (t - first) * rows;
-      out.row1 = start + len;
-      return true;
-    }
-    before = __builtin_amdgcn_readlane(upto, 63);
+  __device__ __forceinline__ GroupScan(const int32_t* off_, int groups_, int M_, int rows_)
+      : off(off_), groups(groups_), M(M_), rows(rows_) {
+    const int lane = threadIdx.x & 63;
+    n = group_rows(off, groups, M, lane, o0);
+    upto = wave_scan((n + rows - 1) / rows, lane);
   }
-  return false;
-}
+
+  __device__ __forceinline__ int tiles() const {
+    const int lane = threadIdx.x & 63;
+    int total = __builtin_amdgcn_readlane(upto, 63);
+    for (int c = 64; c < groups; c += 64) {
+      int o;
+      const int m = group_rows(off, groups, M, c + lane, o);
+      total += __builtin_amdgcn_readlane(wave_scan((m + rows - 1) / rows, lane), 63);
+    }
+    return total;
+  }
+
+  // The group and rows of tile t (tiles of a group are consecutive); false
+  // when there are fewer tiles.
+  __device__ __forceinline__ bool find(int t, GroupTile& out) const {
+    const int lane = threadIdx.x & 63;
+    int o = o0, m = n, up = upto;
+    for (int c = 0;;) {
+      const uint64_t past = __ballot(up > t);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        const int len = __builtin_amdgcn_readlane(m, l);
+        const int first = __builtin_amdgcn_readlane(up, l) - (len + rows - 1) / rows;
+        out.g = c + l;
+        out.row0 = __builtin_amdgcn_readlane(o, l) + (t - first) * rows;
+        out.row1 = __builtin_amdgcn_readlane(o, l) + len;
+        return true;
+      }
+      c += 64;
+      if (c >= groups) return false;
+      const int before = __builtin_amdgcn_readlane(up, 63);
+      m = group_rows(off, groups, M, c + lane, o);
+      up = before + wave_scan((m + rows - 1) / rows, lane);
+    }
+  }
+};
 
 // Turns the parameters of a grouped product into those of the one product
 // that row tile t belongs to: rows up to the group's end, the group's weights
 // and bias.  Returns the tile's first row, or -1 when there is no tile t.
-__device__ __forceinline__ int enter_group(GemmP& p, int rows, int t) {
+__device__ __forceinline__ int enter_group(GemmP& p, const GroupScan& s, int t) {
   GroupTile gt;
-  if (!group_tile(p.goff, p.groups, p.M, rows, t, gt)) return -1;
+  if (!s.find(t, gt)) return -1;
   p.M = gt.row1;
   const int64_t first = (int64_t)gt.g * p.N;
   p.w += first * p.ldw;

@@ -77,7 +77,8 @@ SIZES = [
     ([1], 40, 128), ([0, 0, 1, 0], 33, 256), ([1] * 8, 64, 384), ([0, 5, 0, 0, 16, 17, 1], 130, 256),
     ([33, 0, 31, 0], 129, 640), ([0, 0, 200, 0], 96, 128), ([40] * 5, 250, 512),
     ([127, 128, 129, 0, 1, 255, 300], 264, 256), ([600, 2, 0, 700], 300, 384), ([3, 0] * 70, 24, 128),
-    ([0] * 66 + [9, 150, 61], 48, 256), ([1000, 1500], 520, 4224),
+    ([0] * 66 + [9, 150, 61], 48, 256), ([300] * 3 + [0] * 61 + [200, 0, 0, 77], 72, 128),
+    ([5] * 64, 40, 128), ([5] * 65, 40, 128), ([1000, 1500], 520, 4224),
 ]
 
 
