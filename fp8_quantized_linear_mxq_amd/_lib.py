@@ -1,4 +1,6 @@
-"""ctypes binding of libmxq (include/mxq.h).
+"""Binding of libmxq (include/mxq.h): ctypes, and for the calls that a model
+makes in every layer (quantize, gemm, gemm_grouped, qk_norm_rope) the
+marshalling module built from csrc/torch_binding.cpp.
 
 Argument marshalling only: every step of the layer runs inside libmxq's HIP
 kernels.  PyTorch supplies device memory and the current stream.  If the
@@ -8,7 +10,6 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct
 from dataclasses import dataclass
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -49,17 +50,14 @@ class QTensorC(C.Structure):
                 ("tensor_scale", C.c_void_p)]
 
 
-# The same layout as bytes: a read-only operand is passed as one of these (a
-# tenth of the time of building the Structure).
-_QTENSOR = struct.Struct("iiqqQqQqQ")
-
 _lib = None
 _torch = None   # the torch module, bound by load(): an import statement costs 0.2 us a call
+_fast = None    # the marshalling module
 
 
 def load():
     """Load libmxq.so (built in-tree by ``build.py``); raises if absent."""
-    global _lib, _torch
+    global _lib, _torch, _fast
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -110,12 +108,15 @@ def load():
     lib.mxq_status_string.restype = C.c_char_p
     lib.mxq_version.argtypes = []
     lib.mxq_version.restype = i32
-    # entry points whose operands the binding passes as bytes
-    b = C.c_char_p
-    lib.gemm = C.CFUNCTYPE(i32, b, b, vp, vp, i64, vp, i32, vp, vp, i64, i64, vp, sz, vp)(("mxq_gemm", lib))
-    lib.gemm_grouped = C.CFUNCTYPE(i32, b, b, i32, vp, vp, vp, i64, vp)(("mxq_gemm_grouped", lib))
-    lib.quantize = C.CFUNCTYPE(i32, vp, i32, i64, i64, i64, i32, vp, vp, i32, vp, i64, b, vp, sz,
-                               vp)(("mxq_quantize", lib))
+    if _torch is not None:
+        try:
+            from . import _torch_binding
+        except ImportError as e:
+            raise RuntimeError("the torch marshalling module is not built for this Python and torch; run "
+                               "python -m fp8_quantized_linear_mxq_amd.build") from e
+        _torch_binding.bind(*[C.cast(f, vp).value for f in (lib.mxq_quantize, lib.mxq_gemm,
+                                                            lib.mxq_gemm_grouped, lib.mxq_qk_norm_rope)])
+        _fast = _torch_binding
     _lib = lib
     return lib
 
@@ -131,12 +132,12 @@ def _ptr(t):
 
 def _stream(stream):
     """The given stream's handle, or the current device's current stream (read
-    as a handle: building the Stream object takes 3 us of a small call's 12)."""
+    as a handle: building the Stream object takes 3 us)."""
     if stream is not None:
         return stream.cuda_stream
     if _torch.cuda.is_initialized():
         return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
-    return _torch.cuda.current_stream().cuda_stream
+    return _torch.cuda.current_stream().cuda_stream if _torch.cuda.is_available() else 0
 
 
 def storage(fmt: int, cols: int):
@@ -177,29 +178,17 @@ class QTensor:
                         scales.stride(0) * scales.element_size() if scales is not None else 0,
                         ts.data_ptr() if ts is not None else None)
 
-    def packed(self) -> bytes:
-        """c() as bytes, for the entry points that only read the operand."""
-        codes, scales, ts = self.codes, self.scales, self.tensor_scale
-        return _QTENSOR.pack(self.fmt, 0, self.rows, self.cols,
-                             0 if codes is None else codes.data_ptr(),
-                             0 if codes is None else codes.stride(0) * codes.element_size(),
-                             0 if scales is None else scales.data_ptr(),
-                             0 if scales is None else scales.stride(0) * scales.element_size(),
-                             0 if ts is None else ts.data_ptr())
-
 
 def empty_qtensor(fmt: int, rows: int, cols: int, device="cuda") -> QTensor:
     """Allocates (torch) the buffers of a quantized operand."""
-    load()
-    torch = _torch
-    if fmt == INT8 and cols % 32 == 0:
-        return QTensor(fmt, rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
-                       torch.empty((rows, 1), dtype=torch.float32, device=device))
+    import torch
     cb, sb = storage(fmt, cols)
     # row strides padded to the ABI's alignment (16 B codes; 4 B scales, 16 B
     # for INT4's fp32 scales)
     codes = torch.empty((rows, (cb + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    if fmt == INT4:
+    if fmt == INT8:
+        scales = torch.empty((rows, 1), dtype=torch.float32, device=device)
+    elif fmt == INT4:
         scales = torch.empty((rows, (sb // 4 + 3) // 4 * 4), dtype=torch.float32, device=device)
     else:
         scales = torch.empty((rows, (sb + 3) // 4 * 4), dtype=torch.uint8, device=device)
@@ -248,26 +237,28 @@ def quantize(x, fmt: int, hadamard: int = 0, static_tensor_scale=None, l1t=None,
     ``l1p`` (L1 from pack_l1t) instead of ``l1t``, mxq_quantize_lrp."""
     lib = load()
     torch = _torch
+    if stream is not None and (out is None or workspace is None):
+        with torch.cuda.stream(stream):   # what is allocated here belongs to the stream that writes it
+            return quantize(x, fmt, hadamard, static_tensor_scale, l1t, u, out, workspace, l1p=l1p)
     rows, cols = x.shape
     dt = DT_BF16 if x.dtype == torch.bfloat16 else DT_F32
     if out is None:
-        out = empty_qtensor(fmt, rows, cols, x.device)
+        out = (QTensor(INT8, rows, cols, *_fast.empty_int8(x)) if fmt == INT8 and cols % 32 == 0
+               else empty_qtensor(fmt, rows, cols, x.device))
     if workspace is None:
-        n = workspace_size(OP_QUANTIZE, rows, cols, fmt) if fmt != INT8 else 0
+        n = workspace_size(OP_QUANTIZE, rows, cols, fmt) if fmt == NVFP4 else 0   # the one that needs any
         if n > 0:
             workspace = torch.empty((n,), dtype=torch.uint8, device=x.device)
-    wsp, wsn = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+    wsn = 0 if workspace is None else workspace.numel()
     if l1p is not None:
         qc = out.c()
         st = lib.mxq_quantize_lrp(_ptr(x), dt, rows, cols, x.stride(0), hadamard,
                                   _ptr(static_tensor_scale), _ptr(l1p), l1p.shape[0], _ptr(u),
-                                  0 if u is None else u.stride(0), C.byref(qc), wsp, wsn, _stream(stream))
+                                  0 if u is None else u.stride(0), C.byref(qc), _ptr(workspace), wsn,
+                                  _stream(stream))
         _check("mxq_quantize_lrp", st)
         return out
-    rank = 0 if l1t is None else l1t.shape[0]
-    st = lib.quantize(x.data_ptr(), dt, rows, cols, x.stride(0), hadamard,
-                      _ptr(static_tensor_scale), _ptr(l1t), rank, _ptr(u),
-                      0 if u is None else u.stride(0), out.packed(), wsp, wsn, _stream(stream))
+    st = _fast.quantize(x, dt, hadamard, static_tensor_scale, l1t, u, out, workspace, wsn, _stream(stream))
     if st != 0:
         raise MxqError("mxq_quantize", st)
     return out
@@ -294,18 +285,25 @@ def gemm(a: QTensor, w: QTensor, n_out: int | None = None, w_out_col=None, u=Non
          bias=None, out=None, stream=None, workspace=None):
     """mxq_gemm; returns the bf16 [M, n_out] output tensor.  ``workspace``:
     a device tensor, None (allocated when the route can use one) or False."""
-    lib = load()
-    n_out = w.rows if n_out is None else n_out
-    if out is None:
-        out = a.codes.new_empty((a.rows, n_out), dtype=_torch.bfloat16)
-    rank = 0 if l2t is None else l2t.shape[1]
-    wsp, wsn = (None, 0) if workspace is None and w.fmt != INT4 else _gemm_workspace(a, [w], workspace)
-    st = lib.gemm(a.packed(), w.packed(), _ptr(w_out_col), _ptr(u), 0 if u is None else u.stride(0),
-                  _ptr(l2t), rank, _ptr(bias), out.data_ptr(), out.stride(0), n_out, wsp, wsn,
-                  _stream(stream))
-    if st != 0:
-        raise MxqError("mxq_gemm", st)
-    return out
+    load()
+    if stream is not None and (out is None or workspace is None):
+        with _torch.cuda.stream(stream):
+            return gemm(a, w, n_out, w_out_col, u, l2t, bias, out, workspace=workspace)
+    wsn = 0
+    if workspace is False:
+        workspace = None
+    elif workspace is not None:
+        wsn = workspace.numel() * workspace.element_size()
+    elif w.fmt == INT4:   # the one weight format that can use one
+        wsn = workspace_size(OP_GEMM, a.rows, w.rows, w.fmt)
+        if wsn > 0:
+            workspace = _torch.empty((wsn,), dtype=_torch.uint8, device=a.codes.device)
+        wsn = max(wsn, 0)
+    r = _fast.gemm(a, w, w.rows if n_out is None else n_out, w_out_col, u, l2t, bias, out, workspace, wsn,
+                   _stream(stream))
+    if type(r) is int:
+        raise MxqError("mxq_gemm", r)
+    return r
 
 
 def gemm_mixed(a: QTensor, groups: list, w_perm, n_out: int, u=None, l2t=None, bias=None,
@@ -331,17 +329,14 @@ def gemm_grouped(a: QTensor, w: QTensor, offsets, bias=None, out=None, stream=No
     cuda, [experts + 1]) their groups, ``w`` the experts' weights one after
     the other ([experts * N, K]), ``bias`` bf16 [experts, N]; returns the bf16
     [rows, N] output tensor (rows of no group are left as they are in ``out``)."""
-    lib = load()
-    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
-        raise ValueError("gemm_grouped needs contiguous 1-D int32 offsets")
-    groups = offsets.shape[0] - 1
-    if out is None:
-        out = a.codes.new_empty((a.rows, w.rows // groups if groups > 0 else 0), dtype=_torch.bfloat16)
-    st = lib.gemm_grouped(a.packed(), w.packed(), groups, offsets.data_ptr(), _ptr(bias), out.data_ptr(),
-                          out.stride(0), _stream(stream))
-    if st != 0:
-        raise MxqError("mxq_gemm_grouped", st)
-    return out
+    load()
+    if stream is not None and out is None:
+        with _torch.cuda.stream(stream):
+            return gemm_grouped(a, w, offsets, bias)
+    r = _fast.gemm_grouped(a, w, offsets, bias, out, _stream(stream))
+    if type(r) is int:
+        raise MxqError("mxq_gemm_grouped", r)
+    return r
 
 
 def qk_norm_rope(x, n_q_heads: int, n_k_heads: int, head_dim: int, q_weight=None, k_weight=None,
@@ -352,43 +347,16 @@ def qk_norm_rope(x, n_q_heads: int, n_k_heads: int, head_dim: int, q_weight=None
     rotation given by the float32 tables ``cos`` and ``sin`` [n_pos, rot/2].
     Returns (q [tokens, n_q_heads, head_dim], k [tokens, n_k_heads, head_dim]);
     ``q_out`` and ``k_out`` may be given with any token and head strides."""
-    lib = load()
-    torch = _torch
-    dt = x.dtype
-    if dt not in (torch.bfloat16, torch.float32) or x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("qk_norm_rope needs a row-major 2-D float32 or bfloat16 tensor")
-    tokens, width = x.shape
-    if width < (n_q_heads + n_k_heads) * head_dim:
-        raise ValueError("qk_norm_rope: x is narrower than its heads")
-    for g in (q_weight, k_weight):
-        if g is not None and (g.dtype != dt or g.shape != (head_dim,) or g.stride(0) != 1):
-            raise ValueError("qk_norm_rope: weights are contiguous [head_dim] tensors of x's dtype")
-    rot = n_pos = 0
-    if cos is not None:
-        shape = cos.shape
-        if (sin is None or cos.dtype != torch.float32 or sin.dtype != torch.float32 or len(shape) != 2
-                or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous()):
-            raise ValueError("qk_norm_rope: cos and sin are contiguous float32 [n_pos, rot / 2]")
-        n_pos, rot = shape[0], 2 * shape[1]
-        if positions is not None and (positions.dtype != torch.int32 or positions.shape != (tokens,)
-                                      or not positions.is_contiguous()):
-            raise ValueError("qk_norm_rope: positions are contiguous int32 [tokens]")
-    if q_out is None:
-        q_out = x.new_empty((tokens, n_q_heads, head_dim))
-    if k_out is None:
-        k_out = x.new_empty((tokens, n_k_heads, head_dim))
-    for t, heads in ((q_out, n_q_heads), (k_out, n_k_heads)):
-        if t.dtype != dt or t.shape != (tokens, heads, head_dim) or t.stride(2) != 1:
-            raise ValueError("qk_norm_rope: outputs are [tokens, heads, head_dim] of x's dtype")
-    st = lib.mxq_qk_norm_rope(x.data_ptr(), DT_BF16 if dt == torch.bfloat16 else DT_F32, tokens,
-                              x.stride(0), n_q_heads, n_k_heads, head_dim, _ptr(q_weight),
-                              _ptr(k_weight), eps, _ptr(cos), _ptr(sin), n_pos, rot,
-                              int(interleaved), _ptr(positions), q_out.data_ptr(), q_out.stride(0),
-                              q_out.stride(1), k_out.data_ptr(), k_out.stride(0), k_out.stride(1),
-                              _stream(stream))
-    if st != 0:
-        raise MxqError("mxq_qk_norm_rope", st)
-    return q_out, k_out
+    load()
+    if stream is not None and (q_out is None or k_out is None):
+        with _torch.cuda.stream(stream):
+            return qk_norm_rope(x, n_q_heads, n_k_heads, head_dim, q_weight, k_weight, cos, sin, positions,
+                                eps, interleaved, q_out, k_out)
+    r = _fast.qk_norm_rope(x, n_q_heads, n_k_heads, head_dim, q_weight, k_weight, cos, sin, positions,
+                           eps, int(interleaved), q_out, k_out, _stream(stream))
+    if type(r) is int:
+        raise MxqError("mxq_qk_norm_rope", r)
+    return r
 
 
 def conv3x3_gemm_mixed(x: QTensor, height: int, width: int, groups: list, w_perm, n_out: int,

@@ -1,5 +1,5 @@
 """Build libmxq.so (and the matrix-core probe library) in-tree with hipcc
-for gfx950.
+for gfx950, and the torch marshalling module with the host compiler.
 
 Usage: python -m fp8_quantized_linear_mxq_amd.build  (or build() from Python).
 Objects go to _build/ at the repository root; the shared library is written
@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +25,8 @@ SOURCES = ["api.cpp", "quantize.hip", "lowrank.hip", "gemm_mx.hip", "gemm_dq.hip
            "mse.hip", "lowrank_split.hip", "quantize_i8.hip", "gemm_i8.hip", "gemm_few.hip",
            "qk_norm.hip"]
 ARCH = "gfx950"
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING_LIB = os.path.join(PKG, "_torch_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def hipcc() -> str:
@@ -50,10 +53,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """The Python module that marshals torch tensors (host code only)."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{i}" for i in inc), BINDING_SRC,
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -68,7 +90,7 @@ def build(verbose: bool = True) -> str:
         raise RuntimeError(f"probe build failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PROBE_LIB)
     if verbose:
-        print(f"built {LIB} and {PROBE_LIB}")
+        print(f"built {LIB}, {BINDING_LIB} and {PROBE_LIB}")
     return LIB
 
 
