@@ -15,6 +15,11 @@
 // in four runs of 8; both operands permute K alike).  Waves take pairs of
 // steps in turn, so each reads whole 128-byte lines.  Rows past the end of an
 // operand re-read its last row and are never stored.
+//
+// One token, weights from HBM: int8 1152 -> 4608 in 4.6 us (5.3 MB, and 2.6 us
+// of that is an empty launch), 2048 -> 1536 on 8 of 64 experts in 8.3 us (25 MB,
+// 3.0 TB/s): every wave's loads are in flight at once, and what is left is
+// starting the workgroups and one round trip to memory.
 #include "device_common.h"
 #include "gemm_common.h"
 #include "gemm_pipe.h"

@@ -86,7 +86,8 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring
 
   // Load t of a wave covers rows 8 (4t + wave) + lane / 8; the lane's chunk of
   // its row is the same for every t.  Offsets from the tile's first row stay
-  // within 32 bits (row strides are at most 2**24, checked by the host); rows past the end re-read the last.
+  // within 32 bits (row strides are at most 2**24, checked by the host); rows
+  // past the end re-read the last.
   const int lr = 8 * wave + (lane >> 3);
   const int lc = ((lane & 7) ^ swz<CH>(lr)) * 16;
   uint32_t va[LD], vw[LD];

@@ -77,6 +77,7 @@ struct GroupScan {
         const int l = __builtin_ctzll(past);
         const int len = __builtin_amdgcn_readlane(m, l);
         const int first = __builtin_amdgcn_readlane(up, l) - (len + rows - 1) / rows;
+        if (t < first) return false;   // only where unsorted offsets make the sum overflow
         out.g = c + l;
         out.row0 = __builtin_amdgcn_readlane(o, l) + (t - first) * rows;
         out.row1 = __builtin_amdgcn_readlane(o, l) + len;

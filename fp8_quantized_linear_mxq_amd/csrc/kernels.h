@@ -42,12 +42,12 @@ struct QuantizeArgs {
   bool nv_two_pass;                 // dynamic NVFP4: skip the one-pass kernel
 };
 
-// INT8 rows (one scale per row); scales of ld_scales bytes between rows.
-hipError_t launch_quantize_i8(const QuantizeArgs& a, hipStream_t s);
-
 constexpr int kAmaxPartials = 1024;  // NVFP4 phase-1 grid (workspace floats)
 
 hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
+
+// The same for FMT_INT8: one fp32 scale per row, rows ld_scales bytes apart.
+hipError_t launch_quantize_i8(const QuantizeArgs& a, hipStream_t s);
 
 // Device address and size of the current device's scratch array for the
 // allocation-free quantize (the NVFP4 amax partials).
@@ -83,6 +83,7 @@ struct GemmArgs {
   const int32_t* goff;
   int64_t groups;
 };
+// INT8 x INT8, plain or grouped.
 hipError_t launch_gemm_i8(const GemmArgs& a, hipStream_t s);
 // Products with few rows (or few per group): INT8 x INT8, MXFP4 x MXFP4 and
 // bf16 x MXFP4; see few_rows().

@@ -10,6 +10,9 @@
  *        fp32 accumulation, optional rank-r bf16 branch, bf16 out (mxq_gemm)
  *   plus the weight-side per-output-channel format choice        (mxq_select_format)
  *   and the timestep-bucket activation-format lookup             (mxq_act_format_for_step)
+ * and, next to it, the 8-bit integer layer (the same two entry points with
+ * MXQ_FMT_INT8), products grouped by expert (mxq_gemm_grouped) and the norms of
+ * query and key heads with the position rotation (mxq_qk_norm_rope).
  *
  * Sources (pages the method is described on, cited by title and section):
  *  - "Bridging the Gap Between Promise and Performance for Microscaling FP4
@@ -204,8 +207,8 @@ mxq_status mxq_pack_l1t(const void* l1t, int32_t rank, int64_t cols, void* l1p, 
  * unpacked L1^T); the projection's factor reads are whole contiguous
  * kilobytes.  It takes the fused quantize + projection path only: lr_rank a
  * multiple of 16 in [16, 128] (0 is MXQ_ERR_INVALID_ARG), bf16 x and
- * hadamard_n 0 (else MXQ_ERR_UNSUPPORTED; so is MXQ_FMT_INT8), cols a multiple of 128 (else
- * MXQ_ERR_SHAPE); like the other low-rank conditions these are checked for
+ * hadamard_n 0 (else MXQ_ERR_UNSUPPORTED; so is MXQ_FMT_INT8), cols a multiple
+ * of 128 (else MXQ_ERR_SHAPE); like the other low-rank conditions these are checked for
  * non-empty inputs.  Other arguments, workspace and errors as mxq_quantize.
  */
 mxq_status mxq_quantize_lrp(const void* x, int32_t dtype, int64_t rows, int64_t cols,
@@ -323,7 +326,8 @@ mxq_status mxq_gemm_mixed(const mxq_qtensor* a, const mxq_qtensor* w_groups, int
  *              access outside the operands.
  *  bias        optional device bf16 [n_groups][N].
  *  out         device bf16 [M][ld_out], N columns; 2-byte aligned.
- * K and row strides as in mxq_gemm, K not 0.  M = 0 or N = 0 is a no-op.  Error bound as in mxq_gemm.
+ * K and row strides as in mxq_gemm, K not 0.  M = 0 or N = 0 is a no-op.
+ * Error bound as in mxq_gemm.
  * The kernel is chosen by M / n_groups (few rows per expert: one that streams
  * the weights of the experts hit), never by what offsets holds.
  */
