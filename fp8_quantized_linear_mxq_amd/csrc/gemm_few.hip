@@ -1,6 +1,6 @@
-// Products with few rows of activations (single tokens, small batches; in a
-// product grouped by expert, few rows per group): INT8 x INT8, and grouped by
-// expert also MXFP4 x MXFP4 and bf16 x MXFP4.
+// Small products (single tokens, small batches, few outputs; in a product
+// grouped by expert, few rows per group): INT8 x INT8, and grouped by expert also
+// MXFP4 x MXFP4 and bf16 x MXFP4.
 //
 // Such a product is bound by reading W once, so nothing is staged: every lane
 // loads its 16-byte pieces of the weight rows straight into the registers the
@@ -187,27 +187,33 @@ hipError_t go(GemmP p, hipStream_t s) {
 
 }  // namespace
 
-// Where this kernel is the faster one, against the tiled kernels.  A plain
-// product: up to 16 rows (int8 16 x 4096 x 4096 7.3 us against 8.9, 32 rows 9.2 /
-// 8.8).  By expert, weights from HBM: int8 up to four rows per group on average
-// (64 groups, N = 1536, K = 2048: 8 rows 8.1 / 10.7, 128 rows 35 / 42, 512 rows 52
-// / 45); 4-bit weights while the experts hit have too few 64-row pieces of
-// weights to fill the GPU with tiles (N = 2048, K = 4096, 4 / 8 / 14 experts:
-// MXFP4 7.6 / 11.4 / 18.7 us against 10.2 / 12.3 / 15.5, bf16 x MXFP4 9.4 / 13.7 /
-// 23.0 against 19.6 / 19.2 / 20.2).
+// Where this kernel is the faster one, against the tiled kernels, operands
+// from HBM: up to 16 rows (int8 16 x 4096 x 4096 7.3 us against 8.9), and wherever
+// the workgroups fit the GPU about once (int8, K = 1152 / 4096: 64 x 1024 4.1 / 7.8
+// us against 5.5 / 12.9, 128 x 1024 4.7 / 9.6 against 5.6 / 12.6 with two weight
+// tiles, 256 x 1024 6.2 / 13.8 against 5.7 / 12.1; the low-rank branch is one
+// output at a time here, so it stays with few rows).  By expert: int8 also up to
+// four rows per group on average, where the weights' traffic decides (64 groups, N
+// = 1536, K = 2048: 8 rows 8.1 / 10.7, 128 rows 35 / 42, 512 rows 52 / 45); 4-bit
+// weights up to 768 tiles of 16 x 16 (K = 4096, N = 2048, one row each for 4 / 8 / 14
+// experts: MXFP4 7.6 / 11.4 / 18.7 us against 10.2 / 12.3 / 15.5, bf16 x MXFP4 9.4 /
+// 13.7 / 23.0 against 19.6 / 19.2 / 20.2; 264 rows, 4 experts, N = 387, K = 2176: bf16 x
+// MXFP4 8.4 against 17.6).
 bool few_rows(const GemmArgs& a) {
-  if (!a.goff) return a.M <= 16;
-  if (a.a_fmt == FMT_INT8) return a.M <= 4 * a.groups;
-  const int64_t hit = a.M < a.groups ? a.M : a.groups, pieces = hit * ((a.N + 63) / 64);
-  return a.M <= 16 * a.groups && pieces < (a.a_fmt == FMT_MXFP4 ? 320 : 384);
+  const double tiles = gemm_tiles(a, 16, 16);
+  if (a.goff && a.a_fmt != FMT_INT8) return tiles <= 768;
+  if (a.goff ? a.M <= 4 * a.groups : a.M <= 16) return true;
+  return a.rank == 0 && tiles <= 512;
 }
 
 hipError_t launch_gemm_few(const GemmArgs& a, hipStream_t s) {
   const GemmP p = gemm_params(a);
-  if (!a.goff) return go<P_I8, 1, false>(p, s);
-  if (a.a_fmt == FMT_INT8) return go<P_I8, 1, true>(p, s);
   if (a.a_fmt == FMT_MXFP4) return go<P_MX4, 2, true>(p, s);
-  return go<P_BF4, 2, true>(p, s);
+  if (a.a_fmt != FMT_INT8) return go<P_BF4, 2, true>(p, s);
+  // int8: one weight tile per workgroup where that fits the GPU once, or rows are few
+  const bool two = !(a.goff ? a.M <= 4 * a.groups : a.M <= 16) && gemm_tiles(a, 16, 16) > 256;
+  if (a.goff) return two ? go<P_I8, 2, true>(p, s) : go<P_I8, 1, true>(p, s);
+  return two ? go<P_I8, 2, false>(p, s) : go<P_I8, 1, false>(p, s);
 }
 
 }  // namespace mxq

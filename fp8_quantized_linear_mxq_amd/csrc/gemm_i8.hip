@@ -57,12 +57,21 @@ constexpr int KS = BK / 32;       // MFMA K-steps per K-tile
 // K-tiles, so every read is visibly independent of the loads in flight and the
 // compiler adds no wait; the K-tiles left over follow it in line (leaving the
 // loop from its middle instead costs 80 spilled registers).
-template <int T, bool LR, bool GRP>
-__global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring_kernel(GemmP p, int gm) {
+//
+// DEEP (T = 1): for grids that leave a compute unit one or two workgroups, so
+// that nothing else hides the way from memory.  kStages stages of whole K-tiles,
+// all but one of them on their way, and a K-tile's fragments read into registers
+// at once under the MFMAs of the one before.  512 x 2048 x 4096 with operands
+// from HBM 21.9 -> 12.5 us, 1024 x 2048 x 4096 (two workgroups) 22.9 -> 19.8; eight
+// stages 12.6 and 23.1, T = 2 with five 22.9 and 23.0.
+template <int T, bool LR, bool GRP, bool DEEP = false>
+__global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 || DEEP ? 2 : 4) void gemm_i8_ring_kernel(GemmP p, int gm) {
   constexpr int TB = 64 * T, HB = 32 * T;   // workgroup and wave tile
   constexpr int LD = TB * CH / 64 / 4;      // loads per wave per slot
   constexpr int kSlot = TB * RB;
-  __shared__ __attribute__((aligned(16))) uint8_t s0[kSlot], s1[kSlot], s2[kSlot], s3[kSlot], s4[kSlot];
+  constexpr int kStages = 4;
+  constexpr int kBuf = DEEP ? 2 * kSlot : kSlot;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[kBuf], s1[kBuf], s2[kBuf], s3[kBuf], s4[kSlot];
   uint8_t* const slots[5] = {s0, s1, s2, s3, s4};
 
   int tm, tn, m0;
@@ -135,7 +144,8 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring
   for (int i = 0; i < T; ++i)
 #pragma unroll
     for (int j = 0; j < T; ++j) acc[i][j] = v16i{};
-  v4i fa[2][T], fw[2][T];
+  constexpr int NF = DEEP ? 2 * KS : 2;   // fragment buffers
+  v4i fa[NF][T], fw[NF][T];
   auto read = [&](const uint8_t* A, const uint8_t* W, int s, int b) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < T; ++i) {
@@ -196,42 +206,96 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  issue(abase, va, 0, s0);
-  issue(wbase, vw, 0, s1);
-  issue(abase, va, 1, s2);
-  issue(wbase, vw, 1, s3);
-  if (KF > 0) {
-    wait_vmcnt<2 * LD>();
+  if constexpr (DEEP) {
+    uint8_t* const st[kStages] = {s0, s1, s2, s3};
+    auto load = [&](int kt, uint8_t* stage) __attribute__((always_inline)) {
+      issue(abase, va, kt, stage);
+      issue(wbase, vw, kt, stage + kSlot);
+    };
+    auto read_all = [&](const uint8_t* stage, int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) read(stage, stage + kSlot, s, b * KS + s);
+    };
+    // K-tile kt is in registers (buffer I % 2) and its stage is free once every
+    // wave's reads of it are done; K-tile kt+1 has landed
+    auto deep_step = [&](auto stage_of, int kt) __attribute__((always_inline)) {
+      constexpr int I = decltype(stage_of)::value;
+      wait_lgkmcnt0();
+      wait_vmcnt<(kStages - 2) * 2 * LD>();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      read_all(st[(I + 1) % kStages], (I + 1) & 1);
+      load(kt + kStages, st[I]);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) mma((I & 1) * KS + s);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int t = 0; t < kStages; ++t) load(t, st[t]);
+    wait_vmcnt<(kStages - 1) * 2 * LD>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    read(s0, s1, 0, 0);
+    read_all(s0, 0);
     int kt = 0;
-    for (; kt + 5 <= KF; kt += 5) {
-      step(std::integral_constant<int, 0>{}, kt);
-      step(std::integral_constant<int, 1>{}, kt + 1);
-      step(std::integral_constant<int, 2>{}, kt + 2);
-      step(std::integral_constant<int, 3>{}, kt + 3);
-      step(std::integral_constant<int, 4>{}, kt + 4);
+    for (; kt + 4 <= KF; kt += 4) {
+      deep_step(std::integral_constant<int, 0>{}, kt);
+      deep_step(std::integral_constant<int, 1>{}, kt + 1);
+      deep_step(std::integral_constant<int, 2>{}, kt + 2);
+      deep_step(std::integral_constant<int, 3>{}, kt + 3);
     }
-    if (kt < KF) step(std::integral_constant<int, 0>{}, kt);
-    if (kt + 1 < KF) step(std::integral_constant<int, 1>{}, kt + 1);
-    if (kt + 2 < KF) step(std::integral_constant<int, 2>{}, kt + 2);
-    if (kt + 3 < KF) step(std::integral_constant<int, 3>{}, kt + 3);
-  }
-  wait_vmcnt<0>();
-  wait_lgkmcnt0();
-  __syncthreads();
-  if (rest > 0) {   // the K-steps of a last, partial K-tile
-    const int ia = (2 * KF) % 5, iw = (2 * KF + 1) % 5;
-    const uint8_t* A = ia == 0 ? s0 : ia == 1 ? s1 : ia == 2 ? s2 : ia == 3 ? s3 : s4;
-    const uint8_t* W = iw == 0 ? s0 : iw == 1 ? s1 : iw == 2 ? s2 : iw == 3 ? s3 : s4;
+    if (kt < KF) deep_step(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < KF) deep_step(std::integral_constant<int, 1>{}, kt + 1);
+    if (kt + 2 < KF) deep_step(std::integral_constant<int, 2>{}, kt + 2);
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    __syncthreads();
+    // the K-steps of a last, partial K-tile, already in registers
 #pragma unroll
     for (int s = 0; s < KS - 1; ++s)
       if (s < rest) {
-        read(A, W, s, 0);
-        mma(0);
+        if (KF & 1) mma(KS + s);
+        else mma(s);
       }
+  } else {
+    issue(abase, va, 0, s0);
+    issue(wbase, vw, 0, s1);
+    issue(abase, va, 1, s2);
+    issue(wbase, vw, 1, s3);
+    if (KF > 0) {
+      wait_vmcnt<2 * LD>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      read(s0, s1, 0, 0);
+      int kt = 0;
+      for (; kt + 5 <= KF; kt += 5) {
+        step(std::integral_constant<int, 0>{}, kt);
+        step(std::integral_constant<int, 1>{}, kt + 1);
+        step(std::integral_constant<int, 2>{}, kt + 2);
+        step(std::integral_constant<int, 3>{}, kt + 3);
+        step(std::integral_constant<int, 4>{}, kt + 4);
+      }
+      if (kt < KF) step(std::integral_constant<int, 0>{}, kt);
+      if (kt + 1 < KF) step(std::integral_constant<int, 1>{}, kt + 1);
+      if (kt + 2 < KF) step(std::integral_constant<int, 2>{}, kt + 2);
+      if (kt + 3 < KF) step(std::integral_constant<int, 3>{}, kt + 3);
+    }
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
     __syncthreads();
+    if (rest > 0) {   // the K-steps of a last, partial K-tile
+      const int ia = (2 * KF) % 5, iw = (2 * KF + 1) % 5;
+      const uint8_t* A = ia == 0 ? s0 : ia == 1 ? s1 : ia == 2 ? s2 : ia == 3 ? s3 : s4;
+      const uint8_t* W = iw == 0 ? s0 : iw == 1 ? s1 : iw == 2 ? s2 : iw == 3 ? s3 : s4;
+  #pragma unroll
+      for (int s = 0; s < KS - 1; ++s)
+        if (s < rest) {
+          read(A, W, s, 0);
+          mma(0);
+        }
+      __syncthreads();
+    }
   }
 
   // Epilogue: the tile in bf16 through slots 0-3 (64 rows of 512 bytes each,
@@ -312,7 +376,7 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 ? 2 : 4) void gemm_i8_ring
   }
 }
 
-template <int T>
+template <int T, bool DEEP = false>
 hipError_t launch_ring(GemmP p, hipStream_t s) {
   constexpr int TB = 64 * T;
   const bool grp = p.goff != nullptr;
@@ -323,9 +387,9 @@ hipError_t launch_ring(GemmP p, hipStream_t s) {
   int gm = 1;
   while (gm * 2 <= p.tiles_m && (int64_t)gm * 2 * gm * 2 <= (tiles + 7) / 8) gm *= 2;
   const dim3 grid((unsigned)tiles);
-  if (grp) gemm_i8_ring_kernel<T, false, true><<<grid, 256, 0, s>>>(p, gm);
-  else if (p.rank == 0) gemm_i8_ring_kernel<T, false, false><<<grid, 256, 0, s>>>(p, gm);
-  else if constexpr (T < 4) gemm_i8_ring_kernel<T, true, false><<<grid, 256, 0, s>>>(p, gm);
+  if (grp) gemm_i8_ring_kernel<T, false, true, DEEP><<<grid, 256, 0, s>>>(p, gm);
+  else if (p.rank == 0) gemm_i8_ring_kernel<T, false, false, DEEP><<<grid, 256, 0, s>>>(p, gm);
+  else if constexpr (T < 4) gemm_i8_ring_kernel<T, true, false, DEEP><<<grid, 256, 0, s>>>(p, gm);
   else return hipErrorInvalidValue;   // not launched: no registers left for the branch
   return hipGetLastError();
 }
@@ -351,15 +415,15 @@ hipError_t launch_gemm_i8(const GemmArgs& a, hipStream_t s) {
   // the tile sizes trade reuse (a T = 4 tile loads a quarter of the bytes per
   // MFMA of a T = 1 tile) against how many workgroups there are to fill the
   // GPU: 8192^3 2543 / 2154 Top/s with T = 4 / 2, 4096 x 4608 x 1152 46 / 32 /
-  // 42 us, 777 x 1001 x 1184 34 / 10.4 / 6.2 us with T = 4 / 2 / 1.  Groups
-  // leave half a tile empty each, on average.
-  auto tiles = [&](int tb) {
-    const double m = a.groups > 1 ? (double)a.M / tb + 0.5 * std::min<int64_t>(a.groups, a.M)
-                                  : (double)((a.M + tb - 1) / tb);
-    return m * (double)((a.N + tb - 1) / tb);
-  };
-  const double kt = (double)((a.K + BK - 1) / BK);
-  const double c1 = cost<1>(tiles(64), kt), c2 = cost<2>(tiles(128), kt), c4 = cost<4>(tiles(256), kt);
+  // 42 us, 777 x 1001 x 1184 34 / 10.4 / 6.2 us with T = 4 / 2 / 1
+  const double kt = (double)((a.K + BK - 1) / BK), t64 = gemm_tiles(a, 64, 64);
+  // one or two workgroups of T = 1 per compute unit, operands from HBM: DEEP /
+  // T = 1 / T = 2 at 512 x 2048: K = 512 4.6 / 5.0 / 7.4 us, 1152 6.6 / 8.8 / 11.8,
+  // 4096 12.5 / 21.9 / 26.6; at 1024 x 2048: 6.1 / 5.7 / 7.5, 9.0 / 9.2 / 11.5, 19.8 /
+  // 22.8 / 26.7; at 2048 x 2048 (four) 10.0 / 7.7 / 8.0, 13.4 / 11.5 / 11.5, 37 / 37 / 28
+  if (t64 <= 256 || (t64 <= 512 && kt >= 9)) return launch_ring<1, true>(p, s);
+  const double c1 = cost<1>(t64, kt), c2 = cost<2>(gemm_tiles(a, 128, 128), kt),
+               c4 = cost<4>(gemm_tiles(a, 256, 256), kt);
   // T = 4 has no registers left for the low-rank branch
   if (a.rank == 0 && c4 < c2 && c4 < c1) return launch_ring<4>(p, s);
   return c2 < c1 ? launch_ring<2>(p, s) : launch_ring<1>(p, s);

@@ -349,12 +349,15 @@ hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
 hipError_t launch_gemm_mx(const GemmArgs& a, hipStream_t s) {
   const GemmP p = gemm_params(a);
   const bool lr = a.rank > 0;
-  // Rows grouped by expert: the tile by the rows per group, on average (times
-  // for 32 groups, K = 4096, N = 2048, weights from HBM).
-  if (a.goff && a.M <= 16 * a.groups) {
-    // the weights' traffic decides; four workgroups' loads in flight per compute
-    // unit: 64 rows 26.5 us against 31.1 with 128 x 128, 256 rows 30.7 / 32.6,
-    // 1024 rows 44 / 35
+  // Rows grouped by expert (32 groups, K = 4096, N = 2048 where nothing else is
+  // said; operands from HBM).
+  const double t64 = gemm_tiles(a, 64, 64);
+  if (a.goff && (a.M <= 16 * a.groups || t64 <= 768)) {
+    // few rows per group: the weights' traffic decides; four workgroups' loads in
+    // flight per compute unit: 64 rows 26.5 us against 31.1 with 128 x 128, 256 rows
+    // 30.7 / 32.6, 1024 rows 44 / 35.  Or few tiles: 4 groups, N = 1024, 1200 rows (t64
+    // = 336) 14.6 us against 19.2 with 128 x 128 and 29 with 256 x 192, 2000 rows (530)
+    // 16.8 / 19.4 / 30, 4000 rows of K = 2048 (1024) 15.3 / 15.1 / 21
     if (a.K > 4096) return launch_cfg<1, 1, 2, true>(lr, p, s);
     return launch_cfg<1, 1, 2, false>(lr, p, s);
   }
@@ -362,9 +365,10 @@ hipError_t launch_gemm_mx(const GemmArgs& a, hipStream_t s) {
   if (a.goff) {
     // 128 x 128, 256 x 192, 256 x 256: 4096 rows 62 / 69 / 80 us, 8192 rows 91 /
     // 74 / 84, 16384 rows 142 / 133 / 125 (the last pays with 2.5 rounds of tiles,
-    // half of one empty per group)
-    if (a.M < 192 * a.groups) return launch_cfg<2, 2, 2, false>(lr, p, s);
-    const double tiles = ((double)a.M / 256 + 0.5 * (double)a.groups) * (double)((a.N + 255) / 256);
+    // half of one empty per group; 4 groups, N = 1024, 4000 rows: 15 / 21 / 21, with
+    // 72 tiles for 256 compute units)
+    const double tiles = gemm_tiles(a, 256, 256);
+    if (a.M < 192 * a.groups || tiles < 128) return launch_cfg<2, 2, 2, false>(lr, p, s);
     if (tiles >= 2.5 * 256) return launch_cfg<2, 4, 4, false>(lr, p, s);
     return launch_cfg<2, 3, 4, false>(lr, p, s);
   }

@@ -85,6 +85,15 @@ struct GemmArgs {
 };
 // INT8 x INT8, plain or grouped.
 hipError_t launch_gemm_i8(const GemmArgs& a, hipStream_t s);
+
+// Output tiles of tm x tn that a product has; grouped by expert, about: every
+// group with rows leaves half a tile empty.
+inline double gemm_tiles(const GemmArgs& a, int tm, int tn) {
+  const double rows = a.goff && a.groups > 1 ? (double)a.M / tm + 0.5 * (double)(a.M < a.groups ? a.M : a.groups)
+                                             : (double)((a.M + tm - 1) / tm);
+  return rows * (double)((a.N + tn - 1) / tn);
+}
+
 // Products with few rows (or few per group): INT8 x INT8, MXFP4 x MXFP4 and
 // bf16 x MXFP4; see few_rows().
 bool few_rows(const GemmArgs& a);

@@ -166,3 +166,33 @@ def test_grouped_in_a_graph_with_new_offsets():
                 g.replay()
                 torch.cuda.synchronize()
                 assert torch.equal(out, mxq.gemm_grouped(a, w, off))
+
+
+# Each tile shape that the number of tiles selects: (sizes, n, k) from a few
+# 16-row tiles to three rounds of 256 x 256
+TILED = [([70, 0, 30], 100, 160), ([300, 2, 0, 350], 500, 416), ([700, 690, 0, 710], 1000, 288),
+         ([1100, 1000, 0, 900], 1200, 256), ([2100, 30, 1900], 1800, 128), ([7000, 1, 6900], 3000, 128)]
+
+
+@pytest.mark.parametrize("case", range(len(TILED)))
+@pytest.mark.parametrize("pair", PAIRS)
+def test_grouped_tile_shapes(pair, case):
+    """Against float64 products on the device."""
+    import torch
+    import fp8_quantized_linear_mxq_amd as mxq
+    sizes, n, k = TILED[case]
+    if pair != "INT8":
+        k = (k + 127) // 128 * 128
+    rng = np.random.default_rng(900 + case)
+    off = _offsets(sizes)
+    gu.say(f"grouped {pair} sizes {sizes} N={n} K={k}")
+    (a, av), (w, wv) = _acts(rng, pair, int(off[-1]), k), _weights(rng, pair, len(sizes) * n, k)
+    y = mxq.gemm_grouped(a, w, torch.from_numpy(off).cuda())
+    for g in range(len(sizes)):
+        rows = slice(int(off[g]), int(off[g + 1]))
+        ad = torch.from_numpy(av[rows]).cuda()
+        wd = torch.from_numpy(wv[g * n:(g + 1) * n]).cuda().t().contiguous()
+        want = ad @ wd
+        tol = 1e-5 * (1 + 2 ** -8) * (ad.abs() @ wd.abs()) + 2.0 ** -8 * want.abs() + 2.0 ** -133
+        err = (y[rows].double() - want).abs()
+        assert bool((err <= tol).all()), f"group {g}: worst {float((err / tol).max()):.3g}"

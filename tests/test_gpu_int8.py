@@ -266,3 +266,41 @@ def test_layer_on_other_stream_and_in_a_graph():
             torch.cuda.synchronize()
             eager = mxq.gemm(mxq.quantize(x, mxq.INT8), w)
             assert torch.equal(y, eager)
+
+
+# Grids of one or two 64 x 64 tiles per compute unit: every number of K-tiles
+# around the four stages, with and without a partial last one.
+@pytest.mark.parametrize("k", [32, 128, 160, 256, 384, 512, 544, 640, 768, 992, 1024, 1152, 4128])
+def test_gemm_staged_k(k):
+    import fp8_quantized_linear_mxq_amd as mxq
+    m, n = 200, 770
+    gu.say(f"int8 gemm {m}x{n}x{k}")
+    rng = np.random.default_rng(k)
+    (qa, sa), (qw, sw) = _codes(rng, m, k), _codes(rng, n, k)
+    y = mxq.gemm(_operand(qa, sa), _operand(qw, sw))
+    gu.check_gemm(y, o8.dequantize(qa, sa), o8.dequantize(qw, sw), 1.0, tag=f"int8 {m}x{n}x{k}")
+
+
+# small products of more than 16 rows, with one and with two weight tiles per
+# workgroup; 512 and just over 512 tiles of 64 x 64
+@pytest.mark.parametrize("m,n,k", [(100, 500, 288), (100, 900, 1184), (250, 500, 96), (1024, 2048, 1184),
+                                   (1030, 2048, 160), (2000, 1000, 256)])
+def test_gemm_small_and_middle(m, n, k):
+    test_gemm(m, n, k)
+
+
+@pytest.mark.parametrize("m,n", [(60, 90), (1000, 2500)])
+def test_gemm_lowrank_rows_and_tiles(m, n):
+    """The low-rank branch on the staged tiles (one per compute unit) and on
+    those of a larger grid."""
+    import fp8_quantized_linear_mxq_amd as mxq
+    k, r = 160, 16
+    gu.say(f"int8 gemm {m}x{n}x{k} with a rank-{r} branch")
+    rng = np.random.default_rng(m)
+    (qa, sa), (qw, sw) = _codes(rng, m, k), _codes(rng, n, k)
+    u = (rng.standard_normal((m, r)) * 4).astype(np.float32)
+    l2 = wl.bf16_to_f32(wl.f32_to_bf16_bits(rng.normal(0, 0.02, (r, n)).astype(np.float32)))
+    y = mxq.gemm(_operand(qa, sa), _operand(qw, sw), u=gu.to_dev_f32(u),
+                 l2t=gu.to_dev_bf16(wl.f32_to_bf16_bits(np.ascontiguousarray(l2.T))))
+    gu.check_gemm(y, o8.dequantize(qa, sa), o8.dequantize(qw, sw), 1.0, l2=l2, u=u.astype(np.float64),
+                  x=np.abs(u).astype(np.float64), l1=np.eye(r), tag="lowrank")
