@@ -306,7 +306,7 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
   // straddle two waves' columns).
   constexpr int WRS = TBN * 2 + 16;            // LDS bytes per staged row (padded)
   if constexpr ((TBM / 2) * WRS <= STAGE) {
-    if (!p.col_map && (p.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0) {
+    if (!p.col_map) {
       epilogue_wg<TM, TN, WGM, STAGE>(p, acc, m0, n0, wm, wn, lane, st0, st1);
       return;
     }

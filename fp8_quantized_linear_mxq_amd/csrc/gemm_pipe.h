@@ -234,6 +234,31 @@ __device__ __forceinline__ void add_lowrank(const GemmP& p, v16f (&acc)[TI][TN],
   }
 }
 
+// ROWS x COLS staged bf16 values (at(r, c): the LDS address of element c of
+// row r) to output rows that are not 16-byte aligned: THREADS threads store
+// neighbouring pairs, or single elements where the rows are only 2-byte aligned,
+// so that an instruction still writes whole lines (grouped MXFP4, 4025 rows, N =
+// 2030, K = 768: 23.5 us; each lane's quads stored directly 41.8).
+template <int ROWS, int COLS, int THREADS, class F>
+__device__ __forceinline__ void store_rows(const GemmP& p, int row0, int col0, int n_lim, int tid, F at) {
+  if ((p.ld_out & 1) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0) {
+    for (int idx = tid; idx < ROWS * COLS / 2; idx += THREADS) {
+      const int r = idx / (COLS / 2), c = idx % (COLS / 2) * 2, row = row0 + r, n = col0 + c;
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(at(r, c));
+      if (row >= p.M) continue;
+      uint16_t* const o = p.out + (int64_t)row * p.ld_out + n;
+      if (n + 2 <= n_lim) *reinterpret_cast<uint32_t*>(o) = v;
+      else if (n < n_lim) *o = (uint16_t)v;
+    }
+    return;
+  }
+  for (int idx = tid; idx < ROWS * COLS; idx += THREADS) {
+    const int r = idx / COLS, c = idx % COLS, row = row0 + r, n = col0 + c;
+    const uint16_t v = *reinterpret_cast<const uint16_t*>(at(r, c));
+    if (row < p.M && n < n_lim) p.out[(int64_t)row * p.ld_out + n] = v;
+  }
+}
+
 // Epilogue for the transposed accumulator layout: scales by alpha, adds the
 // low-rank branch (LR), the bias, and applies the column map.  `lds_region`
 // (32 * (TN * 64 + 16) bytes private to the wave, or null) enables the
@@ -252,14 +277,13 @@ __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN],
         for (int q = 0; q < 16; ++q) acc[i][j][q] *= alpha;
   }
   if constexpr (LR) add_lowrank<TI, TN>(p, acc, row0, col0, lane);
-  // stores: without a column map and with a 16-byte aligned output, each
-  // 32-row tile goes through the wave's LDS region (row-major) and leaves as
-  // 16-byte pieces of whole rows; otherwise each lane stores its quads
-  // directly (the four columns of a quad are shared by its TI rows, so their
+  // stores: without a column map each 32-row tile goes through the wave's LDS
+  // region (row-major) and leaves as whole rows, in 16-byte pieces where the
+  // output is aligned; otherwise each lane stores its quads directly (the four columns of a quad are shared by its TI rows, so their
   // map entries and bias are fetched once per quad).
   const int n_lim = p.N < p.n_out ? p.N : p.n_out;
-  const bool staged = lds_region && !p.col_map && (p.ld_out & 7) == 0 &&
-                      (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  const bool staged = lds_region && !p.col_map;
+  const bool wide = (p.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
   const bool vec = !p.col_map && (p.ld_out & 3) == 0 &&
                    (reinterpret_cast<uintptr_t>(p.out) & 7) == 0;
   if (staged) {
@@ -282,6 +306,11 @@ __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN],
           pk.y = pack_bf16_rne(v[2], v[3]);
           *reinterpret_cast<uint2*>(lds_region + l32 * RS + (j * 32 + 8 * g + 4 * half) * 2) = pk;
         }
+      if (!wide) {
+        store_rows<32, TN * 32, 64>(p, row0 + i * 32, col0, n_lim, lane,
+                                    [&](int r, int c) { return lds_region + r * RS + c * 2; });
+        continue;
+      }
 #pragma unroll
       for (int t = 0; t < 32 * CPR / 64; ++t) {
         const int idx = t * 64 + lane;
@@ -378,6 +407,12 @@ __device__ __forceinline__ void epilogue_wg(const GemmP& p, v16f (&acc)[TM][TN],
       }
   }
   __syncthreads();
+  if ((p.ld_out & 7) != 0 || (reinterpret_cast<uintptr_t>(p.out) & 15) != 0) {
+    store_rows<TBM, TBN, NT>(p, m0, n0, n_lim, threadIdx.x, [&](int r, int c) {
+      return (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS) + c * 2;
+    });
+    return;
+  }
   for (int idx = threadIdx.x; idx < TBM * CPR; idx += NT) {
     const int r = idx / CPR, ch = idx % CPR;
     const uint8_t* src = (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS) + ch * 16;
