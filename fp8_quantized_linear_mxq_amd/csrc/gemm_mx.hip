@@ -363,14 +363,15 @@ hipError_t launch_gemm_mx(const GemmArgs& a, hipStream_t s) {
   }
   if (a.K > 4096) return launch_cfg<2, 2, 2, true>(lr, p, s);
   if (a.goff) {
-    // 128 x 128, 256 x 192, 256 x 256: 4096 rows 62 / 69 / 80 us, 8192 rows 91 /
-    // 74 / 84, 16384 rows 142 / 133 / 125 (the last pays with 2.5 rounds of tiles,
-    // half of one empty per group; 4 groups, N = 1024, 4000 rows: 15 / 21 / 21, with
-    // 72 tiles for 256 compute units)
-    const double tiles = gemm_tiles(a, 256, 256);
-    if (a.M < 192 * a.groups || tiles < 128) return launch_cfg<2, 2, 2, false>(lr, p, s);
-    if (tiles >= 2.5 * 256) return launch_cfg<2, 4, 4, false>(lr, p, s);
-    return launch_cfg<2, 3, 4, false>(lr, p, s);
+    // The 256-row tiles pay from two rounds of the 256 compute units on; the
+    // 128 x 128 ones run two to a unit and end more evenly.  128 x 128, 256 x 192, 256
+    // x 256: 4096 rows 62 / 69 / 80 us, 8192 rows 91 / 74 / 84, 16384 rows 142 / 133 / 125;
+    // 4 groups: 8000 rows, N = 2048 (two rounds of 256 x 256 just begun) 63 / 63 / 63,
+    // 16384 rows 106 / 101 / 85; 16000 rows, N = 1024 53 / 62 / 62; 4000 rows, K = 1024
+    // 16 / 17 / 17.
+    if (gemm_tiles(a, 256, 256) >= 2 * 256) return launch_cfg<2, 4, 4, false>(lr, p, s);
+    if (a.M >= 192 * a.groups && gemm_tiles(a, 256, 192) >= 2 * 256) return launch_cfg<2, 3, 4, false>(lr, p, s);
+    return launch_cfg<2, 2, 2, false>(lr, p, s);
   }
   // Large tiles move the fewest bytes per MFMA; pick the one whose tile count
   // fills the 256 compute units in the fewest rounds, per unit of tile work.

@@ -238,7 +238,7 @@ __device__ __forceinline__ void add_lowrank(const GemmP& p, v16f (&acc)[TI][TN],
 // row r) to output rows that are not 16-byte aligned: THREADS threads store
 // neighbouring pairs, or single elements where the rows are only 2-byte aligned,
 // so that an instruction still writes whole lines (grouped MXFP4, 4025 rows, N =
-// 2030, K = 768: 23.5 us; each lane's quads stored directly 41.8).
+// 2030, K = 768, 256 x 192 tiles: 23.5 us; each lane's quads stored directly 41.8).
 template <int ROWS, int COLS, int THREADS, class F>
 __device__ __forceinline__ void store_rows(const GemmP& p, int row0, int col0, int n_lim, int tid, F at) {
   if ((p.ld_out & 1) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0) {

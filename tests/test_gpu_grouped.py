@@ -169,9 +169,10 @@ def test_grouped_in_a_graph_with_new_offsets():
 
 
 # Each tile shape that the number of tiles selects: (sizes, n, k) from a few
-# 16-row tiles to three rounds of 256 x 256
+# 16-row tiles to two rounds of 256 x 192 and of 256 x 256
 TILED = [([70, 0, 30], 100, 160), ([300, 2, 0, 350], 500, 416), ([700, 690, 0, 710], 1000, 288),
-         ([1100, 1000, 0, 900], 1200, 256), ([2100, 30, 1900], 1800, 128), ([7000, 1, 6900], 3000, 128)]
+         ([1100, 1000, 0, 900], 1200, 256), ([2100, 30, 1900], 1800, 128), ([7000, 1, 6900], 2000, 128),
+         ([7000, 1, 6900], 3000, 128)]
 
 
 @pytest.mark.parametrize("case", range(len(TILED)))
