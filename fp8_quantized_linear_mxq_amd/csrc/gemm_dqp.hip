@@ -187,7 +187,7 @@ __device__ __forceinline__ void dqp_body(const DqpParams& dp) {
   int tm, tn, m0;
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
-    const int tiles_m = gs.tiles();
+    const int tiles_m = gs.tiles(p.tiles_m);
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, dp.gm, tm, tn);
     m0 = enter_group(p, gs, tm);

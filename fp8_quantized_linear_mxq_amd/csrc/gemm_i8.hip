@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 || DEEP ? 2 : 4) void gemm
   int tm, tn, m0;
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TB);
-    const int tiles_m = gs.tiles();
+    const int tiles_m = gs.tiles(p.tiles_m);
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
     m0 = enter_group(p, gs, tm);

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
   int tm, tn, m0;
   if constexpr (GRP) {   // rows grouped by expert: the tile's group, then as one product
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
-    const int tiles_m = gs.tiles();
+    const int tiles_m = gs.tiles(p.tiles_m);
     if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
     tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
     m0 = enter_group(p, gs, tm);

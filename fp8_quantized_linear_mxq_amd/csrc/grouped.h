@@ -8,7 +8,11 @@
 // load and some 60 instructions next to a product's main loop and spares a
 // launch that builds a table.  Offsets are clamped to [0, M] and a group
 // whose end lies before its start is empty, so offsets that are not sorted
-// give unspecified results but no access outside the operands.
+// give unspecified results but no access outside the operands.  Such offsets can
+// count a row in many groups: the sums are unsigned, which holds the tiles of 64
+// groups (every other one with all of up to 2**30 rows, 16 to a tile) on top of
+// the tiles before them, and a grid never works on more tiles than it was sized
+// for.
 #pragma once
 
 #include "device_common.h"
@@ -32,10 +36,10 @@ __device__ __forceinline__ int group_rows(const int32_t* off, int groups, int M,
   return max(o1 - o0, 0);
 }
 
-__device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive sum
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {   // inclusive sum
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
+    const uint32_t o = __shfl_up(v, d);
     if (lane >= d) v += o;
   }
   return v;
@@ -46,7 +50,8 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive sum
 struct GroupScan {
   const int32_t* off;
   int groups, M, rows;
-  int o0, n, upto;   // of group `lane` of the first 64: first row, rows, tiles up to its end
+  int o0, n;         // of group `lane` of the first 64: first row, rows
+  uint32_t upto;     // and tiles up to its end
 
   __device__ __forceinline__ GroupScan(const int32_t* off_, int groups_, int M_, int rows_)
       : off(off_), groups(groups_), M(M_), rows(rows_) {
@@ -55,29 +60,31 @@ struct GroupScan {
     upto = wave_scan((n + rows - 1) / rows, lane);
   }
 
-  __device__ __forceinline__ int tiles() const {
+  // Tiles of all groups, at most `most` (the bound that the grid was sized for).
+  __device__ __forceinline__ int tiles(int most) const {
     const int lane = threadIdx.x & 63;
-    int total = __builtin_amdgcn_readlane(upto, 63);
+    uint32_t total = min(last(upto), (uint32_t)most);
     for (int c = 64; c < groups; c += 64) {
       int o;
       const int m = group_rows(off, groups, M, c + lane, o);
-      total += __builtin_amdgcn_readlane(wave_scan((m + rows - 1) / rows, lane), 63);
+      total = min(total + last(wave_scan((m + rows - 1) / rows, lane)), (uint32_t)most);
     }
-    return total;
+    return (int)total;
   }
 
   // The group and rows of tile t (tiles of a group are consecutive); false
   // when there are fewer tiles.
   __device__ __forceinline__ bool find(int t, GroupTile& out) const {
     const int lane = threadIdx.x & 63;
-    int o = o0, m = n, up = upto;
+    int o = o0, m = n;
+    uint32_t up = upto;
     for (int c = 0;;) {
-      const uint64_t past = __ballot(up > t);
+      const uint64_t past = __ballot(up > (uint32_t)t);
       if (past) {
         const int l = __builtin_ctzll(past);
         const int len = __builtin_amdgcn_readlane(m, l);
-        const int first = __builtin_amdgcn_readlane(up, l) - (len + rows - 1) / rows;
-        if (t < first) return false;   // only where unsorted offsets make the sum overflow
+        // tiles before the group: at most t, as no group before reaches past t
+        const int first = __builtin_amdgcn_readlane((int)up, l) - (len + rows - 1) / rows;
         out.g = c + l;
         out.row0 = __builtin_amdgcn_readlane(o, l) + (t - first) * rows;
         out.row1 = __builtin_amdgcn_readlane(o, l) + len;
@@ -85,10 +92,15 @@ struct GroupScan {
       }
       c += 64;
       if (c >= groups) return false;
-      const int before = __builtin_amdgcn_readlane(up, 63);
+      const uint32_t before = last(up);
       m = group_rows(off, groups, M, c + lane, o);
       up = before + wave_scan((m + rows - 1) / rows, lane);
     }
+  }
+
+ private:
+  static __device__ __forceinline__ uint32_t last(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
   }
 };
 
