@@ -115,6 +115,22 @@ bool bias_of(const at::Tensor* t, int64_t n) {
          fail("bias is a contiguous bfloat16 tensor, one element per output column");
 }
 
+// bf16 values, or their bits under an integer type
+bool bf16_bits(const at::Tensor& t) {
+  const auto ty = t.scalar_type();
+  return ty == at::kBFloat16 || ty == at::kShort || ty == at::kUInt16;
+}
+
+// u of the low-rank branch: fp32 [rows, rank], rows any stride apart
+bool lowrank_u(const at::Tensor* u, int64_t rows, int64_t rank) {
+  return !u || (u->scalar_type() == at::kFloat && row_major(*u) && u->size(0) >= rows && u->size(1) >= rank) ||
+         fail("u is a row-major float32 tensor [rows, rank]");
+}
+
+bool one_float(const at::Tensor* t, const char* what) {
+  return !t || (t->scalar_type() == at::kFloat && t->numel() >= 1) || fail(what);
+}
+
 template <class F>
 PyObject* guarded(F f) {   // no C++ exception crosses into Python
   try {
@@ -140,16 +156,21 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !to_tensor(a[5], &u, "u is a tensor") || !q.read(a[6]) ||
         !to_tensor(a[7], &ws, "workspace is a tensor") || !to_i64(a[8], &wsn) || !to_i64(a[9], &stream))
       return nullptr;
-    if (!x || !row_major(*x) || x->scalar_type() != (dt == MXQ_DT_BF16 ? at::kBFloat16 : at::kFloat) ||
-        (l1t && l1t->dim() < 1) || (u && u->dim() < 1)) {
+    if (!x || !row_major(*x) || x->scalar_type() != (dt == MXQ_DT_BF16 ? at::kBFloat16 : at::kFloat)) {
       fail("quantize needs a row-major 2-D float32 or bfloat16 tensor");
       return nullptr;
     }
+    if (l1t && (!bf16_bits(*l1t) || l1t->dim() != 2 || l1t->size(1) != x->size(1) || !l1t->is_contiguous())) {
+      fail("l1t is a contiguous bfloat16 tensor [rank, cols]");
+      return nullptr;
+    }
+    if ((l1t && !lowrank_u(u, x->size(0), l1t->size(0))) || !one_float(g, "static_tensor_scale is a float32 tensor"))
+      return nullptr;
     mxq_status st;
     Py_BEGIN_ALLOW_THREADS
     st = g_quantize(x->data_ptr(), (int32_t)dt, x->size(0), x->size(1), ld(*x), (int32_t)had,
                     static_cast<const float*>(ptr(g)), ptr(l1t), l1t ? (int32_t)l1t->size(0) : 0,
-                    static_cast<float*>(ptr(u)), u ? u->stride(0) : 0, &q, ptr(ws), (size_t)wsn,
+                    static_cast<float*>(ptr(u)), u && l1t ? ld(*u) : 0, &q, ptr(ws), (size_t)wsn,
                     reinterpret_cast<void*>(stream));
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
