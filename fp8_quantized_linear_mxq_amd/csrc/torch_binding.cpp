@@ -208,10 +208,19 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !to_tensor(a[7], &out, "out is a tensor") || !to_tensor(a[8], &ws, "workspace is a tensor") ||
         !to_i64(a[9], &wsn) || !to_i64(a[10], &stream))
       return nullptr;
-    if (!qa.codes || n_out < 0 || (u && u->dim() < 1) || (l2t && l2t->dim() != 2)) {
-      fail("gemm needs the operand's codes and a 2-D l2t");
+    if (!qa.codes || n_out < 0) {
+      fail("gemm needs the operand's codes");
       return nullptr;
     }
+    if (map && (map->scalar_type() != at::kInt || !map->is_contiguous() || map->numel() < qw.rows)) {
+      fail("w_out_col is a contiguous int32 tensor, one element per weight row");
+      return nullptr;
+    }
+    if (l2t && (!bf16_bits(*l2t) || l2t->dim() != 2 || l2t->size(0) < n_out || !l2t->is_contiguous())) {
+      fail("l2t is a contiguous bfloat16 tensor [n_out, rank]");
+      return nullptr;
+    }
+    if (l2t && !lowrank_u(u, qa.rows, l2t->size(1))) return nullptr;
     if (!bias_of(bias, n_out) || (out && !output(*out, qa.rows, n_out))) return nullptr;
     at::Tensor made;
     if (!out) {
@@ -221,7 +230,7 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     mxq_status st;
     Py_BEGIN_ALLOW_THREADS
     st = g_gemm(&qa, &qw, static_cast<const int32_t*>(ptr(map)), static_cast<const float*>(ptr(u)),
-                u ? u->stride(0) : 0, ptr(l2t), l2t ? (int32_t)l2t->size(1) : 0, ptr(bias), out->data_ptr(),
+                u && l2t ? ld(*u) : 0, ptr(l2t), l2t ? (int32_t)l2t->size(1) : 0, ptr(bias), out->data_ptr(),
                 ld(*out), n_out, ptr(ws), (size_t)wsn, reinterpret_cast<void*>(stream));
     Py_END_ALLOW_THREADS
     if (st != MXQ_OK) return PyLong_FromLong(st);

@@ -58,3 +58,57 @@ def test_quantize_takes_strided_u_and_bits():
     got = mxq.quantize(x, mxq.INT8, l1t=l1.view(torch.int16), u=wide)
     assert torch.equal(got.codes, want.codes) and torch.equal(wide[:M, :R], u)
     assert not bool(wide[M:].any()) and not bool(wide[:, R:].any())
+
+
+# ---- gemm: column map, low-rank operands -----------------------------------
+
+N = 48
+
+
+def product(fmt=mxq.INT8, m=M, n=N, k=K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    return (mxq.quantize(torch.randn(m, k, generator=g, device="cuda"), fmt),
+            mxq.quantize(torch.randn(n, k, generator=g, device="cuda"), fmt))
+
+
+@pytest.mark.parametrize("cols", [
+    lambda: torch.randperm(N, device="cuda"), lambda: torch.arange(N - 1, dtype=torch.int32, device="cuda"),
+    lambda: torch.arange(2 * N, dtype=torch.int32, device="cuda")[::2], lambda: zeros(N),
+    lambda: torch.arange(N, dtype=torch.int32),
+], ids=["int64", "short", "strided", "f32", "host"])
+@pytest.mark.parametrize("fmt", [mxq.INT8, mxq.MXFP4])
+def test_gemm_refuses_column_map(cols, fmt):
+    a, w = product(fmt)
+    with pytest.raises(ValueError):
+        mxq.gemm(a, w, w_out_col=cols())
+
+
+@pytest.mark.parametrize("u,l2t", [
+    (lambda: zeros(M - 1, R), lambda: zeros(N, R, dtype=BF16)), (lambda: zeros(M, R - 16), lambda: zeros(N, R, dtype=BF16)),
+    (lambda: zeros(M, R, dtype=BF16), lambda: zeros(N, R, dtype=BF16)), (lambda: zeros(R, M).t(), lambda: zeros(N, R, dtype=BF16)),
+    (lambda: zeros(M, R), lambda: zeros(N - 1, R, dtype=BF16)), (lambda: zeros(M, R), lambda: zeros(N, R)),
+    (lambda: zeros(M, R), lambda: zeros(N, R, dtype=torch.float16)), (lambda: zeros(M, R), lambda: zeros(R, N, dtype=BF16).t()),
+    (lambda: zeros(M, R), lambda: zeros(N, 2 * R, dtype=BF16)[:, :R]), (lambda: zeros(M, R), lambda: zeros(N * R, dtype=BF16)),
+], ids=["u rows", "u rank", "u bf16", "u transposed", "l2t rows", "l2t f32", "l2t f16", "l2t transposed",
+        "l2t row stride", "l2t 1-D"])
+@pytest.mark.parametrize("fmt", [mxq.INT8, mxq.MXFP4])
+def test_gemm_refuses_lowrank(u, l2t, fmt):
+    a, w = product(fmt)
+    with pytest.raises(ValueError):
+        mxq.gemm(a, w, u=u(), l2t=l2t())
+
+
+@pytest.mark.parametrize("fmt", [mxq.INT8, mxq.MXFP4])
+def test_gemm_takes_longer_maps_and_strided_u(fmt):
+    a, w = product(fmt)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    u, l2t = torch.randn(M, R, generator=g, device="cuda"), torch.randn(N, R, generator=g, device="cuda").to(BF16)
+    want = mxq.gemm(a, w, u=u, l2t=l2t)
+    wide = zeros(M + 1, R + 4)
+    wide[:M, :R] = u
+    rev = torch.arange(N, dtype=torch.int32, device="cuda").flip(0)
+    assert torch.equal(mxq.gemm(a, w, u=wide, l2t=l2t.view(torch.int16)), want)
+    y = mxq.gemm(a, w, u=u, l2t=l2t.flip(0).contiguous(), w_out_col=torch.cat([rev, rev]))
+    assert torch.equal(y.flip(1), want)
