@@ -206,11 +206,12 @@ def bf16_operand(x) -> QTensor:
 
 
 def int8_operand(codes, scales) -> QTensor:
-    """int8 codes [rows, K] (cuda, row-major) and one float32 scale per row
-    ([rows] or [rows, 1]) as a quantized operand."""
+    """int8 codes [rows, K] (cuda, row-major; int8, or their bits as uint8)
+    and one float32 scale per row ([rows] or [rows, 1]) as a quantized operand."""
     shape = codes.shape
-    if len(shape) != 2 or codes.element_size() != 1 or (codes.stride(1) != 1 and shape[1] > 1):
-        raise ValueError("int8_operand needs row-major 2-D 8-bit codes")
+    if len(shape) != 2 or codes.element_size() != 1 or codes.is_floating_point() or \
+            (codes.stride(1) != 1 and shape[1] > 1):
+        raise ValueError("int8_operand needs row-major 2-D 8-bit integer codes")
     rows, cols = shape
     sshape = scales.shape
     if scales.element_size() != 4 or not scales.is_floating_point() or sshape[0] != rows or \

@@ -54,6 +54,16 @@ int64_t ld(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : std::max(
 
 bool row_major(const at::Tensor& t) { return t.dim() == 2 && (t.stride(1) == 1 || t.size(1) <= 1); }
 
+// bf16 values, or their bits under an integer type
+bool bf16_bits(const at::Tensor& t) {
+  const auto ty = t.scalar_type();
+  return ty == at::kBFloat16 || ty == at::kShort || ty == at::kUInt16;
+}
+
+bool one_float(const at::Tensor* t, const char* what) {
+  return !t || (t->scalar_type() == at::kFloat && t->numel() >= 1) || fail(what);
+}
+
 // Attribute `name` of a quantized operand, undefined for None.
 bool part(PyObject* q, PyObject* name, at::Tensor* t) {
   PyObject* o = PyObject_GetAttr(q, name);
@@ -73,6 +83,8 @@ bool number(PyObject* q, PyObject* name, int64_t* v) {
   return ok;
 }
 
+constexpr int64_t kMaxCols = int64_t(1) << 40;   // more than any tensor has: no overflow in what follows
+
 // A quantized operand, with the tensors it reads held for the call.
 struct Operand : mxq_qtensor {
   at::Tensor t_codes, t_scales, t_tensor_scale;
@@ -84,19 +96,67 @@ struct Operand : mxq_qtensor {
       return false;
     fmt = (int32_t)f;
     reserved = 0;
-    return side(t_codes, &codes, &ld_codes) && side(t_scales, &scales, &ld_scales) &&
-           ((tensor_scale = static_cast<float*>(t_tensor_scale.defined() ? t_tensor_scale.data_ptr() : nullptr)), true);
+    if (t_tensor_scale.defined() && !one_float(&t_tensor_scale, "an operand's tensor_scale is a float32 tensor")) return false;
+    tensor_scale = static_cast<float*>(t_tensor_scale.defined() ? t_tensor_scale.data_ptr() : nullptr);
+    return side(t_codes, code_bytes(), code_type(), &codes, &ld_codes) &&
+           side(t_scales, scale_bytes(), scale_type(), &scales, &ld_scales);
   }
 
  private:
-  bool side(const at::Tensor& t, void** p, int64_t* bytes) {
+  // Bytes of a row's codes and scales; formats that the library does not know
+  // have none, and are refused there.
+  int64_t code_bytes() const {
+    const int64_t k = std::min(cols, kMaxCols);
+    switch (fmt) {
+      case MXQ_FMT_BF16: return 2 * k;
+      case MXQ_FMT_MXFP8: case MXQ_FMT_INT8: return k;
+      case MXQ_FMT_MXFP4: case MXQ_FMT_NVFP4: case MXQ_FMT_INT4: return k / 2;
+      default: return 0;
+    }
+  }
+  int64_t scale_bytes() const {
+    const int64_t k = std::min(cols, kMaxCols);
+    switch (fmt) {
+      case MXQ_FMT_INT8: return 4;
+      case MXQ_FMT_INT4: return k / 32 * 4;
+      case MXQ_FMT_NVFP4: return k / 16;
+      case MXQ_FMT_MXFP4: case MXQ_FMT_MXFP8: return k / 32;
+      default: return 0;
+    }
+  }
+
+  // Codes and the scale codes of the block formats are bytes under any type but
+  // the wider floating ones, whose values would be taken for them; bf16
+  // operands, integers and fp32 scales are what they say.
+  enum Type { kBytes, kBits16, kInt8, kFloat32 };
+  Type code_type() const { return fmt == MXQ_FMT_BF16 ? kBits16 : fmt == MXQ_FMT_INT8 ? kInt8 : kBytes; }
+  Type scale_type() const { return fmt == MXQ_FMT_INT8 || fmt == MXQ_FMT_INT4 ? kFloat32 : kBytes; }
+  static bool is(const at::Tensor& t, Type ty) {
+    const auto s = t.scalar_type();
+    switch (ty) {
+      case kBits16: return bf16_bits(t);
+      case kInt8: return s == at::kChar || s == at::kByte;
+      case kFloat32: return s == at::kFloat;
+      default: return !(at::isFloatingType(s) && t.element_size() > 1) && !at::isComplexType(s);
+    }
+  }
+
+  bool side(const at::Tensor& t, int64_t need, Type type, void** p, int64_t* bytes) {
     *p = nullptr;
     *bytes = 0;
     if (!t.defined()) return true;
     if (t.dim() < 1 || t.size(0) < rows) return fail("an operand's codes and scales have its rows");
     *p = t.data_ptr();
     *bytes = t.stride(0) * (int64_t)t.element_size();
-    return true;
+    if (rows <= 0 || cols <= 0) return true;
+    if (!is(t, type)) return fail("an operand's codes and scales have its format's types");
+    int64_t row = (int64_t)t.element_size();   // bytes of a row, which lie together
+    for (int64_t d = t.dim() - 1; d > 0; --d) {
+      if (t.size(d) != 1 && t.stride(d) * (int64_t)t.element_size() != row)
+        return fail("the rows of an operand's codes and scales are contiguous");
+      row *= t.size(d);
+    }
+    return row >= need || fail("an operand's codes and scales are as wide as its columns");
   }
 };
 
@@ -115,20 +175,10 @@ bool bias_of(const at::Tensor* t, int64_t n) {
          fail("bias is a contiguous bfloat16 tensor, one element per output column");
 }
 
-// bf16 values, or their bits under an integer type
-bool bf16_bits(const at::Tensor& t) {
-  const auto ty = t.scalar_type();
-  return ty == at::kBFloat16 || ty == at::kShort || ty == at::kUInt16;
-}
-
 // u of the low-rank branch: fp32 [rows, rank], rows any stride apart
 bool lowrank_u(const at::Tensor* u, int64_t rows, int64_t rank) {
   return !u || (u->scalar_type() == at::kFloat && row_major(*u) && u->size(0) >= rows && u->size(1) >= rank) ||
          fail("u is a row-major float32 tensor [rows, rank]");
-}
-
-bool one_float(const at::Tensor* t, const char* what) {
-  return !t || (t->scalar_type() == at::kFloat && t->numel() >= 1) || fail(what);
 }
 
 template <class F>

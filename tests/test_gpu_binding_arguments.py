@@ -112,3 +112,72 @@ def test_gemm_takes_longer_maps_and_strided_u(fmt):
     assert torch.equal(mxq.gemm(a, w, u=wide, l2t=l2t.view(torch.int16)), want)
     y = mxq.gemm(a, w, u=u, l2t=l2t.flip(0).contiguous(), w_out_col=torch.cat([rev, rev]))
     assert torch.equal(y.flip(1), want)
+
+
+# ---- quantized operands ----------------------------------------------------
+
+def test_int8_operand_refuses_float8():
+    a, _ = product()
+    for dt in (torch.float8_e4m3fn, torch.float8_e5m2):
+        with pytest.raises(ValueError):
+            mxq.int8_operand(a.codes.view(dt), a.scales)
+
+
+# what is wrong with codes or scales of 6 x 256 operands, by format
+WRONG = [
+    (mxq.INT8, "codes", lambda t: t.view(torch.float8_e4m3fn)), (mxq.INT8, "codes", lambda t: t.to(torch.int32)),
+    (mxq.INT8, "codes", lambda t: t[:, :K - 16]), (mxq.INT8, "codes", lambda t: t.t().contiguous().t()),
+    (mxq.INT8, "scales", lambda t: t.view(torch.int32)), (mxq.INT8, "scales", lambda t: t.to(torch.float64)),
+    (mxq.INT8, "scales", lambda t: t.to(torch.float16)),
+    (mxq.MXFP4, "codes", lambda t: t.to(BF16)), (mxq.MXFP4, "codes", lambda t: t[:, :K // 2 - 16]),
+    (mxq.MXFP4, "codes", lambda t: t.repeat(1, 2)[:, ::2]), (mxq.MXFP4, "scales", lambda t: t.float()),
+    (mxq.MXFP4, "scales", lambda t: t[:, :4]), (mxq.MXFP4, "scales", lambda t: t.flatten()),
+    (mxq.NVFP4, "tensor_scale", lambda t: t.double()), (mxq.NVFP4, "tensor_scale", lambda t: t[:0]),
+    (mxq.NVFP4, "scales", lambda t: t[:, :8]), (mxq.BF16, "codes", lambda t: t.to(torch.float16)),
+    (mxq.BF16, "codes", lambda t: t[:, :K - 8]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WRONG)))
+def test_operands_refuse(case):
+    """As an operand of a product, and as what quantize writes."""
+    fmt, name, spoil = WRONG[case]
+    if fmt == mxq.BF16:
+        a, w = mxq.bf16_operand(zeros(M, K, dtype=BF16)), product(mxq.MXFP4)[1]
+    else:
+        a, w = product(fmt)
+    mxq.gemm(a, w)
+    bad = mxq.QTensor(a.fmt, a.rows, a.cols, a.codes, a.scales, a.tensor_scale)
+    setattr(bad, name, spoil(getattr(a, name)))
+    with pytest.raises(ValueError):
+        mxq.gemm(bad, w)
+    if fmt in (mxq.INT8, mxq.MXFP4):
+        with pytest.raises(ValueError):
+            mxq.gemm_grouped(bad, w, torch.tensor([0, M], dtype=torch.int32, device="cuda"))
+    if fmt != mxq.BF16:
+        with pytest.raises(ValueError):
+            mxq.gemm(a, mxq.QTensor(w.fmt, w.rows, w.cols, *[spoil(v) if n == name else v for n, v in
+                                                             [("codes", w.codes), ("scales", w.scales),
+                                                              ("tensor_scale", w.tensor_scale)]]))
+        with pytest.raises(ValueError):
+            mxq.quantize(zeros(M, K), fmt, out=bad)
+
+
+def test_operands_take_bits_and_packed_types():
+    """The same bytes under other types, and rows wider than the columns."""
+    for fmt in (mxq.INT8, mxq.MXFP4, mxq.NVFP4, mxq.MXFP8, mxq.INT4):
+        a, w = product(mxq.MXFP4 if fmt == mxq.INT4 else fmt)
+        w = product(mxq.MXFP4)[1] if fmt == mxq.MXFP8 else product(fmt)[1]
+        want = mxq.gemm(a, w)
+        wide = torch.zeros(M, a.codes.shape[1] + 32, dtype=torch.uint8, device="cuda")
+        wide[:, :a.codes.shape[1]] = a.codes
+        assert torch.equal(mxq.gemm(mxq.QTensor(a.fmt, M, K, wide, a.scales, a.tensor_scale), w), want)
+        if fmt == mxq.INT8:
+            other = mxq.QTensor(a.fmt, M, K, a.codes.view(torch.int8), a.scales.flatten())
+        else:
+            other = mxq.QTensor(a.fmt, M, K, a.codes.view(torch.int32), a.scales.view(torch.int8), a.tensor_scale)
+        assert torch.equal(mxq.gemm(other, w), want)
+    x = torch.randn(M, K, device="cuda").to(BF16)
+    w = product(mxq.MXFP4)[1]
+    assert torch.equal(mxq.gemm(mxq.QTensor(mxq.BF16, M, K, x.view(torch.int16), None), w),
+                       mxq.gemm(mxq.bf16_operand(x), w))
