@@ -258,7 +258,7 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !to_tensor(a[7], &out, "out is a tensor") || !to_tensor(a[8], &ws, "workspace is a tensor") ||
         !to_i64(a[9], &wsn) || !to_i64(a[10], &stream))
       return nullptr;
-    if (!qa.codes || n_out < 0) {
+    if (!qa.t_codes.defined() || n_out < 0) {
       fail("gemm needs the operand's codes");
       return nullptr;
     }
@@ -300,7 +300,7 @@ PyObject* gemm_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !to_tensor(a[2], &off, "offsets is a tensor") || !to_tensor(a[3], &bias, "bias is a tensor") ||
         !to_tensor(a[4], &out, "out is a tensor") || !to_i64(a[5], &stream))
       return nullptr;
-    if (!qa.codes || !off || off->scalar_type() != at::kInt || off->dim() != 1 || !off->is_contiguous()) {
+    if (!qa.t_codes.defined() || !off || off->scalar_type() != at::kInt || off->dim() != 1 || !off->is_contiguous()) {
       fail("gemm_grouped needs the operand's codes and contiguous 1-D int32 offsets");
       return nullptr;
     }

@@ -181,3 +181,18 @@ def test_operands_take_bits_and_packed_types():
     w = product(mxq.MXFP4)[1]
     assert torch.equal(mxq.gemm(mxq.QTensor(mxq.BF16, M, K, x.view(torch.int16), None), w),
                        mxq.gemm(mxq.bf16_operand(x), w))
+
+
+@pytest.mark.parametrize("fmt", [mxq.INT8, mxq.MXFP4, mxq.NVFP4, mxq.BF16])
+def test_no_rows(fmt):
+    """An empty batch: its tensors have no address, and it is a no-op."""
+    a = mxq.bf16_operand(zeros(0, K, dtype=BF16)) if fmt == mxq.BF16 else mxq.quantize(zeros(0, K), fmt)
+    w = product(mxq.MXFP4 if fmt == mxq.BF16 else fmt)[1]
+    assert mxq.gemm(a, w).shape == (0, N)
+    out = torch.full((4, N), 3.0, dtype=BF16, device="cuda")
+    mxq.gemm(a, w, out=out)
+    assert bool((out == 3).all())
+    if fmt != mxq.NVFP4:
+        off = torch.zeros(3, dtype=torch.int32, device="cuda")
+        y = mxq.gemm_grouped(a, w, off)
+        assert y.shape == (0, N // 2) and y.dtype == BF16
