@@ -164,14 +164,14 @@ at::Tensor bf16_like(const at::Tensor& t, at::IntArrayRef sizes) {
   return at::empty(sizes, t.options().dtype(at::kBFloat16).requires_grad(false));
 }
 
-// bf16 [rows, cols], rows any stride apart
+// [rows, cols], rows any stride apart; bf16, or a 16-bit type that its bits are put into
 bool output(const at::Tensor& t, int64_t rows, int64_t cols) {
-  return (t.scalar_type() == at::kBFloat16 && row_major(t) && t.size(0) >= rows && t.size(1) >= cols) ||
-         fail("out is a row-major bfloat16 tensor of the product's size");
+  return (t.element_size() == 2 && row_major(t) && t.size(0) >= rows && t.size(1) >= cols) ||
+         fail("out is a row-major tensor of the product's size, bfloat16 or its bits");
 }
 
 bool bias_of(const at::Tensor* t, int64_t n) {
-  return !t || (t->scalar_type() == at::kBFloat16 && t->is_contiguous() && t->numel() >= n) ||
+  return !t || (bf16_bits(*t) && t->is_contiguous() && t->numel() >= n) ||
          fail("bias is a contiguous bfloat16 tensor, one element per output column");
 }
 

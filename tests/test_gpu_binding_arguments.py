@@ -196,3 +196,22 @@ def test_no_rows(fmt):
         off = torch.zeros(3, dtype=torch.int32, device="cuda")
         y = mxq.gemm_grouped(a, w, off)
         assert y.shape == (0, N // 2) and y.dtype == BF16
+
+
+@pytest.mark.parametrize("dt", [torch.int16, torch.uint16, torch.float16])
+@pytest.mark.parametrize("fmt", [mxq.INT8, mxq.MXFP4])
+def test_out_and_bias_as_bits(fmt, dt):
+    """out may be memory of any 16-bit type that the bf16 results are put into,
+    bias bf16 bits of an integer type."""
+    a, w = product(fmt)
+    bias = torch.randn(N, device="cuda").to(BF16)
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    want = mxq.gemm(a, w, bias=bias)
+    bits = bias if dt == torch.float16 else bias.view(dt)
+    out = zeros(M, N, dtype=dt)
+    assert mxq.gemm(a, w, bias=bits, out=out) is out and torch.equal(out.view(BF16), want)
+    out = zeros(M, N, dtype=dt)
+    mxq.gemm_grouped(a, w, off, bias=bits, out=out)
+    assert torch.equal(out.view(BF16), mxq.gemm_grouped(a, w, off, bias=bias))
+    with pytest.raises(ValueError):
+        mxq.gemm(a, w, bias=bias.to(torch.float16))
