@@ -156,6 +156,8 @@ struct Operand : mxq_qtensor {
         return fail("the rows of an operand's codes and scales are contiguous");
       row *= t.size(d);
     }
+    // a single row may have any stride: it is given one that the library takes
+    if (rows == 1) *bytes = (row + 15) / 16 * 16;
     return row >= need || fail("an operand's codes and scales are as wide as its columns");
   }
 };

@@ -215,3 +215,29 @@ def test_out_and_bias_as_bits(fmt, dt):
     assert torch.equal(out.view(BF16), mxq.gemm_grouped(a, w, off, bias=bias))
     with pytest.raises(ValueError):
         mxq.gemm(a, w, bias=bias.to(torch.float16))
+
+
+@pytest.mark.parametrize("fmt", [mxq.INT8, mxq.MXFP4, mxq.BF16])
+def test_one_row_operands_of_any_stride(fmt):
+    """One token (and one output channel) as a transposed column, an expanded
+    row and a row of a strided view."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.randn(1, K, generator=g, device="cuda").to(BF16)
+    a = mxq.bf16_operand(x) if fmt == mxq.BF16 else mxq.quantize(x, fmt)
+    w = product(mxq.MXFP4 if fmt == mxq.BF16 else fmt)[1]
+    w1 = mxq.QTensor(w.fmt, 1, K, w.codes[:1], w.scales[:1])
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    want, want1 = mxq.gemm(a, w), mxq.gemm(a, w1)
+
+    def forms(t):
+        if t is None:
+            return [None] * 3
+        return [t.reshape(-1, 1).contiguous().t(), t[0].expand(1, -1),
+                torch.cat([t] * 3)[::3] if t.shape[1] > 1 else t.expand(1, 1)]
+
+    for codes, scales in zip(forms(a.codes), forms(a.scales)):
+        one = mxq.QTensor(a.fmt, 1, K, codes, scales)
+        assert torch.equal(mxq.gemm(one, w), want) and torch.equal(mxq.gemm_grouped(one, w, off), want)
+    for codes, scales in zip(forms(w1.codes), forms(w1.scales)):
+        assert torch.equal(mxq.gemm(a, mxq.QTensor(w.fmt, 1, K, codes, scales)), want1)
