@@ -225,10 +225,13 @@ def pack_l1t(l1t, stream=None):
     fused quantize + low-rank kernel reads; returned with the same shape."""
     import torch
     lib = load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return pack_l1t(l1t)
     rank, cols = l1t.shape
     l1t = l1t.contiguous()
     out = torch.empty_like(l1t)
-    _check("mxq_pack_l1t", lib.mxq_pack_l1t(_ptr(l1t), rank, cols, _ptr(out), _stream(stream)))
+    _check("mxq_pack_l1t", lib.mxq_pack_l1t(_ptr(l1t), rank, cols, _ptr(out), _stream(None)))
     return out
 
 
@@ -312,6 +315,9 @@ def gemm_mixed(a: QTensor, groups: list, w_perm, n_out: int, u=None, l2t=None, b
     """mxq_gemm_mixed over weight groups (QTensor list) and their permutation."""
     import torch
     lib = load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return gemm_mixed(a, groups, w_perm, n_out, u, l2t, bias, out, workspace=workspace)
     if out is None:
         out = torch.empty((a.rows, n_out), dtype=torch.bfloat16, device=a.codes.device)
     ac = a.c()
@@ -320,7 +326,7 @@ def gemm_mixed(a: QTensor, groups: list, w_perm, n_out: int, u=None, l2t=None, b
     wsp, wsn = _gemm_workspace(a, groups, workspace)
     st = lib.mxq_gemm_mixed(C.byref(ac), arr, len(groups), _ptr(w_perm), _ptr(u),
                             0 if u is None else u.stride(0), _ptr(l2t), rank, _ptr(bias),
-                            _ptr(out), out.stride(0), n_out, wsp, wsn, _stream(stream))
+                            _ptr(out), out.stride(0), n_out, wsp, wsn, _stream(None))
     _check("mxq_gemm_mixed", st)
     return out
 
@@ -367,6 +373,9 @@ def conv3x3_gemm_mixed(x: QTensor, height: int, width: int, groups: list, w_perm
     groups of 9*C columns; returns the bf16 [x.rows, n_out] output tensor."""
     import torch
     lib = load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return conv3x3_gemm_mixed(x, height, width, groups, w_perm, n_out, bias, out, workspace=workspace)
     if out is None:
         out = torch.empty((x.rows, n_out), dtype=torch.bfloat16, device=x.codes.device)
     xc = x.c()
@@ -374,7 +383,7 @@ def conv3x3_gemm_mixed(x: QTensor, height: int, width: int, groups: list, w_perm
     wsp, wsn = _gemm_workspace(x, groups, workspace)
     st = lib.mxq_conv3x3_gemm_mixed(C.byref(xc), height, width, arr, len(groups), _ptr(w_perm),
                                     _ptr(bias), _ptr(out), out.stride(0), n_out, wsp, wsn,
-                                    _stream(stream))
+                                    _stream(None))
     _check("mxq_conv3x3_gemm_mixed", st)
     return out
 
@@ -384,6 +393,9 @@ def select_format(w, candidates=(INT4, MXFP4, NVFP4), stream=None):
     counts i32[c], g f32[1]) as device tensors."""
     import torch
     lib = load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return select_format(w, candidates)
     n, k = w.shape
     dt = DT_BF16 if w.dtype == torch.bfloat16 else DT_F32
     dev = w.device
@@ -396,7 +408,7 @@ def select_format(w, candidates=(INT4, MXFP4, NVFP4), stream=None):
     cand = (C.c_int32 * len(candidates))(*candidates)
     st = lib.mxq_select_format(_ptr(w), dt, n, k, w.stride(0), cand, len(candidates),
                                _ptr(choice), _ptr(sse), _ptr(perm), _ptr(counts), _ptr(g),
-                               _ptr(ws), ws.numel(), _stream(stream))
+                               _ptr(ws), ws.numel(), _stream(None))
     _check("mxq_select_format", st)
     return choice, sse, perm, counts, g
 
@@ -407,6 +419,9 @@ def quantize_mse(w, fmt: int, out: QTensor | None = None, workspace=None,
     MXFP4 or NVFP4 codes with least-squared-error scales."""
     import torch
     lib = load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return quantize_mse(w, fmt, out, workspace)
     rows, cols = w.shape
     dt = DT_BF16 if w.dtype == torch.bfloat16 else DT_F32
     if out is None:
@@ -416,7 +431,7 @@ def quantize_mse(w, fmt: int, out: QTensor | None = None, workspace=None,
         workspace = torch.empty((max(n, 16),), dtype=torch.uint8, device=w.device)
     qc = out.c()
     st = lib.mxq_quantize_mse(_ptr(w), dt, rows, cols, w.stride(0), C.byref(qc),
-                              _ptr(workspace), workspace.numel(), _stream(stream))
+                              _ptr(workspace), workspace.numel(), _stream(None))
     _check("mxq_quantize_mse", st)
     return out
 
@@ -427,6 +442,9 @@ def lowrank_split(w, rank: int, iters: int = 0, stream=None):
     sigma float32 [rank])."""
     import torch
     lib = load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with torch.cuda.stream(stream):
+            return lowrank_split(w, rank, iters)
     n, k = w.shape
     dev = w.device
     l1t = torch.empty((rank, k), dtype=torch.bfloat16, device=dev)
@@ -437,6 +455,6 @@ def lowrank_split(w, rank: int, iters: int = 0, stream=None):
                      dtype=torch.uint8, device=dev)
     st = lib.mxq_lowrank_split(_ptr(w), n, k, w.stride(0), rank, iters, _ptr(l1t), _ptr(l2t),
                                _ptr(resid), resid.stride(0), _ptr(sigma), _ptr(ws), ws.numel(),
-                               _stream(stream))
+                               _stream(None))
     _check("mxq_lowrank_split", st)
     return l1t, l2t, resid, sigma
