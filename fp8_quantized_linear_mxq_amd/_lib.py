@@ -55,6 +55,18 @@ _torch = None   # the torch module, bound by load(): an import statement costs 0
 _fast = None    # the marshalling module
 
 
+class _NotBuilt:
+    """In place of the marshalling module: the calls through it raise, the
+    library's other entry points work without it."""
+
+    def __init__(self, cause):
+        self.cause = cause
+
+    def __getattr__(self, name):
+        raise RuntimeError("the torch marshalling module is not built for this Python and torch; run "
+                           "python -m fp8_quantized_linear_mxq_amd.build") from self.cause
+
+
 def load():
     """Load libmxq.so (built in-tree by ``build.py``); raises if absent."""
     global _lib, _torch, _fast
@@ -111,12 +123,11 @@ def load():
     if _torch is not None:
         try:
             from . import _torch_binding
+            _torch_binding.bind(*[C.cast(f, vp).value for f in (lib.mxq_quantize, lib.mxq_gemm,
+                                                                lib.mxq_gemm_grouped, lib.mxq_qk_norm_rope)])
+            _fast = _torch_binding
         except ImportError as e:
-            raise RuntimeError("the torch marshalling module is not built for this Python and torch; run "
-                               "python -m fp8_quantized_linear_mxq_amd.build") from e
-        _torch_binding.bind(*[C.cast(f, vp).value for f in (lib.mxq_quantize, lib.mxq_gemm,
-                                                            lib.mxq_gemm_grouped, lib.mxq_qk_norm_rope)])
-        _fast = _torch_binding
+            _fast = _NotBuilt(e)
     _lib = lib
     return lib
 

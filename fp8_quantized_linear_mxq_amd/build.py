@@ -1,5 +1,8 @@
 """Build libmxq.so (and the matrix-core probe library) in-tree with hipcc
-for gfx950, and the torch marshalling module with the host compiler.
+for gfx950, and the torch marshalling module with the host compiler.  The
+libraries need neither torch nor a host compiler: without torch the module is
+left out (Python callers need both), and an error in its build is raised once
+they are written.
 
 Usage: python -m fp8_quantized_linear_mxq_amd.build  (or build() from Python).
 Objects go to _build/ at the repository root; the shared library is written
@@ -53,21 +56,30 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_binding() -> None:
-    """The Python module that marshals torch tensors (host code only)."""
-    import torch
-    from torch.utils import cpp_extension
-    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
-    tmp = BINDING_LIB + ".tmp"
-    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f"-isystem{i}" for i in inc), BINDING_SRC,
-           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-o", tmp]
+def _run(what: str, cmd: list, out: str) -> None:
+    """Run the command that writes out.tmp, then move it into place."""
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"binding build failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING_LIB)
+        raise RuntimeError(f"{what} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+
+
+def _build_binding() -> bool:
+    """The Python module that marshals torch tensors (host code only); False
+    without torch."""
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return False
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    _run("binding build",
+         [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f"-isystem{i}" for i in inc), BINDING_SRC,
+          "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-o", BINDING_LIB + ".tmp"], BINDING_LIB)
+    return True
 
 
 def build(verbose: bool = True) -> str:
@@ -75,22 +87,12 @@ def build(verbose: bool = True) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, SOURCES))
-        binding.result()
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    # the matrix-core probes: a separate library, never loaded by the layer
-    tmp = PROBE_LIB + ".tmp"
-    cmd = [hipcc(), *_flags(), "-shared", PROBE_SRC, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"probe build failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, PROBE_LIB)
+        _run("link", [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", LIB + ".tmp"], LIB)
+        # the matrix-core probes: a separate library, never loaded by the layer
+        _run("probe build", [hipcc(), *_flags(), "-shared", PROBE_SRC, "-o", PROBE_LIB + ".tmp"], PROBE_LIB)
+        made = [LIB, PROBE_LIB] + ([BINDING_LIB] if binding.result() else [])
     if verbose:
-        print(f"built {LIB}, {BINDING_LIB} and {PROBE_LIB}")
+        print("built " + ", ".join(made))
     return LIB
 
 
