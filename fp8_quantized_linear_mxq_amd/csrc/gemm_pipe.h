@@ -6,6 +6,8 @@
 #include "device_common.h"
 #include "gemm_common.h"
 
+#include <type_traits>
+
 namespace mxq {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
@@ -235,38 +237,67 @@ __device__ __forceinline__ void add_lowrank(const GemmP& p, v16f (&acc)[TI][TN],
 }
 
 // ROWS x COLS staged bf16 values (at(r, c): the LDS address of element c of
-// row r) to output rows that are not 16-byte aligned: THREADS threads store
-// neighbouring pairs, or single elements where the rows are only 2-byte aligned,
-// so that an instruction still writes whole lines (grouped MXFP4, 4025 rows, N =
-// 2030, K = 768, 256 x 192 tiles: 23.5 us; each lane's quads stored directly 41.8).
-template <int ROWS, int COLS, int THREADS, class F>
-__device__ __forceinline__ void store_rows(const GemmP& p, int row0, int col0, int n_lim, int tid, F at) {
-  if ((p.ld_out & 1) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 3) == 0) {
-    for (int idx = tid; idx < ROWS * COLS / 2; idx += THREADS) {
-      const int r = idx / (COLS / 2), c = idx % (COLS / 2) * 2, row = row0 + r, n = col0 + c;
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(at(r, c));
-      if (row >= p.M) continue;
-      uint16_t* const o = p.out + (int64_t)row * p.ld_out + n;
-      if (n + 2 <= n_lim) *reinterpret_cast<uint32_t*>(o) = v;
-      else if (n < n_lim) *o = (uint16_t)v;
+// row r) to output rows: THREADS threads store neighbouring pieces of V elements,
+// so that an instruction writes whole lines.  Rows of 2- and 4-byte alignment,
+// against each lane's quads stored from its registers (4096 x 4608 x 1152): MXFP4
+// 74 -> 47.5 and 40.6 us, NVFP4 77.5 -> 60.5 and 78 -> 59; 8-byte rows of the
+// whole-tile form 46 -> 36.5.  Up to eight pieces are read before they are stored
+// and rows past the last are left out: one at a time, a small grid waits for
+// every one of them (64 x 4096 x 4096 MXFP8 x NVFP4, odd stride 72.6 us, now 67.9,
+// quads from registers 67.1).
+template <int V, int ROWS, int COLS, int THREADS, class F>
+__device__ __forceinline__ void store_pieces(const GemmP& p, int row0, int col0, int n_lim, int tid, F at) {
+  using Piece = std::conditional_t<V == 4, uint2, std::conditional_t<V == 2, uint32_t, uint16_t>>;
+  constexpr int PER = COLS / V, N = ROWS * PER / THREADS, U = N % 8 == 0 ? 8 : 4;
+  static_assert(ROWS * PER % THREADS == 0 && N % U == 0, "whole batches");
+  for (int t = 0; t < N; t += U) {
+    if (row0 + t * THREADS / PER >= p.M) break;
+    Piece v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int idx = (t + k) * THREADS + tid;
+      v[k] = *reinterpret_cast<const Piece*>(at(idx / PER, idx % PER * V));
     }
-    return;
-  }
-  for (int idx = tid; idx < ROWS * COLS; idx += THREADS) {
-    const int r = idx / COLS, c = idx % COLS, row = row0 + r, n = col0 + c;
-    const uint16_t v = *reinterpret_cast<const uint16_t*>(at(r, c));
-    if (row < p.M && n < n_lim) p.out[(int64_t)row * p.ld_out + n] = v;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int idx = (t + k) * THREADS + tid, row = row0 + idx / PER, n = col0 + idx % PER * V;
+      if (row >= p.M || n >= n_lim) continue;
+      uint16_t* const o = p.out + (int64_t)row * p.ld_out + n;
+      if (n + V <= n_lim) {
+        *reinterpret_cast<Piece*>(o) = v[k];
+      } else {
+        uint16_t e[V];
+        __builtin_memcpy(e, &v[k], sizeof(Piece));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (n + i < n_lim) o[i] = e[i];
+      }
+    }
   }
 }
 
+// Output rows that are not 16-byte aligned, in the widest pieces that they take
+// (of four elements only with QUADS).
+template <bool QUADS, int ROWS, int COLS, int THREADS, class F>
+__device__ __forceinline__ void store_rows(const GemmP& p, int row0, int col0, int n_lim, int tid, F at) {
+  const uint64_t low = (uint64_t)p.ld_out * 2 | reinterpret_cast<uintptr_t>(p.out);
+  if constexpr (QUADS) {
+    if ((low & 7) == 0) {
+      store_pieces<4, ROWS, COLS, THREADS>(p, row0, col0, n_lim, tid, at);
+      return;
+    }
+  }
+  if ((low & 3) == 0) store_pieces<2, ROWS, COLS, THREADS>(p, row0, col0, n_lim, tid, at);
+  else store_pieces<1, ROWS, COLS, THREADS>(p, row0, col0, n_lim, tid, at);
+}
+
 // Epilogue for the transposed accumulator layout: scales by alpha, adds the
-// low-rank branch (LR), the bias, and applies the column map.  `lds_region`
-// (32 * (TN * 64 + 16) bytes private to the wave, or null) enables the
-// staged row-wise stores.
+// low-rank branch (LR), the bias, and applies the column map.  `lds_region`:
+// 32 * (TN * 64 + 16) bytes private to the wave, for the staged row-wise stores.
 template <bool LR, int TI, int TN>
 __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN], float alpha,
                                             int row0, int col0, int lane,
-                                            uint8_t* lds_region = nullptr) {
+                                            uint8_t* lds_region) {
   const int l32 = lane & 31, half = lane >> 5;
   if (alpha != 1.0f) {
 #pragma unroll
@@ -279,13 +310,17 @@ __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN],
   if constexpr (LR) add_lowrank<TI, TN>(p, acc, row0, col0, lane);
   // stores: without a column map each 32-row tile goes through the wave's LDS
   // region (row-major) and leaves as whole rows, in 16-byte pieces where the
-  // output is aligned; otherwise each lane stores its quads directly (the four columns of a quad are shared by its TI rows, so their
-  // map entries and bias are fetched once per quad).
+  // output is aligned.  With a map, and for rows of 8-byte alignment, each lane
+  // stores its quads directly (the four columns of a quad are shared by its TI
+  // rows, so their map entries and bias are fetched once per quad).  For those
+  // rows quads from registers and 8-byte pieces through LDS are within 6% of
+  // each other, either way (quads / LDS: bf16 x NVFP4 777 x 1000 x 1152 15.9 / 16.6
+  // us, 64 x 4096 x 4096 41.1 / 41.8; MXFP8 x MXFP4 4096 x 4608 x 1152 52.0 / 49.3).
   const int n_lim = p.N < p.n_out ? p.N : p.n_out;
-  const bool staged = lds_region && !p.col_map;
   const bool wide = (p.ld_out & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
   const bool vec = !p.col_map && (p.ld_out & 3) == 0 &&
                    (reinterpret_cast<uintptr_t>(p.out) & 7) == 0;
+  const bool staged = !p.col_map && (wide || !vec);
   if (staged) {
     constexpr int RS = TN * 64 + 16;        // LDS bytes per staged row (padded)
     constexpr int CPR = TN * 4;             // 16-byte pieces per row
@@ -307,7 +342,7 @@ __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN],
           *reinterpret_cast<uint2*>(lds_region + l32 * RS + (j * 32 + 8 * g + 4 * half) * 2) = pk;
         }
       if (!wide) {
-        store_rows<32, TN * 32, 64>(p, row0 + i * 32, col0, n_lim, lane,
+        store_rows<false, 32, TN * 32, 64>(p, row0 + i * 32, col0, n_lim, lane,
                                     [&](int r, int c) { return lds_region + r * RS + c * 2; });
         continue;
       }
@@ -372,10 +407,11 @@ __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN],
   }
 }
 
-// Whole-tile staged epilogue (no column map; 16-byte aligned output rows):
+// Whole-tile staged epilogue (no column map):
 // each wave writes its accumulators (+ bias, bf16) into the LDS image of the
 // workgroup tile -- rows [0, TBM/2) in `lo`, the rest in `hi` -- then every
-// thread stores 16-byte pieces of whole tile rows with non-temporal stores.
+// thread stores 16-byte pieces of whole tile rows with non-temporal stores
+// (store_rows where the output rows are not 16-byte aligned).
 // Accumulator layout (D^T = W A^T): lane l of MFMA tile (i, j) holds row
 // i*32 + l%32 and columns j*32 + 8g + 4(l/32) + [0, 4) at acc[i][j][4g..4g+3].
 template <int TM, int TN, int WGM, int STAGE>
@@ -408,7 +444,7 @@ __device__ __forceinline__ void epilogue_wg(const GemmP& p, v16f (&acc)[TM][TN],
   }
   __syncthreads();
   if ((p.ld_out & 7) != 0 || (reinterpret_cast<uintptr_t>(p.out) & 15) != 0) {
-    store_rows<TBM, TBN, NT>(p, m0, n0, n_lim, threadIdx.x, [&](int r, int c) {
+    store_rows<true, TBM, TBN, NT>(p, m0, n0, n_lim, threadIdx.x, [&](int r, int c) {
       return (r < TBM / 2 ? lo + r * WRS : hi + (r - TBM / 2) * WRS) + c * 2;
     });
     return;
