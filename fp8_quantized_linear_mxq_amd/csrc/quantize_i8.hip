@@ -124,7 +124,8 @@ __device__ __forceinline__ float amax8(const float (&f)[8]) {
   return m;
 }
 
-// 8 codes of a row with scale s (inv = 1 / s, usable when `fast`).
+// 8 codes of a row of DT values with scale s (inv = 1 / s, usable when `fast`).
+template <int DT>
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv, bool fast) {
   // t + 1.5 * 2**23 rounds t to the nearest integer, ties to even, and holds
   // its two's complement in the low mantissa bits
@@ -133,7 +134,9 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv
   float near = 1.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = f[e] * inv;
+    // a NaN keeps its payload, whose low byte may be -128: it is made -127, below
+    // which no other value lies (bf16 NaNs have no such bits)
+    const float t = DT == DT_F32 ? fmaxf(f[e] * inv, -127.0f) : f[e] * inv;
     const float a = t + kMagic;
     u[e] = __float_as_uint(a);
     near = fminf(near, fabsf(fabsf(t - (a - kMagic)) - 0.5f));
@@ -244,14 +247,14 @@ __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(I8Params p) {
       } else {
         unpack8<DT>(raw[j], f);
       }
-      if (c < p.cols) *reinterpret_cast<uint2*>(out + c) = encode8(f, s, inv, fast);
+      if (c < p.cols) *reinterpret_cast<uint2*>(out + c) = encode8<DT>(f, s, inv, fast);
     }
   } else {
     for (int c = c0; c - lane * 8 < p.cols; c += STEP) {
       float f[8];
       unpack8<DT>(load8<DT>(p, row, c), f);
       if constexpr (HAD > 0) hadamard8<HAD>(f, lane);
-      if (c < p.cols) *reinterpret_cast<uint2*>(out + c) = encode8(f, s, inv, fast);
+      if (c < p.cols) *reinterpret_cast<uint2*>(out + c) = encode8<DT>(f, s, inv, fast);
     }
   }
 }
