@@ -188,8 +188,9 @@ __device__ __forceinline__ void dqp_body(const DqpParams& dp) {
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
     const int tiles_m = gs.tiles(p.tiles_m);
-    if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
-    tile_coords(blockIdx.x, tiles_m, p.tiles_n, dp.gm, tm, tn);
+    const int bid = block_index();
+    if (bid >= tiles_m * p.tiles_n) return;
+    tile_coords(bid, tiles_m, p.tiles_n, dp.gm, tm, tn);
     m0 = enter_group(p, gs, tm);
     if (m0 < 0) return;
   } else {
@@ -514,7 +515,7 @@ hipError_t launch_grouped(DqpParams dp, hipStream_t s) {
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
   dp.gm = 1;
   while (dp.gm * 2 <= dp.g.tiles_m && (int64_t)dp.gm * 2 * dp.gm * 2 <= (tiles + 7) / 8) dp.gm *= 2;
-  grouped_dqp_kernel<AK, WK, TM, TN, WGM, SLAB, WGN><<<(unsigned)tiles, 64 * WGM * WGN, 0, s>>>(dp);
+  grouped_dqp_kernel<AK, WK, TM, TN, WGM, SLAB, WGN><<<grid_of(tiles), 64 * WGM * WGN, 0, s>>>(dp);
   return hipGetLastError();
 }
 

@@ -46,7 +46,11 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_few_kernel(GemmP p) {
   __shared__ Acc part[kWaves][NT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
-  const int tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
+  const uint32_t bid = block_index();
+  const int tn = bid % (uint32_t)p.tiles_n, tm = bid / (uint32_t)p.tiles_n;
+  // in a plain product only the workgroups that fill the grid's last row are past
+  // the end (then of at most 16 rows): they compute and store nothing, since a
+  // test here would keep the arguments' loads behind it (5.0 -> 5.4 us for one token)
   int m0 = tm * 16;
   if constexpr (GRP) {
     m0 = enter_group(p, GroupScan(p.goff, p.groups, p.M, 16), tm);
@@ -201,7 +205,7 @@ hipError_t go(GemmP p, hipStream_t s) {
   p.tiles_n = (p.N + 16 * NT - 1) / (16 * NT);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  gemm_few_kernel<P, NT, GRP><<<(unsigned)tiles, 64 * kWaves, 0, s>>>(p);
+  gemm_few_kernel<P, NT, GRP><<<grid_of(tiles), 64 * kWaves, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -74,16 +74,18 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 || DEEP ? 2 : 4) void gemm
   __shared__ __attribute__((aligned(16))) uint8_t s0[kBuf], s1[kBuf], s2[kBuf], s3[kBuf], s4[kSlot];
   uint8_t* const slots[5] = {s0, s1, s2, s3, s4};
 
+  const int bid = block_index();
   int tm, tn, m0;
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TB);
     const int tiles_m = gs.tiles(p.tiles_m);
-    if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
-    tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
+    if (bid >= tiles_m * p.tiles_n) return;
+    tile_coords(bid, tiles_m, p.tiles_n, gm, tm, tn);
     m0 = enter_group(p, gs, tm);
     if (m0 < 0) return;
   } else {
-    tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, gm, tm, tn);
+    if (bid >= p.tiles_m * p.tiles_n) return;
+    tile_coords(bid, p.tiles_m, p.tiles_n, gm, tm, tn);
     m0 = tm * TB;
   }
   const int n0 = tn * TB;
@@ -386,7 +388,7 @@ hipError_t launch_ring(GemmP p, hipStream_t s) {
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
   int gm = 1;
   while (gm * 2 <= p.tiles_m && (int64_t)gm * 2 * gm * 2 <= (tiles + 7) / 8) gm *= 2;
-  const dim3 grid((unsigned)tiles);
+  const dim3 grid = grid_of(tiles);
   if (grp) gemm_i8_ring_kernel<T, false, true, DEEP><<<grid, 256, 0, s>>>(p, gm);
   else if (p.rank == 0) gemm_i8_ring_kernel<T, false, false, DEEP><<<grid, 256, 0, s>>>(p, gm);
   else if constexpr (T < 4) gemm_i8_ring_kernel<T, true, false, DEEP><<<grid, 256, 0, s>>>(p, gm);

@@ -76,8 +76,9 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
   if constexpr (GRP) {   // rows grouped by expert: the tile's group, then as one product
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
     const int tiles_m = gs.tiles(p.tiles_m);
-    if ((int)blockIdx.x >= tiles_m * p.tiles_n) return;
-    tile_coords(blockIdx.x, tiles_m, p.tiles_n, gm, tm, tn);
+    const int bid = block_index();
+    if (bid >= tiles_m * p.tiles_n) return;
+    tile_coords(bid, tiles_m, p.tiles_n, gm, tm, tn);
     m0 = enter_group(p, gs, tm);
     if (m0 < 0) return;
   } else {
@@ -322,6 +323,7 @@ hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
   p.tiles_m = p.goff ? (int)group_tiles_bound(p.M, p.groups, 32 * TM * WGM)
                      : (p.M + 32 * TM * WGM - 1) / (32 * TM * WGM);
   p.tiles_n = (p.N + 64 * TN - 1) / (64 * TN);
+  if ((int64_t)p.tiles_m * p.tiles_n > INT32_MAX) return hipErrorInvalidValue;
   const int tiles = p.tiles_m * p.tiles_n;
   // tile-rows per group: one XCD's share (tiles / 8) as a near-square block
   int gm = 1;
@@ -333,8 +335,8 @@ hipError_t launch_cfg(bool lr, GemmP p, hipStream_t s) {
                    reinterpret_cast<uintptr_t>(p.ws) % 16 == 0 && p.K % (2 * BK) == 0;
   const dim3 grid(tiles);
   if (p.goff) {
-    if (vsc) gemm_mx_kernel<TM, TN, WGM, SLAB, false, true, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
-    else gemm_mx_kernel<TM, TN, WGM, SLAB, false, false, true><<<grid, 128 * WGM, 0, s>>>(p, gm);
+    if (vsc) gemm_mx_kernel<TM, TN, WGM, SLAB, false, true, true><<<grid_of(tiles), 128 * WGM, 0, s>>>(p, gm);
+    else gemm_mx_kernel<TM, TN, WGM, SLAB, false, false, true><<<grid_of(tiles), 128 * WGM, 0, s>>>(p, gm);
     return hipGetLastError();
   }
   if (lr && vsc) gemm_mx_kernel<TM, TN, WGM, SLAB, true, true><<<grid, 128 * WGM, 0, s>>>(p, gm);

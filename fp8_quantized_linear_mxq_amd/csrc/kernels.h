@@ -6,6 +6,18 @@
 
 namespace mxq {
 
+// Grids of many workgroups: a launch holds fewer than 2**32 threads along x, and
+// cuts off what is more without an error.  From 2**22 workgroups on (of at most
+// 512 threads) they go in rows of that many; the last row's may be past the end,
+// where the kernel has nothing to do.  block_index() (device_common.h) is the
+// workgroup's number.
+constexpr int kGridRowBits = 22;
+inline dim3 grid_of(int64_t blocks) {
+  constexpr int64_t kRow = int64_t(1) << kGridRowBits;
+  if (blocks <= kRow) return dim3((unsigned)blocks);
+  return dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
+}
+
 struct LoraDownArgs {
   const uint16_t* x;   // bf16 [rows][ldx]
   int64_t rows, cols, ldx;

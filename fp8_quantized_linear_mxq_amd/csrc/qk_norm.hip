@@ -92,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_kernel(QkParams p) {
   const QkNormArgs& a = p.a;
   constexpr int HPW = 64 / LPH;   // heads of a wave at a time
   const int lane = threadIdx.x & 63;
-  const int64_t task = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const int64_t task = (int64_t)block_index() * (kThreads / 64) + (threadIdx.x >> 6);
   const int64_t tok = task / p.chunks;
   if (tok >= a.tokens) return;   // whole waves leave
   const int h0 = (int)(task - tok * p.chunks) * HPW * kHeads + lane / LPH;
@@ -191,7 +191,7 @@ hipError_t go(QkParams p, hipStream_t s) {
   p.chunks = (p.a.n_q + p.a.n_k + PER - 1) / PER;
   const int64_t waves = p.a.tokens * p.chunks, blocks = (waves + kThreads / 64 - 1) / (kThreads / 64);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  qk_norm_kernel<DT, INTER, LPH><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+  qk_norm_kernel<DT, INTER, LPH><<<grid_of(blocks), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(I8Params p) {
   constexpr int RPB = kThreads / 64 / WPR;   // rows per workgroup
   constexpr int STEP = WPR * 64 * 8;         // columns per piece of the row's waves
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row0 = (int64_t)blockIdx.x * RPB + wave / WPR;
+  const int64_t row0 = (int64_t)block_index() * RPB + wave / WPR;
   const bool live = row0 < p.rows;
   const int64_t row = live ? row0 : p.rows - 1;
   const int c0 = ((wave % WPR) * 64 + lane) * 8;
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(I8Params p) {
 template <int DT, int HAD, int J, int WPR>
 hipError_t go(const I8Params& p, hipStream_t s) {
   constexpr int RPB = kThreads / 64 / WPR;
-  quantize_i8_kernel<DT, HAD, J, WPR><<<(unsigned)((p.rows + RPB - 1) / RPB), kThreads, 0, s>>>(p);
+  quantize_i8_kernel<DT, HAD, J, WPR><<<grid_of((p.rows + RPB - 1) / RPB), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
