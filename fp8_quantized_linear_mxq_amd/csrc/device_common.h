@@ -20,8 +20,9 @@ enum : int { FMT_MXFP4 = 1, FMT_MXFP8 = 2, FMT_NVFP4 = 3, FMT_INT4 = 4, FMT_BF16
               FMT_INT8 = 6 };
 enum : int { DT_F32 = 1, DT_BF16 = 2 };
 
-// Number of this workgroup in a grid from grid_of(); fewer than 2**31.
-__device__ __forceinline__ int block_index() { return (int)((blockIdx.y << kGridRowBits) | blockIdx.x); }
+// Number of this workgroup in a grid from grid_of(), below 2**31.  Unsigned, so
+// that 64-bit divisions of it stay short ones.
+__device__ __forceinline__ uint32_t block_index() { return (blockIdx.y << kGridRowBits) | blockIdx.x; }
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b16) {
   return __uint_as_float(b16 << 16);

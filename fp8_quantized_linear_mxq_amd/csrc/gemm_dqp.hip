@@ -188,7 +188,7 @@ __device__ __forceinline__ void dqp_body(const DqpParams& dp) {
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
     const int tiles_m = gs.tiles(p.tiles_m);
-    const int bid = block_index();
+    const int bid = (int)block_index();
     if (bid >= tiles_m * p.tiles_n) return;
     tile_coords(bid, tiles_m, p.tiles_n, dp.gm, tm, tn);
     m0 = enter_group(p, gs, tm);

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : T == 2 || DEEP ? 2 : 4) void gemm
   __shared__ __attribute__((aligned(16))) uint8_t s0[kBuf], s1[kBuf], s2[kBuf], s3[kBuf], s4[kSlot];
   uint8_t* const slots[5] = {s0, s1, s2, s3, s4};
 
-  const int bid = block_index();
+  const int bid = (int)block_index();
   int tm, tn, m0;
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TB);

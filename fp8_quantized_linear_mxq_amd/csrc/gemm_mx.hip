@@ -76,7 +76,7 @@ __global__ __launch_bounds__(128 * WGM, 1) void gemm_mx_kernel(GemmP p, int gm) 
   if constexpr (GRP) {   // rows grouped by expert: the tile's group, then as one product
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
     const int tiles_m = gs.tiles(p.tiles_m);
-    const int bid = block_index();
+    const int bid = (int)block_index();
     if (bid >= tiles_m * p.tiles_n) return;
     tile_coords(bid, tiles_m, p.tiles_n, gm, tm, tn);
     m0 = enter_group(p, gs, tm);
