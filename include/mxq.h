@@ -327,9 +327,9 @@ mxq_status mxq_gemm_mixed(const mxq_qtensor* a, const mxq_qtensor* w_groups, int
  *  bias        optional device bf16 [n_groups][N].
  *  out         device bf16 [M][ld_out], N columns; 2-byte aligned.
  * K and row strides as in mxq_gemm, K not 0.  M = 0 or N = 0 is a no-op.
- * Error bound as in mxq_gemm.
- * The kernel is chosen by M / n_groups (few rows per expert: one that streams
- * the weights of the experts hit), never by what offsets holds.
+ * Error bound as in mxq_gemm; long K is summed in slabs here too.
+ * The kernel is chosen by the sizes (few rows per expert, or few output tiles:
+ * one that streams the weights of the experts hit), never by what offsets holds.
  */
 mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t n_groups,
                             const int32_t* offsets, const void* bias, void* out, int64_t ld_out,
