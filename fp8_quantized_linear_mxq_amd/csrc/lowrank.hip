@@ -21,7 +21,7 @@ constexpr int kMaxRank = 128;
 __global__ __launch_bounds__(256) void lora_down_kernel(LoraDownArgs a) {
   __shared__ float part[4][kRows][kMaxRank];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t m0 = (int64_t)blockIdx.x * kRows;
+  const int64_t m0 = (int64_t)block_index() * kRows;
   const int r16 = lane & 15, kq = lane >> 4;   // MFMA row / K-quarter of 8
   const int64_t row = m0 + r16 < a.rows ? m0 + r16 : a.rows - 1;
   const uint16_t* xr = a.x + row * a.ldx + kq * 8;
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void lora_down_kernel(LoraDownArgs a) {
 hipError_t launch_lora_down(const LoraDownArgs& a, hipStream_t s) {
   const int64_t blocks = (a.rows + kRows - 1) / kRows;
   if (blocks == 0) return hipSuccess;
-  lora_down_kernel<<<dim3((unsigned)blocks), 256, 0, s>>>(a);
+  lora_down_kernel<<<grid_of(blocks), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

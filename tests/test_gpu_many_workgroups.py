@@ -99,3 +99,17 @@ def test_grouped_many_experts(pair):
     want = (k * torch.exp2(kind.float())).bfloat16()[:, None]
     for r in range(0, groups, 512):
         assert bool((y[r:r + 512] == want[r:r + 512]).all()), f"rows from {r}"
+
+
+def test_quantize_lowrank():
+    """The projection of 270 million rows, 16 to a workgroup, next to the codes."""
+    room(100)
+    n = 270_000_000
+    gu.say(f"int8 quantize of {n} rows with a rank-16 projection")
+    block = torch.randn(1_000_000, 32, device="cuda").bfloat16()
+    l1t = torch.randn(16, 32, device="cuda").bfloat16()
+    u, want_u = torch.empty(n, 16, device="cuda"), torch.empty(len(block), 16, device="cuda")
+    want = mxq.quantize(block, mxq.INT8, l1t=l1t, u=want_u)
+    q = mxq.quantize(block.repeat(n // len(block), 1), mxq.INT8, l1t=l1t, u=u)
+    same_blocks(u, want_u)
+    same_blocks(q.codes, want.codes)
