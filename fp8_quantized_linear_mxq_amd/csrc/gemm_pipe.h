@@ -291,6 +291,15 @@ __device__ __forceinline__ void store_rows(const GemmP& p, int row0, int col0, i
   else store_pieces<1, ROWS, COLS, THREADS>(p, row0, col0, n_lim, tid, at);
 }
 
+// Makes what the epilogue derives from the lane its own, not values of the
+// prologue kept over the main loop: with eight MFMA tiles a wave has no register
+// for them (spills of the 256-row tiles 28 and 32 -> 16 and 12 bytes a thread, of
+// the MXFP4 ones 24-32 -> 20; smaller tiles spill more with it).
+__device__ __forceinline__ void fresh_lane(int& lane) {
+  asm volatile("" : "+v"(lane));
+  lane &= 63;
+}
+
 // Epilogue for the transposed accumulator layout: scales by alpha, adds the
 // low-rank branch (LR), the bias, and applies the column map.  `lds_region`:
 // 32 * (TN * 64 + 16) bytes private to the wave, for the staged row-wise stores.
@@ -298,6 +307,7 @@ template <bool LR, int TI, int TN>
 __device__ __forceinline__ void epilogue_tr(const GemmP& p, v16f (&acc)[TI][TN], float alpha,
                                             int row0, int col0, int lane,
                                             uint8_t* lds_region) {
+  if constexpr (TI * TN == 8) fresh_lane(lane);
   const int l32 = lane & 31, half = lane >> 5;
   if (alpha != 1.0f) {
 #pragma unroll
@@ -418,6 +428,7 @@ template <int TM, int TN, int WGM, int STAGE>
 __device__ __forceinline__ void epilogue_wg(const GemmP& p, v16f (&acc)[TM][TN], int m0, int n0,
                                             int wm, int wn, int lane, uint8_t* lo, uint8_t* hi) {
   constexpr int TBM = 32 * TM * WGM, TBN = 64 * TN, NT = 128 * WGM;
+  if constexpr (TM * TN == 8) fresh_lane(lane);
   constexpr int WRS = TBN * 2 + 16, CPR = TBN / 8;   // row stride; 16-byte pieces per row
   const int l32 = lane & 31, half = lane >> 5;
   const int n_lim = p.N < p.n_out ? p.N : p.n_out;
