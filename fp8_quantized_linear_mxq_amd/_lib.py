@@ -1,6 +1,6 @@
 """Binding of libmxq (include/mxq.h): ctypes, and for the calls that a model
-makes in every layer (quantize, gemm, gemm_grouped, qk_norm_rope) the
-marshalling module built from csrc/torch_binding.cpp.
+makes in every layer (quantize, gemm, gemm_grouped, qk_norm_rope, gemm_gated,
+layer_norm and their backward passes) the marshalling module built from csrc/torch_binding.cpp.
 
 Argument marshalling only: every step of the layer runs inside libmxq's HIP
 kernels.  PyTorch supplies device memory and the current stream.  If the
@@ -18,11 +18,16 @@ LIB_PATH = os.path.join(PKG, "libmxq.so")
 MXFP4, MXFP8, NVFP4, INT4 = 1, 2, 3, 4
 BF16 = 5   # unquantized bf16 activations (GEMM operand only)
 INT8 = 6   # row-wise int8, one fp32 scale per row
-FORMATS = {"MXFP4": MXFP4, "MXFP8": MXFP8, "NVFP4": NVFP4, "INT4": INT4, "INT8": INT8}
+FP8 = 7    # E4M3, one fp32 scale per row and 128 columns (activations)
+FP8_TILE = 8   # E4M3, one fp32 scale per 128 x 128 tile (weights)
+FORMATS = {"MXFP4": MXFP4, "MXFP8": MXFP8, "NVFP4": NVFP4, "INT4": INT4, "INT8": INT8, "FP8": FP8,
+           "FP8_TILE": FP8_TILE}
 FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 DT_F32, DT_BF16 = 1, 2
 OP_QUANTIZE, OP_GEMM, OP_SELECT, OP_QUANTIZE_MSE, OP_LOWRANK_SPLIT = 1, 2, 3, 4, 5
+OP_GATED_BACKWARD, OP_LAYER_NORM_BACKWARD = 6, 7
 BLOCK = {MXFP4: 32, MXFP8: 32, NVFP4: 16, INT4: 32}
+ACTIVATIONS = {"silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 STATUS = {0: "MXQ_OK", 1: "MXQ_ERR_INVALID_ARG", 2: "MXQ_ERR_UNSUPPORTED",
           3: "MXQ_ERR_ALIGNMENT", 4: "MXQ_ERR_SHAPE", 5: "MXQ_ERR_WORKSPACE",
@@ -31,6 +36,7 @@ STATUS = {0: "MXQ_OK", 1: "MXQ_ERR_INVALID_ARG", 2: "MXQ_ERR_UNSUPPORTED",
 # Every symbol include/mxq.h declares.
 EXPORTS = ("mxq_quantize", "mxq_quantize_noalloc", "mxq_quantize_lrp", "mxq_pack_l1t", "mxq_gemm", "mxq_gemm_mixed", "mxq_conv3x3_gemm_mixed",
            "mxq_gemm_grouped", "mxq_qk_norm_rope",
+           "mxq_gemm_gated", "mxq_gemm_gated_backward", "mxq_layer_norm", "mxq_layer_norm_backward",
            "mxq_select_format", "mxq_quantize_mse", "mxq_lowrank_split",
            "mxq_act_format_for_step", "mxq_workspace_size", "mxq_storage",
            "mxq_status_string", "mxq_version")
@@ -100,6 +106,14 @@ def load():
     lib.mxq_qk_norm_rope.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, vp, C.c_float, vp, vp, i64,
                                      i32, i32, vp, vp, i64, i64, vp, i64, i64, vp]
     lib.mxq_qk_norm_rope.restype = i32
+    lib.mxq_gemm_gated.argtypes = [qp, qp, qp, i32, vp, vp, i64, vp]
+    lib.mxq_gemm_gated.restype = i32
+    lib.mxq_gemm_gated_backward.argtypes = [vp, i64, qp, qp, qp, i32, vp, vp, i64, vp, vp, i64, vp, sz, vp]
+    lib.mxq_gemm_gated_backward.restype = i32
+    lib.mxq_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, C.c_float, vp, i64, vp, vp]
+    lib.mxq_layer_norm.restype = i32
+    lib.mxq_layer_norm_backward.argtypes = [vp, i64, vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, sz, vp]
+    lib.mxq_layer_norm_backward.restype = i32
     lib.mxq_conv3x3_gemm_mixed.argtypes = [qp, i64, i64, qp, i32, vp, vp, vp, i64, i64, vp, sz,
                                            vp]
     lib.mxq_conv3x3_gemm_mixed.restype = i32
@@ -123,8 +137,9 @@ def load():
     if _torch is not None:
         try:
             from . import _torch_binding
-            _torch_binding.bind(*[C.cast(f, vp).value for f in (lib.mxq_quantize, lib.mxq_gemm,
-                                                                lib.mxq_gemm_grouped, lib.mxq_qk_norm_rope)])
+            _torch_binding.bind(*[C.cast(f, vp).value for f in (
+                lib.mxq_quantize, lib.mxq_gemm, lib.mxq_gemm_grouped, lib.mxq_qk_norm_rope, lib.mxq_gemm_gated,
+                lib.mxq_gemm_gated_backward, lib.mxq_layer_norm, lib.mxq_layer_norm_backward, lib.mxq_workspace_size)])
             _fast = _torch_binding
         except ImportError as e:
             _fast = _NotBuilt(e)
@@ -149,6 +164,13 @@ def _stream(stream):
     if _torch.cuda.is_initialized():
         return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
     return _torch.cuda.current_stream().cuda_stream if _torch.cuda.is_available() else 0
+
+
+def _device(stream):
+    """The device that the call's stream belongs to (-1 without a GPU: no tensor is on it)."""
+    if stream is not None:
+        return stream.device_index
+    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -1
 
 
 def storage(fmt: int, cols: int):
@@ -199,6 +221,9 @@ def empty_qtensor(fmt: int, rows: int, cols: int, device="cuda") -> QTensor:
     codes = torch.empty((rows, (cb + 15) // 16 * 16), dtype=torch.uint8, device=device)
     if fmt == INT8:
         scales = torch.empty((rows, 1), dtype=torch.float32, device=device)
+    elif fmt in (FP8, FP8_TILE):   # K-blocks of all rows, or tiles
+        shape = (sb // 4, rows) if fmt == FP8 else ((rows + 127) // 128, sb // 4)
+        scales = torch.empty(shape, dtype=torch.float32, device=device)
     elif fmt == INT4:
         scales = torch.empty((rows, (sb // 4 + 3) // 4 * 4), dtype=torch.float32, device=device)
     else:
@@ -229,6 +254,27 @@ def int8_operand(codes, scales) -> QTensor:
             not (len(sshape) == 1 or (len(sshape) == 2 and sshape[1] == 1)):
         raise ValueError("int8_operand needs float32 scales of shape [rows] or [rows, 1]")
     return QTensor(INT8, rows, cols, codes, scales)
+
+
+_E4M3_TYPES = ("torch.float8_e4m3fn", "torch.uint8", "torch.int8")   # int8: their bits
+
+
+def fp8_operand(codes, scales, tile: bool = False) -> QTensor:
+    """E4M3 codes [rows, K] (cuda, row-major; float8_e4m3fn, or their bits as
+    uint8) as a quantized operand: activations with float32 scales
+    [ceil(K / 128), rows], or with ``tile`` weights with scales
+    [ceil(rows / 128), ceil(K / 128)]; rows of the scales contiguous."""
+    shape = codes.shape
+    if len(shape) != 2 or str(codes.dtype) not in _E4M3_TYPES or \
+            (codes.stride(1) != 1 and shape[1] > 1):
+        raise ValueError("fp8_operand needs row-major 2-D E4M3 codes")
+    rows, cols = shape
+    kb = (cols + 127) // 128
+    want = ((rows + 127) // 128, kb) if tile else (kb, rows)
+    if scales.element_size() != 4 or not scales.is_floating_point() or scales.shape != want or \
+            (scales.stride(1) != 1 and want[1] > 1):
+        raise ValueError(f"fp8_operand needs float32 scales of shape {list(want)}")
+    return QTensor(FP8_TILE if tile else FP8, rows, cols, codes, scales)
 
 
 def pack_l1t(l1t, stream=None):
@@ -374,6 +420,68 @@ def qk_norm_rope(x, n_q_heads: int, n_k_heads: int, head_dim: int, q_weight=None
                            eps, int(interleaved), q_out, k_out, _stream(stream))
     if type(r) is int:
         raise MxqError("mxq_qk_norm_rope", r)
+    return r
+
+
+def gemm_gated(x: QTensor, w_gate: QTensor, w_up: QTensor, act: str = "silu", saved=None, out=None, stream=None):
+    """mxq_gemm_gated: bf16 [rows, N] of act(x w_gate^T) * (x w_up^T), ``act``
+    one of ACTIVATIONS, on FP8 activations and FP8_TILE weights or on bf16
+    operands (bf16_operand).  ``saved``: a float32 tensor [2, rows, N] that
+    receives both products for gemm_gated_backward (bf16 only)."""
+    load()
+    if stream is not None and out is None:
+        with _torch.cuda.stream(stream):
+            return gemm_gated(x, w_gate, w_up, act, saved)
+    r = _fast.gemm_gated(x, w_gate, w_up, ACTIVATIONS.get(act, 0), saved, out, _device(stream), _stream(stream))
+    if type(r) is int:
+        raise MxqError("mxq_gemm_gated", r)
+    return r
+
+
+def gemm_gated_backward(dy, x: QTensor, w_gate: QTensor, w_up: QTensor, saved, act: str = "silu", dx=None,
+                        dw_gate=None, dw_up=None, want=(True, True), workspace=None, stream=None):
+    """mxq_gemm_gated_backward: (dx, dw_gate, dw_up) of gemm_gated on bf16
+    operands for the bf16 gradient ``dy`` [rows, N]; ``want``: whether dx and
+    the weights' gradients are formed (None in their place otherwise)."""
+    load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with _torch.cuda.stream(stream):
+            return gemm_gated_backward(dy, x, w_gate, w_up, saved, act, dx, dw_gate, dw_up, want, workspace)
+    r = _fast.gemm_gated_backward(dy, x, w_gate, w_up, ACTIVATIONS.get(act, 0), saved, int(want[0]), int(want[1]),
+                                  dx, dw_gate, dw_up, workspace, _device(None), _stream(None))
+    if type(r) is int:
+        raise MxqError("mxq_gemm_gated_backward", r)
+    return r
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, stats=None, out=None, stream=None):
+    """mxq_layer_norm over the rows of a 2-D tensor (float32 or bfloat16,
+    cuda), ``weight`` and ``bias`` [cols] of its dtype.  ``stats``: a float32
+    tensor [rows, 2] that receives each row's mean and reciprocal deviation
+    for layer_norm_backward."""
+    load()
+    if stream is not None and out is None:
+        with _torch.cuda.stream(stream):
+            return layer_norm(x, weight, bias, eps, stats)
+    r = _fast.layer_norm(x, weight, bias, eps, stats, out, _device(stream), _stream(stream))
+    if type(r) is int:
+        raise MxqError("mxq_layer_norm", r)
+    return r
+
+
+def layer_norm_backward(dy, x, stats, weight=None, want=(True, True), dx=None, dweight=None, dbias=None,
+                        workspace=None, stream=None):
+    """mxq_layer_norm_backward: (dx, dweight, dbias) for the gradient ``dy`` of
+    layer_norm's output; ``want``: whether dx and the parameters' gradients
+    are formed (None in their place otherwise)."""
+    load()
+    if stream is not None:   # what is allocated here belongs to the stream that writes it
+        with _torch.cuda.stream(stream):
+            return layer_norm_backward(dy, x, stats, weight, want, dx, dweight, dbias, workspace)
+    r = _fast.layer_norm_backward(dy, x, stats, weight, int(want[0]), int(want[1]), dx, dweight, dbias, workspace,
+                                  _device(None), _stream(None))
+    if type(r) is int:
+        raise MxqError("mxq_layer_norm_backward", r)
     return r
 
 

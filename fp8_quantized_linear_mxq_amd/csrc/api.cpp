@@ -22,17 +22,22 @@ int block_of(int fmt) { return fmt == MXQ_FMT_NVFP4 ? 16 : 32; }
 
 // The quantized formats (BF16, unquantized activations, is separate).
 bool known_fmt(int fmt) {
-  return (fmt >= MXQ_FMT_MXFP4 && fmt <= MXQ_FMT_INT4) || fmt == MXQ_FMT_INT8;
+  return (fmt >= MXQ_FMT_MXFP4 && fmt <= MXQ_FMT_INT4) || fmt == MXQ_FMT_INT8 || fmt == MXQ_FMT_FP8 ||
+         fmt == MXQ_FMT_FP8_TILE;
 }
+
+// E4M3 codes with fp32 scales per block of 128.
+bool fp8(int fmt) { return fmt == MXQ_FMT_FP8 || fmt == MXQ_FMT_FP8_TILE; }
 
 int64_t code_bytes(int fmt, int64_t cols) {
   if (fmt == MXQ_FMT_BF16) return 2 * cols;
-  return fmt == MXQ_FMT_MXFP8 || fmt == MXQ_FMT_INT8 ? cols : cols / 2;
+  return fmt == MXQ_FMT_MXFP8 || fmt == MXQ_FMT_INT8 || fp8(fmt) ? cols : cols / 2;
 }
 
 int64_t scale_bytes(int fmt, int64_t cols) {
   if (fmt == MXQ_FMT_BF16) return 0;
   if (fmt == MXQ_FMT_INT8) return 4;   // one fp32 per row
+  if (fp8(fmt)) return (cols + 127) / 128 * 4;
   const int64_t blocks = cols / block_of(fmt);
   return fmt == MXQ_FMT_INT4 ? blocks * 4 : blocks;
 }
@@ -55,8 +60,9 @@ mxq_status check_qtensor(const mxq_qtensor* t) {
   if (t->rows == 0 || t->cols == 0) return MXQ_OK;
   if (!t->codes || !t->scales) return MXQ_ERR_INVALID_ARG;
   if (t->fmt == MXQ_FMT_NVFP4 && !t->tensor_scale) return MXQ_ERR_INVALID_ARG;
-  if (t->ld_codes < code_bytes(t->fmt, t->cols) || t->ld_scales < scale_bytes(t->fmt, t->cols))
-    return MXQ_ERR_INVALID_ARG;
+  // FP8 scales: K-blocks [K / 128] of all rows
+  const int64_t scale_row = t->fmt == MXQ_FMT_FP8 ? 4 * t->rows : scale_bytes(t->fmt, t->cols);
+  if (t->ld_codes < code_bytes(t->fmt, t->cols) || t->ld_scales < scale_row) return MXQ_ERR_INVALID_ARG;
   if (!aligned(t->codes, 16) || t->ld_codes % 16 || !aligned(t->scales, 4) || t->ld_scales % 4)
     return MXQ_ERR_ALIGNMENT;
   if (t->fmt == MXQ_FMT_INT4 && (!aligned(t->scales, 16) || t->ld_scales % 16))
@@ -65,7 +71,9 @@ mxq_status check_qtensor(const mxq_qtensor* t) {
 }
 
 constexpr int64_t kMaxKInt8 = 1 << 17, kMaxLdInt8 = 1 << 24;
+constexpr int64_t kMaxLd = 1 << 24;   // bytes between rows, FP8 and the gated products
 constexpr int32_t kMaxGroups = 1 << 16;
+constexpr int64_t kMaxNormCols = 1 << 26;
 
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
@@ -155,6 +163,13 @@ int64_t mxq_workspace_size(int32_t op, int64_t rows, int64_t cols, int32_t fmt) 
       // rows = N, cols = K, fmt = the rank
       if (fmt < 1 || fmt > 128 || fmt > rows || fmt > cols) return -1;
       return lowrank_split_workspace(rows, cols, fmt);
+    case MXQ_OP_GATED_BACKWARD:
+      // rows = M, cols = N
+      if (rows > INT32_MAX / 2 || cols > kMaxLd / 4 - 64) return -1;
+      return gated_backward_workspace(rows, cols);
+    case MXQ_OP_LAYER_NORM_BACKWARD:
+      if (cols > kMaxNormCols) return -1;
+      return (int64_t)kLayerNormGroups * 2 * cols * 4;
     case MXQ_OP_QUANTIZE_MSE:
       if (fmt != MXQ_FMT_MXFP4 && fmt != MXQ_FMT_NVFP4) return -1;
       return mse_workspace_bytes(fmt, rows);
@@ -211,7 +226,9 @@ static mxq_status quantize_impl(const void* x, int32_t dtype, int64_t rows, int6
   }
   // the fused kernel that reads the packed L1 writes block formats
   if (packed && out->fmt == MXQ_FMT_INT8) return MXQ_ERR_UNSUPPORTED;
-  if (out->fmt == MXQ_FMT_INT8 && (rows > INT32_MAX || cols > INT32_MAX)) return MXQ_ERR_SHAPE;
+  // the product of FP8 operands has no low-rank branch
+  if (fp8(out->fmt) && lr_rank > 0) return MXQ_ERR_UNSUPPORTED;
+  if ((out->fmt == MXQ_FMT_INT8 || fp8(out->fmt)) && (rows > INT32_MAX || cols > INT32_MAX)) return MXQ_ERR_SHAPE;
   const bool dynamic_nv = out->fmt == MXQ_FMT_NVFP4 && !static_tensor_scale;
   if (!noalloc && dynamic_nv && (!workspace || ws_bytes < (size_t)kAmaxPartials * 4))
     return MXQ_ERR_WORKSPACE;
@@ -259,6 +276,7 @@ static mxq_status quantize_impl(const void* x, int32_t dtype, int64_t rows, int6
     a.lr = &l;
   }
   hipError_t e = out->fmt == MXQ_FMT_INT8 ? launch_quantize_i8(a, as_stream(stream))
+                 : fp8(out->fmt)          ? launch_quantize_fp8(a, as_stream(stream))
                                           : launch_quantize(a, as_stream(stream));
   return from_hip(e);
 }
@@ -318,9 +336,15 @@ static mxq_status gemm_checks(const mxq_qtensor* a, const mxq_qtensor* w, const 
     return MXQ_ERR_UNSUPPORTED;
   const bool i8 = a->fmt == MXQ_FMT_INT8;
   if (i8 != (w->fmt == MXQ_FMT_INT8)) return MXQ_ERR_UNSUPPORTED;
+  // FP8 rows against FP8 tiles, without the low-rank branch
+  const bool f8 = a->fmt == MXQ_FMT_FP8;
+  if (a->fmt == MXQ_FMT_FP8_TILE || w->fmt == MXQ_FMT_FP8 || f8 != (w->fmt == MXQ_FMT_FP8_TILE))
+    return MXQ_ERR_UNSUPPORTED;
+  if (f8 && lr_rank > 0) return MXQ_ERR_UNSUPPORTED;
   if (a->rows == 0 || w->rows == 0 || n_out == 0) return MXQ_OK;
   // int8 sums stay within int32 up to K = 2**17
-  if (i8 ? a->cols == 0 || a->cols > kMaxKInt8 : a->cols % 128 != 0) return MXQ_ERR_SHAPE;
+  if (f8 ? a->cols == 0 : i8 ? a->cols == 0 || a->cols > kMaxKInt8 : a->cols % 128 != 0) return MXQ_ERR_SHAPE;
+  if (f8 && (a->ld_codes > kMaxLd || w->ld_codes > kMaxLd)) return MXQ_ERR_SHAPE;
   if (i8 && (a->ld_codes > kMaxLdInt8 || w->ld_codes > kMaxLdInt8)) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX || w->rows > INT32_MAX || a->cols > INT32_MAX || n_out > INT32_MAX)
     return MXQ_ERR_SHAPE;
@@ -384,6 +408,7 @@ static hipError_t gemm_launch(const mxq_qtensor* a, const mxq_qtensor* w, const 
   g.cv_w = cv_w;
   g.cv_c = cv_c;
   if (a->fmt == MXQ_FMT_INT8) return few_rows(g) ? launch_gemm_few(g, s) : launch_gemm_i8(g, s);
+  if (a->fmt == MXQ_FMT_FP8) return launch_gemm_fp8(g, s);
   // E2M1 x E2M1 is exact on the scaled MFMA; every other pair is dequantized
   // exactly to 16-bit operands (E4M3 MFMA products are not summed to fp32
   // accuracy on this hardware)
@@ -450,10 +475,13 @@ mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t 
   if (a->cols != w->cols || w->rows % n_groups) return MXQ_ERR_SHAPE;
   const bool i8 = a->fmt == MXQ_FMT_INT8 && w->fmt == MXQ_FMT_INT8;
   const bool w4 = w->fmt == MXQ_FMT_MXFP4 && (a->fmt == MXQ_FMT_MXFP4 || a->fmt == MXQ_FMT_BF16);
-  if (!i8 && !w4) return MXQ_ERR_UNSUPPORTED;
+  const bool f8 = a->fmt == MXQ_FMT_FP8 && w->fmt == MXQ_FMT_FP8_TILE;
+  if (!i8 && !w4 && !f8) return MXQ_ERR_UNSUPPORTED;
   const int64_t n = w->rows / n_groups;
+  if (f8 && n % 128) return MXQ_ERR_SHAPE;   // an expert's tiles are its own
   if (a->rows == 0 || n == 0) return MXQ_OK;
-  if (a->cols == 0 || (i8 ? a->cols > kMaxKInt8 : a->cols % 128 != 0)) return MXQ_ERR_SHAPE;
+  if (a->cols == 0 || (i8 ? a->cols > kMaxKInt8 : !f8 && a->cols % 128 != 0)) return MXQ_ERR_SHAPE;
+  if (f8 && (a->ld_codes > kMaxLd || w->ld_codes > kMaxLd)) return MXQ_ERR_SHAPE;
   if (i8 && (a->ld_codes > kMaxLdInt8 || w->ld_codes > kMaxLdInt8)) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX / 2 || w->rows > INT32_MAX || a->cols > INT32_MAX) return MXQ_ERR_SHAPE;
   if (!offsets || !out || ld_out < n) return MXQ_ERR_INVALID_ARG;
@@ -466,6 +494,7 @@ mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t 
   g.goff = offsets;
   g.groups = n_groups;
   const hipStream_t s = as_stream(stream);
+  if (f8) return from_hip(launch_gemm_fp8(g, s));
   if (few_rows(g)) return from_hip(launch_gemm_few(g, s));
   if (i8) return from_hip(launch_gemm_i8(g, s));
   return from_hip(a->fmt == MXQ_FMT_MXFP4 ? launch_gemm_mx(g, s) : launch_gemm_dqp(g, s));
@@ -528,6 +557,164 @@ mxq_status mxq_qk_norm_rope(const void* x, int32_t dtype, int64_t tokens, int64_
   return from_hip(launch_qk_norm_rope(a, as_stream(stream)));
 }
 
+// The operands of the gated products: x [M, K] and the weights of both
+// projections [N, K], of one pair of formats.
+static mxq_status gated_checks(const mxq_qtensor* x, const mxq_qtensor* wg, const mxq_qtensor* wu, int32_t act) {
+  for (const mxq_qtensor* t : {x, wg, wu}) {
+    const mxq_status st = check_qtensor(t);
+    if (st != MXQ_OK) return st;
+  }
+  if (act < MXQ_ACT_SILU || act > MXQ_ACT_GELU_TANH) return MXQ_ERR_INVALID_ARG;
+  if (wg->fmt != wu->fmt || !((x->fmt == MXQ_FMT_BF16 && wg->fmt == MXQ_FMT_BF16) ||
+                              (x->fmt == MXQ_FMT_FP8 && wg->fmt == MXQ_FMT_FP8_TILE)))
+    return MXQ_ERR_UNSUPPORTED;
+  if (x->cols != wg->cols || x->cols != wu->cols || wg->rows != wu->rows) return MXQ_ERR_SHAPE;
+  if (x->cols % 8) return MXQ_ERR_SHAPE;   // bf16: whole 16-byte pieces of a row
+  if (x->rows > INT32_MAX / 2 || wg->rows > kMaxLd / 4 - 64 || x->cols > INT32_MAX) return MXQ_ERR_SHAPE;
+  for (const mxq_qtensor* t : {x, wg, wu})
+    if (t->ld_codes > kMaxLd) return MXQ_ERR_SHAPE;
+  return MXQ_OK;
+}
+
+mxq_status mxq_gemm_gated(const mxq_qtensor* x, const mxq_qtensor* w_gate, const mxq_qtensor* w_up, int32_t act,
+                          float* saved, void* out, int64_t ld_out, void* stream) {
+  mxq_status st = gated_checks(x, w_gate, w_up, act);
+  if (st != MXQ_OK) return st;
+  if (saved && x->fmt != MXQ_FMT_BF16) return MXQ_ERR_UNSUPPORTED;
+  if (x->rows == 0 || w_gate->rows == 0) return MXQ_OK;
+  if (x->cols == 0) return MXQ_ERR_SHAPE;
+  const int64_t n = w_gate->rows;
+  if (!out || ld_out < n) return MXQ_ERR_INVALID_ARG;
+  if (!aligned(out, 2) || !aligned(saved, 4)) return MXQ_ERR_ALIGNMENT;
+  unsigned* dbg = nullptr;
+  st = device_entry(&dbg);
+  if (st != MXQ_OK) return st;
+  GatedArgs g;
+  g.g = gemm_args(x, w_gate, nullptr, nullptr, 0, nullptr, 0, nullptr, out, ld_out, n, nullptr, 0);
+  g.w2_codes = static_cast<const uint8_t*>(w_up->codes);
+  g.ldw2 = w_up->ld_codes;
+  g.w2_scales = static_cast<const uint8_t*>(w_up->scales);
+  g.ld_ws2 = w_up->ld_scales;
+  g.act = act;
+  g.gate = saved;
+  g.up = saved ? saved + x->rows * n : nullptr;
+  g.ld_saved = n;
+  return from_hip(x->fmt == MXQ_FMT_FP8 ? launch_gated_fp8(g, as_stream(stream)) : launch_gated_bf16(g, as_stream(stream)));
+}
+
+mxq_status mxq_gemm_gated_backward(const void* dy, int64_t ld_dy, const mxq_qtensor* x, const mxq_qtensor* w_gate,
+                                   const mxq_qtensor* w_up, int32_t act, const float* saved, void* dx, int64_t ld_dx,
+                                   void* dw_gate, void* dw_up, int64_t ld_dw, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  mxq_status st = gated_checks(x, w_gate, w_up, act);
+  if (st != MXQ_OK) return st;
+  if (x->fmt != MXQ_FMT_BF16) return MXQ_ERR_UNSUPPORTED;
+  if (!dw_gate != !dw_up) return MXQ_ERR_INVALID_ARG;   // one product forms both
+  const int64_t m = x->rows, n = w_gate->rows, k = x->cols;
+  if (k == 0 || (!dx && !dw_gate)) return MXQ_OK;
+  if ((dx && ld_dx < k) || (dw_gate && ld_dw < k)) return MXQ_ERR_INVALID_ARG;
+  if (!aligned(dx, 2) || !aligned(dw_gate, 2) || !aligned(dw_up, 2)) return MXQ_ERR_ALIGNMENT;
+  const bool empty = m == 0 || n == 0;
+  if (!empty) {
+    if (!dy || ld_dy < n || !saved) return MXQ_ERR_INVALID_ARG;
+    if (!aligned(dy, 2) || !aligned(saved, 4)) return MXQ_ERR_ALIGNMENT;
+    if (!workspace || ws_bytes < (size_t)gated_backward_workspace(m, n) || !aligned(workspace, 16))
+      return MXQ_ERR_WORKSPACE;
+  }
+  unsigned* dbg = nullptr;
+  st = device_entry(&dbg);
+  if (st != MXQ_OK) return st;
+  GatedBwdArgs g;
+  g.dy = static_cast<const uint16_t*>(dy);
+  g.ld_dy = ld_dy;
+  g.x = static_cast<const uint8_t*>(x->codes);
+  g.ldx = x->ld_codes;
+  g.wg = static_cast<const uint8_t*>(w_gate->codes);
+  g.wu = static_cast<const uint8_t*>(w_up->codes);
+  g.ldw = w_gate->ld_codes;
+  g.ldw2 = w_up->ld_codes;
+  g.gate = saved;
+  g.up = saved ? saved + m * n : nullptr;
+  g.ld_saved = n;
+  g.M = m;
+  g.N = n;
+  g.K = k;
+  g.act = act;
+  g.dx = static_cast<uint16_t*>(dx);
+  g.ld_dx = ld_dx;
+  g.dwg = static_cast<uint16_t*>(dw_gate);
+  g.dwu = static_cast<uint16_t*>(dw_up);
+  g.ld_dw = ld_dw;
+  g.ws = workspace;
+  return from_hip(launch_gated_backward(g, as_stream(stream)));
+}
+
+mxq_status mxq_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const void* weight,
+                          const void* bias, float eps, void* y, int64_t ldy, float* stats, void* stream) {
+  if ((dtype != MXQ_DT_F32 && dtype != MXQ_DT_BF16) || rows < 0 || cols < 0 || !(eps >= 0.f))
+    return MXQ_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return MXQ_OK;
+  if (rows > INT32_MAX || cols > kMaxNormCols) return MXQ_ERR_SHAPE;
+  if (!x || !y || ldx < cols || ldy < cols) return MXQ_ERR_INVALID_ARG;
+  const uintptr_t esz = dtype == MXQ_DT_F32 ? 4 : 2;
+  if (!aligned(x, esz) || !aligned(y, esz) || !aligned(weight, esz) || !aligned(bias, esz) || !aligned(stats, 8))
+    return MXQ_ERR_ALIGNMENT;
+  unsigned* dbg = nullptr;
+  const mxq_status st = device_entry(&dbg);
+  if (st != MXQ_OK) return st;
+  LayerNormArgs a;
+  a.x = x;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.weight = weight;
+  a.bias = bias;
+  a.eps = eps;
+  a.y = y;
+  a.ldy = ldy;
+  a.stats = stats;
+  return from_hip(launch_layer_norm(a, as_stream(stream)));
+}
+
+mxq_status mxq_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int32_t dtype, int64_t rows,
+                                   int64_t cols, int64_t ldx, const float* stats, const void* weight, void* dx,
+                                   int64_t ld_dx, void* dweight, void* dbias, void* workspace, size_t ws_bytes,
+                                   void* stream) {
+  if ((dtype != MXQ_DT_F32 && dtype != MXQ_DT_BF16) || rows < 0 || cols < 0) return MXQ_ERR_INVALID_ARG;
+  const bool params = dweight || dbias;
+  if (cols == 0 || (!params && (!dx || rows == 0))) return MXQ_OK;
+  if (rows > INT32_MAX || cols > kMaxNormCols) return MXQ_ERR_SHAPE;
+  const uintptr_t esz = dtype == MXQ_DT_F32 ? 4 : 2;
+  if (rows > 0) {
+    if (!dy || !x || !stats || ld_dy < cols || ldx < cols || (dx && ld_dx < cols)) return MXQ_ERR_INVALID_ARG;
+    if (!aligned(dy, esz) || !aligned(x, esz) || !aligned(dx, esz) || !aligned(weight, esz) || !aligned(stats, 8))
+      return MXQ_ERR_ALIGNMENT;
+  }
+  if (!aligned(dweight, esz) || !aligned(dbias, esz)) return MXQ_ERR_ALIGNMENT;
+  if (params && (!workspace || ws_bytes < (size_t)kLayerNormGroups * 2 * cols * 4 || !aligned(workspace, 16)))
+    return MXQ_ERR_WORKSPACE;
+  unsigned* dbg = nullptr;
+  const mxq_status st = device_entry(&dbg);
+  if (st != MXQ_OK) return st;
+  LayerNormBwdArgs a;
+  a.dy = dy;
+  a.ld_dy = ld_dy;
+  a.x = x;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.stats = stats;
+  a.weight = weight;
+  a.dx = dx;
+  a.ld_dx = ld_dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.partial = params ? static_cast<float*>(workspace) : nullptr;
+  return from_hip(launch_layer_norm_bwd(a, as_stream(stream)));
+}
+
 mxq_status mxq_conv3x3_gemm_mixed(const mxq_qtensor* x, int64_t height, int64_t width,
                                   const mxq_qtensor* w_groups, int32_t n_groups,
                                   const int32_t* w_perm, const void* bias, void* out,
@@ -537,7 +724,7 @@ mxq_status mxq_conv3x3_gemm_mixed(const mxq_qtensor* x, int64_t height, int64_t 
   mxq_status st = check_qtensor(x);
   if (st != MXQ_OK) return st;
   if (height <= 0 || width <= 0 || n_out < 0) return MXQ_ERR_INVALID_ARG;
-  if (x->fmt == MXQ_FMT_INT4 || x->fmt == MXQ_FMT_BF16 || x->fmt == MXQ_FMT_INT8)
+  if (x->fmt == MXQ_FMT_INT4 || x->fmt == MXQ_FMT_BF16 || x->fmt == MXQ_FMT_INT8 || fp8(x->fmt))
     return MXQ_ERR_UNSUPPORTED;
   if (workspace && !aligned(workspace, 16)) return MXQ_ERR_ALIGNMENT;
   if (height > INT32_MAX / width) return MXQ_ERR_SHAPE;
@@ -551,7 +738,7 @@ mxq_status mxq_conv3x3_gemm_mixed(const mxq_qtensor* x, int64_t height, int64_t 
     const mxq_qtensor* w = &w_groups[g];
     st = check_qtensor(w);
     if (st != MXQ_OK) return st;
-    if (w->fmt == MXQ_FMT_MXFP8 || w->fmt == MXQ_FMT_BF16 || w->fmt == MXQ_FMT_INT8)
+    if (w->fmt == MXQ_FMT_MXFP8 || w->fmt == MXQ_FMT_BF16 || w->fmt == MXQ_FMT_INT8 || fp8(w->fmt))
       return MXQ_ERR_UNSUPPORTED;
     // the scaled-MFMA route (MXFP4 x MXFP4) reads no implicit im2col
     if (x->fmt == MXQ_FMT_MXFP4 && w->fmt == MXQ_FMT_MXFP4 && w->rows > 0)

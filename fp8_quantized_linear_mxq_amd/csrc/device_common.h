@@ -17,7 +17,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 // Format identifiers (same values as mxq_format in mxq.h).
 enum : int { FMT_MXFP4 = 1, FMT_MXFP8 = 2, FMT_NVFP4 = 3, FMT_INT4 = 4, FMT_BF16 = 5,
-              FMT_INT8 = 6 };
+              FMT_INT8 = 6, FMT_FP8 = 7, FMT_FP8_TILE = 8 };
 enum : int { DT_F32 = 1, DT_BF16 = 2 };
 
 // Number of this workgroup in a grid from grid_of(), below 2**31.  Unsigned, so

@@ -61,6 +61,10 @@ hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t s);
 // The same for FMT_INT8: one fp32 scale per row, rows ld_scales bytes apart.
 hipError_t launch_quantize_i8(const QuantizeArgs& a, hipStream_t s);
 
+// The same for FMT_FP8 (scales [K / 128][rows], K-blocks ld_scales bytes apart) and
+// FMT_FP8_TILE ([rows / 128][K / 128]).
+hipError_t launch_quantize_fp8(const QuantizeArgs& a, hipStream_t s);
+
 // Device address and size of the current device's scratch array for the
 // allocation-free quantize (the NVFP4 amax partials).
 hipError_t quantize_scratch(void** out, size_t* bytes);
@@ -132,6 +136,62 @@ struct QkNormArgs {
   void* k; int64_t k_token, k_head;
 };
 hipError_t launch_qk_norm_rope(const QkNormArgs& a, hipStream_t s);
+
+// E4M3 codes with block scales, plain or grouped by expert.
+hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t s);
+
+// y = f(a w^T) * (a w2^T): g holds the operands and the output of the gate's
+// product, w2 the up projection's weights.
+struct GatedArgs {
+  GemmArgs g;
+  const uint8_t* w2_codes; int64_t ldw2;
+  const uint8_t* w2_scales; int64_t ld_ws2;
+  int act;
+  float* gate; float* up; int64_t ld_saved;   // fp32 pre-activations, or null
+};
+hipError_t launch_gated_fp8(const GatedArgs& a, hipStream_t s);
+hipError_t launch_gated_bf16(const GatedArgs& a, hipStream_t s);
+
+// Gradients of the bf16 form.  Null outputs are left out.
+struct GatedBwdArgs {
+  const uint16_t* dy; int64_t ld_dy;             // elements
+  const uint8_t* x; int64_t ldx;                 // bytes
+  const uint8_t* wg; const uint8_t* wu; int64_t ldw, ldw2;
+  const float* gate; const float* up; int64_t ld_saved;
+  int64_t M, N, K;
+  int act;
+  uint16_t* dx; int64_t ld_dx;
+  uint16_t* dwg; uint16_t* dwu; int64_t ld_dw;
+  void* ws;                                      // gated_backward_workspace() bytes
+};
+int64_t gated_backward_workspace(int64_t M, int64_t N);
+hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t s);
+
+// Layer norm of the rows of a matrix; weight, bias and stats may be null.
+struct LayerNormArgs {
+  const void* x; int dtype;
+  int64_t rows, cols, ldx;
+  const void* weight; const void* bias;
+  float eps;
+  void* y; int64_t ldy;
+  float* stats;            // [rows][2]: mean, 1 / standard deviation
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
+
+constexpr int kLayerNormGroups = 512;   // workgroups of the backward pass, at most
+// Null gradients are left out; partial (null without dweight and dbias):
+// kLayerNormGroups * 2 * cols floats.
+struct LayerNormBwdArgs {
+  const void* dy; int64_t ld_dy;
+  const void* x; int dtype;
+  int64_t rows, cols, ldx;
+  const float* stats;
+  const void* weight;
+  void* dx; int64_t ld_dx;
+  void* dweight; void* dbias;
+  float* partial;
+};
+hipError_t launch_layer_norm_bwd(const LayerNormBwdArgs& a, hipStream_t s);
 
 struct SelectArgs {
   const void* w; int dtype;

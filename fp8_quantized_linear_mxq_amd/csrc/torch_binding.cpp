@@ -1,5 +1,6 @@
 // Argument marshalling of the per-layer entry points for Python callers:
-// quantize, gemm, gemm_grouped and qk_norm_rope on torch tensors.
+// quantize, gemm, gemm_grouped, qk_norm_rope, gemm_gated, layer_norm and the two
+// backward passes on torch tensors.
 //
 // A decode step makes one such call per layer, and there the time of the call
 // on the host is what counts: quantize, gemm, gemm_grouped and qk_norm_rope of
@@ -13,6 +14,7 @@
 #include <Python.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
@@ -25,6 +27,11 @@ decltype(&mxq_quantize) g_quantize;
 decltype(&mxq_gemm) g_gemm;
 decltype(&mxq_gemm_grouped) g_grouped;
 decltype(&mxq_qk_norm_rope) g_qk;
+decltype(&mxq_gemm_gated) g_gated;
+decltype(&mxq_gemm_gated_backward) g_gated_bwd;
+decltype(&mxq_layer_norm) g_norm;
+decltype(&mxq_layer_norm_backward) g_norm_bwd;
+decltype(&mxq_workspace_size) g_ws_size;
 
 PyObject *s_fmt, *s_rows, *s_cols, *s_codes, *s_scales, *s_tensor_scale;
 
@@ -98,8 +105,8 @@ struct Operand : mxq_qtensor {
     reserved = 0;
     if (t_tensor_scale.defined() && !one_float(&t_tensor_scale, "an operand's tensor_scale is a float32 tensor")) return false;
     tensor_scale = static_cast<float*>(t_tensor_scale.defined() ? t_tensor_scale.data_ptr() : nullptr);
-    return side(t_codes, code_bytes(), code_type(), &codes, &ld_codes) &&
-           side(t_scales, scale_bytes(), scale_type(), &scales, &ld_scales);
+    return side(t_codes, rows, code_bytes(), code_type(), &codes, &ld_codes) &&
+           side(t_scales, scale_rows(), scale_bytes(), scale_type(), &scales, &ld_scales);
   }
 
  private:
@@ -109,7 +116,7 @@ struct Operand : mxq_qtensor {
     const int64_t k = std::min(cols, kMaxCols);
     switch (fmt) {
       case MXQ_FMT_BF16: return 2 * k;
-      case MXQ_FMT_MXFP8: case MXQ_FMT_INT8: return k;
+      case MXQ_FMT_MXFP8: case MXQ_FMT_INT8: case MXQ_FMT_FP8: case MXQ_FMT_FP8_TILE: return k;
       case MXQ_FMT_MXFP4: case MXQ_FMT_NVFP4: case MXQ_FMT_INT4: return k / 2;
       default: return 0;
     }
@@ -118,6 +125,8 @@ struct Operand : mxq_qtensor {
     const int64_t k = std::min(cols, kMaxCols);
     switch (fmt) {
       case MXQ_FMT_INT8: return 4;
+      case MXQ_FMT_FP8: return 4 * std::min(rows, kMaxCols);
+      case MXQ_FMT_FP8_TILE: return (k + 127) / 128 * 4;
       case MXQ_FMT_INT4: return k / 32 * 4;
       case MXQ_FMT_NVFP4: return k / 16;
       case MXQ_FMT_MXFP4: case MXQ_FMT_MXFP8: return k / 32;
@@ -125,12 +134,19 @@ struct Operand : mxq_qtensor {
     }
   }
 
+  // Rows of the scales: one per row, K-block (FP8) or 128 rows (FP8_TILE).
+  int64_t scale_rows() const {
+    return fmt == MXQ_FMT_FP8 ? (std::min(cols, kMaxCols) + 127) / 128 : fmt == MXQ_FMT_FP8_TILE ? rows / 128 + (rows % 128 > 0) : rows;
+  }
+
   // Codes and the scale codes of the block formats are bytes under any type but
   // the wider floating ones, whose values would be taken for them; bf16
   // operands, integers and fp32 scales are what they say.
   enum Type { kBytes, kBits16, kInt8, kFloat32 };
   Type code_type() const { return fmt == MXQ_FMT_BF16 ? kBits16 : fmt == MXQ_FMT_INT8 ? kInt8 : kBytes; }
-  Type scale_type() const { return fmt == MXQ_FMT_INT8 || fmt == MXQ_FMT_INT4 ? kFloat32 : kBytes; }
+  Type scale_type() const {
+    return fmt == MXQ_FMT_INT8 || fmt == MXQ_FMT_INT4 || fmt == MXQ_FMT_FP8 || fmt == MXQ_FMT_FP8_TILE ? kFloat32 : kBytes;
+  }
   static bool is(const at::Tensor& t, Type ty) {
     const auto s = t.scalar_type();
     switch (ty) {
@@ -141,11 +157,11 @@ struct Operand : mxq_qtensor {
     }
   }
 
-  bool side(const at::Tensor& t, int64_t need, Type type, void** p, int64_t* bytes) {
+  bool side(const at::Tensor& t, int64_t n, int64_t need, Type type, void** p, int64_t* bytes) {
     *p = nullptr;
     *bytes = 0;
     if (!t.defined()) return true;
-    if (t.dim() < 1 || t.size(0) < rows) return fail("an operand's codes and scales have its rows");
+    if (t.dim() < 1 || t.size(0) < n) return fail("an operand's codes and scales have its rows");
     *p = t.data_ptr();
     *bytes = t.stride(0) * (int64_t)t.element_size();
     if (rows <= 0 || cols <= 0) return true;
@@ -157,7 +173,7 @@ struct Operand : mxq_qtensor {
       row *= t.size(d);
     }
     // a single row may have any stride: it is given one that the library takes
-    if (rows == 1) *bytes = (row + 15) / 16 * 16;
+    if (n == 1) *bytes = (row + 15) / 16 * 16;
     return row >= need || fail("an operand's codes and scales are as wide as its columns");
   }
 };
@@ -396,16 +412,249 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(quantize, gemm, gemm_grouped, qk_norm_rope): the addresses of the C ABI
+// Whether all of them (null and undefined ones aside) are on device `dev`, whose stream the call uses.
+bool on_device(int64_t dev, std::initializer_list<const at::Tensor*> ts) {
+  for (const at::Tensor* t : ts)
+    if (t && t->defined() && t->get_device() != dev) return fail("tensors are on the device of the call's stream");
+  return true;
+}
+
+PyObject* give(at::Tensor& made, PyObject* given) {
+  if (made.defined()) return THPVariable_Wrap(std::move(made));
+  Py_INCREF(given);
+  return given;
+}
+
+PyObject* pack3(PyObject* a, PyObject* b, PyObject* c) {
+  PyObject* r = a && b && c ? PyTuple_Pack(3, a, b, c) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  Py_XDECREF(c);
+  return r;
+}
+
+// gemm_gated(x, w_gate, w_up, act, saved, out, device, stream) -> out or status
+PyObject* gemm_gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand x, g, u;
+    const at::Tensor *saved, *out;
+    int64_t act, dev, stream;
+    if (!count(n, 8) || !x.read(a[0]) || !g.read(a[1]) || !u.read(a[2]) || !to_i64(a[3], &act) ||
+        !to_tensor(a[4], &saved, "saved is a tensor") || !to_tensor(a[5], &out, "out is a tensor") ||
+        !to_i64(a[6], &dev) || !to_i64(a[7], &stream))
+      return nullptr;
+    if (!x.t_codes.defined()) {
+      fail("gemm_gated needs the operand's codes");
+      return nullptr;
+    }
+    if (saved && (saved->scalar_type() != at::kFloat || !saved->is_contiguous() || saved->dim() != 3 ||
+                  saved->size(0) != 2 || saved->size(1) != x.rows || saved->size(2) != g.rows)) {
+      fail("saved is a contiguous float32 tensor [2, rows, outputs]");
+      return nullptr;
+    }
+    if ((out && !output(*out, x.rows, g.rows)) ||
+        !on_device(dev, {&x.t_codes, &x.t_scales, &g.t_codes, &g.t_scales, &u.t_codes, &u.t_scales, saved, out}))
+      return nullptr;
+    at::Tensor made;
+    if (!out) {
+      made = bf16_like(x.t_codes, {x.rows, g.rows});
+      out = &made;
+    }
+    mxq_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_gated(&x, &g, &u, (int32_t)act, static_cast<float*>(ptr(saved)), out->data_ptr(), ld(*out),
+                 reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    if (st != MXQ_OK) return PyLong_FromLong(st);
+    return give(made, a[5]);
+  });
+}
+
+// gemm_gated_backward(dy, x, w_gate, w_up, act, saved, want_dx, want_dw, dx, dw_gate, dw_up, ws, device, stream)
+// -> (dx, dw_gate, dw_up), None for those not wanted, or status
+PyObject* gemm_gated_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Operand x, g, u;
+    const at::Tensor *dy, *saved, *dx, *dg, *du, *ws;
+    int64_t act, want_dx, want_dw, dev, stream;
+    if (!count(n, 14) || !to_tensor(a[0], &dy, "dy is a tensor") || !x.read(a[1]) || !g.read(a[2]) || !u.read(a[3]) ||
+        !to_i64(a[4], &act) || !to_tensor(a[5], &saved, "saved is a tensor") || !to_i64(a[6], &want_dx) ||
+        !to_i64(a[7], &want_dw) || !to_tensor(a[8], &dx, "dx is a tensor") || !to_tensor(a[9], &dg, "dw_gate is a tensor") ||
+        !to_tensor(a[10], &du, "dw_up is a tensor") || !to_tensor(a[11], &ws, "workspace is a tensor") ||
+        !to_i64(a[12], &dev) || !to_i64(a[13], &stream))
+      return nullptr;
+    auto refuse = [](const char* what) -> PyObject* {
+      fail(what);
+      return nullptr;
+    };
+    const int64_t rows = x.rows, outs = g.rows, k = x.cols;
+    if (!x.t_codes.defined() || !dy || dy->scalar_type() != at::kBFloat16 || !row_major(*dy) || dy->size(0) != rows ||
+        dy->size(1) != outs)
+      return refuse("gemm_gated_backward: dy is a row-major bfloat16 tensor [rows, outputs]");
+    if (!saved || saved->scalar_type() != at::kFloat || !saved->is_contiguous() || saved->dim() != 3 ||
+        saved->size(0) != 2 || saved->size(1) != rows || saved->size(2) != outs)
+      return refuse("saved is a contiguous float32 tensor [2, rows, outputs]");
+    at::Tensor mx, mg, mu, mw;
+    auto gradient = [&](const at::Tensor*& t, at::Tensor& made, int64_t want, int64_t r) {
+      if (!want) {
+        t = nullptr;
+      } else if (!t) {
+        made = bf16_like(x.t_codes, {r, k});
+        t = &made;
+      } else if (!output(*t, r, k)) {
+        return false;
+      }
+      return true;
+    };
+    if (!gradient(dx, mx, want_dx, rows) || !gradient(dg, mg, want_dw, outs) || !gradient(du, mu, want_dw, outs)) return nullptr;
+    if (dg && outs > 1 && ld(*dg) != ld(*du)) return refuse("dw_gate and dw_up have one row stride");
+    const int64_t need = g_ws_size(MXQ_OP_GATED_BACKWARD, rows, outs, 0);
+    if (!ws && need > 0) {
+      mw = at::empty({need}, x.t_codes.options().dtype(at::kByte).requires_grad(false));
+      ws = &mw;
+    }
+    if (ws && !ws->is_contiguous()) return refuse("the workspace is a contiguous tensor");
+    if (!on_device(dev, {dy, &x.t_codes, &g.t_codes, &u.t_codes, saved, dx, dg, du, ws})) return nullptr;
+    mxq_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_gated_bwd(dy->data_ptr(), ld(*dy), &x, &g, &u, (int32_t)act, static_cast<const float*>(ptr(saved)), ptr(dx),
+                     dx ? ld(*dx) : 0, ptr(dg), ptr(du), dg ? ld(*dg) : 0, ptr(ws), ws ? ws->nbytes() : 0,
+                     reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    if (st != MXQ_OK) return PyLong_FromLong(st);
+    return pack3(give(mx, want_dx ? a[8] : Py_None), give(mg, want_dw ? a[9] : Py_None), give(mu, want_dw ? a[10] : Py_None));
+  });
+}
+
+bool norm_param(const at::Tensor* t, const at::Tensor& x, const char* what) {
+  return !t || (t->scalar_type() == x.scalar_type() && t->dim() == 1 && t->size(0) == x.size(1) && t->is_contiguous()) ||
+         fail(what);
+}
+
+bool norm_rows(const at::Tensor* t, const at::Tensor& x, const char* what) {
+  return !t || (t->scalar_type() == x.scalar_type() && row_major(*t) && t->sizes() == x.sizes()) || fail(what);
+}
+
+bool norm_input(const at::Tensor* x) {
+  return (x && (x->scalar_type() == at::kBFloat16 || x->scalar_type() == at::kFloat) && row_major(*x)) ||
+         fail("layer_norm needs a row-major 2-D float32 or bfloat16 tensor");
+}
+
+bool norm_stats(const at::Tensor* t, const at::Tensor& x) {
+  return !t || (t->scalar_type() == at::kFloat && t->is_contiguous() && t->dim() == 2 && t->size(0) == x.size(0) &&
+                t->size(1) == 2) || fail("stats is a contiguous float32 tensor [rows, 2]");
+}
+
+// layer_norm(x, weight, bias, eps, stats, out, device, stream) -> out or status
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *x, *w, *b, *stats, *out;
+    int64_t dev, stream;
+    if (!count(n, 8) || !to_tensor(a[0], &x, "x is a tensor") || !to_tensor(a[1], &w, "weight is a tensor") ||
+        !to_tensor(a[2], &b, "bias is a tensor") || !to_tensor(a[4], &stats, "stats is a tensor") ||
+        !to_tensor(a[5], &out, "out is a tensor") || !to_i64(a[6], &dev) || !to_i64(a[7], &stream))
+      return nullptr;
+    const double eps = PyFloat_AsDouble(a[3]);
+    if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+    if (!norm_input(x) || !norm_param(w, *x, "weight is a contiguous [cols] tensor of x's dtype") ||
+        !norm_param(b, *x, "bias is a contiguous [cols] tensor of x's dtype") || !norm_stats(stats, *x) ||
+        !norm_rows(out, *x, "out is a row-major tensor of x's dtype and size") || !on_device(dev, {x, w, b, stats, out}))
+      return nullptr;
+    at::Tensor made;
+    if (!out) {
+      made = at::empty(x->sizes(), x->options().requires_grad(false).memory_format(at::MemoryFormat::Contiguous));
+      out = &made;
+    }
+    mxq_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_norm(x->data_ptr(), x->scalar_type() == at::kFloat ? MXQ_DT_F32 : MXQ_DT_BF16, x->size(0), x->size(1), ld(*x),
+                ptr(w), ptr(b), (float)eps, out->data_ptr(), ld(*out), static_cast<float*>(ptr(stats)),
+                reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    if (st != MXQ_OK) return PyLong_FromLong(st);
+    return give(made, a[5]);
+  });
+}
+
+// layer_norm_backward(dy, x, stats, weight, want_dx, want_params, dx, dweight, dbias, ws, device, stream)
+// -> (dx, dweight, dbias), None for those not wanted, or status
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *dy, *x, *stats, *w, *dx, *dw, *db, *ws;
+    int64_t want_dx, want_p, dev, stream;
+    if (!count(n, 12) || !to_tensor(a[0], &dy, "dy is a tensor") || !to_tensor(a[1], &x, "x is a tensor") ||
+        !to_tensor(a[2], &stats, "stats is a tensor") || !to_tensor(a[3], &w, "weight is a tensor") ||
+        !to_i64(a[4], &want_dx) || !to_i64(a[5], &want_p) || !to_tensor(a[6], &dx, "dx is a tensor") ||
+        !to_tensor(a[7], &dw, "dweight is a tensor") || !to_tensor(a[8], &db, "dbias is a tensor") ||
+        !to_tensor(a[9], &ws, "workspace is a tensor") || !to_i64(a[10], &dev) || !to_i64(a[11], &stream))
+      return nullptr;
+    if (!norm_input(x)) return nullptr;
+    if (!dy || !stats) {
+      fail("layer_norm_backward needs dy and stats");
+      return nullptr;
+    }
+    if (!norm_rows(dy, *x, "dy is a row-major tensor of x's dtype and size") || !norm_stats(stats, *x) ||
+        !norm_param(w, *x, "weight is a contiguous [cols] tensor of x's dtype"))
+      return nullptr;
+    const auto opt = x->options().requires_grad(false);
+    at::Tensor mx, mw, mb, ms;
+    if (!want_dx) dx = nullptr;
+    if (!want_p) dw = db = nullptr;
+    if (want_dx && !dx) {
+      mx = at::empty(x->sizes(), opt.memory_format(at::MemoryFormat::Contiguous));
+      dx = &mx;
+    }
+    if (want_p && !dw) {
+      mw = at::empty({x->size(1)}, opt);
+      dw = &mw;
+    }
+    if (want_p && !db) {
+      mb = at::empty({x->size(1)}, opt);
+      db = &mb;
+    }
+    if (!norm_rows(dx, *x, "dx is a row-major tensor of x's dtype and size") ||
+        !norm_param(dw, *x, "dweight is a contiguous [cols] tensor of x's dtype") ||
+        !norm_param(db, *x, "dbias is a contiguous [cols] tensor of x's dtype"))
+      return nullptr;
+    if (want_p && !ws) {
+      const int64_t need = g_ws_size(MXQ_OP_LAYER_NORM_BACKWARD, x->size(0), x->size(1), 0);
+      if (need > 0) {
+        ms = at::empty({need}, opt.dtype(at::kByte));
+        ws = &ms;
+      }
+    }
+    if (ws && !ws->is_contiguous()) {
+      fail("the workspace is a contiguous tensor");
+      return nullptr;
+    }
+    if (!on_device(dev, {dy, x, stats, w, dx, dw, db, ws})) return nullptr;
+    mxq_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_norm_bwd(dy->data_ptr(), ld(*dy), x->data_ptr(), x->scalar_type() == at::kFloat ? MXQ_DT_F32 : MXQ_DT_BF16,
+                    x->size(0), x->size(1), ld(*x), static_cast<const float*>(ptr(stats)), ptr(w), ptr(dx),
+                    dx ? ld(*dx) : 0, ptr(dw), ptr(db), ptr(ws), ws ? ws->nbytes() : 0, reinterpret_cast<void*>(stream));
+    Py_END_ALLOW_THREADS
+    if (st != MXQ_OK) return PyLong_FromLong(st);
+    return pack3(give(mx, want_dx ? a[6] : Py_None), give(mw, want_p ? a[7] : Py_None), give(mb, want_p ? a[8] : Py_None));
+  });
+}
+
+// bind(quantize, gemm, gemm_grouped, qk_norm_rope, gemm_gated, gemm_gated_backward, layer_norm,
+// layer_norm_backward, workspace_size): the addresses of the C ABI
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  int64_t p[4];
-  if (!count(n, 4)) return nullptr;
-  for (int i = 0; i < 4; ++i)
+  int64_t p[9];
+  if (!count(n, 9)) return nullptr;
+  for (int i = 0; i < 9; ++i)
     if (!to_i64(a[i], &p[i])) return nullptr;
   g_quantize = reinterpret_cast<decltype(g_quantize)>(p[0]);
   g_gemm = reinterpret_cast<decltype(g_gemm)>(p[1]);
   g_grouped = reinterpret_cast<decltype(g_grouped)>(p[2]);
   g_qk = reinterpret_cast<decltype(g_qk)>(p[3]);
+  g_gated = reinterpret_cast<decltype(g_gated)>(p[4]);
+  g_gated_bwd = reinterpret_cast<decltype(g_gated_bwd)>(p[5]);
+  g_norm = reinterpret_cast<decltype(g_norm)>(p[6]);
+  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[7]);
+  g_ws_size = reinterpret_cast<decltype(g_ws_size)>(p[8]);
   Py_RETURN_NONE;
 }
 
@@ -416,7 +665,9 @@ constexpr PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {
     method<bind>("bind"), method<quantize>("quantize"), method<empty_int8>("empty_int8"), method<gemm>("gemm"),
-    method<gemm_grouped>("gemm_grouped"), method<qk_norm_rope>("qk_norm_rope"), {nullptr, nullptr, 0, nullptr}};
+    method<gemm_grouped>("gemm_grouped"), method<qk_norm_rope>("qk_norm_rope"), method<gemm_gated>("gemm_gated"),
+    method<gemm_gated_backward>("gemm_gated_backward"), method<layer_norm>("layer_norm"),
+    method<layer_norm_backward>("layer_norm_backward"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -12,7 +12,11 @@
  *   and the timestep-bucket activation-format lookup             (mxq_act_format_for_step)
  * and, next to it, the 8-bit integer layer (the same two entry points with
  * MXQ_FMT_INT8), products grouped by expert (mxq_gemm_grouped) and the norms of
- * query and key heads with the position rotation (mxq_qk_norm_rope).
+ * query and key heads with the position rotation (mxq_qk_norm_rope); and a
+ * feed-forward block for training in bf16 and serving on 8-bit floating point
+ * codes: the layer norm in front of it (mxq_layer_norm), both gated projections in
+ * one product (mxq_gemm_gated), with their gradients, and the FP8 layer (mxq_quantize
+ * and mxq_gemm with MXQ_FMT_FP8 and MXQ_FMT_FP8_TILE).
  *
  * Sources (pages the method is described on, cited by title and section):
  *  - "Bridging the Gap Between Promise and Performance for Microscaling FP4
@@ -36,6 +40,9 @@
  *   INT4   symmetric two's-complement int4, one fp32 scale per 32 (weights)
  *   INT8   symmetric two's-complement int8, one fp32 scale per row (activations
  *          and weights of the 8-bit layer)
+ *   FP8      E4M3 elements, one fp32 scale per row and 128 columns (activations)
+ *   FP8_TILE E4M3 elements, one fp32 scale per tile of 128 rows x 128 columns
+ *          (weights); a last block or tile may be narrower
  * Rounding: nearest, ties to even, saturating at the largest finite value,
  * decided on the exact real quotient.  Scale rules:
  *   MX     e = clamp(floor(log2 amax) - emax_elem, -127, 127), code e + 127,
@@ -44,12 +51,16 @@
  *   INT4   s = RN_fp32(amax / 7); q = clamp(RNE(x / s), -7, 7).
  *   INT8   s = RN_fp32(row amax / 127); q = clamp(RNE(x / s), -127, 127);
  *          s = 0 gives q = 0.
+ *   FP8    s = RN_fp32(block amax / 448); q = RN_E4M3(x / s); s = 0 gives q = 0.
  *
  * Storage (all device memory, row-major, K contiguous):
  *   codes   4-bit formats: [rows][K/2] bytes, element 2i in the low nibble
- *           of byte i; MXFP8, INT8: [rows][K] bytes.
+ *           of byte i; MXFP8, INT8, FP8, FP8_TILE: [rows][K] bytes.
  *   scales  MX: [rows][K/32] E8M0 bytes; NVFP4: [rows][K/16] E4M3 bytes;
- *           INT4: [rows][K/32] fp32; INT8: [rows][1] fp32.
+ *           INT4: [rows][K/32] fp32; INT8: [rows][1] fp32; FP8: [ceil(K/128)]
+ *           [rows] fp32, the rows of a K-block together (the product reads one
+ *           per lane, so a wave's read is one line); FP8_TILE: [ceil(rows/128)]
+ *           [ceil(K/128)] fp32.
  *   tensor_scale  NVFP4 only: one fp32 in device memory.
  * Weights, like nn.Linear, are stored [out][in] with the reduction index
  * contiguous: W [N][K], the low-rank factors as L1^T [r][K] and L2^T [N][r].
@@ -120,8 +131,17 @@ typedef enum mxq_format {
   MXQ_FMT_BF16 = 5,
   /* Row-wise int8: two's-complement codes in [-127, 127], one fp32 scale per
    * row (an activation token, or a weight's output channel). */
-  MXQ_FMT_INT8 = 6
+  MXQ_FMT_INT8 = 6,
+  /* E4M3 codes with one fp32 scale per row and block of 128 columns: scales
+   * [ceil(cols/128)][rows], ld_scales bytes between blocks of columns. */
+  MXQ_FMT_FP8 = 7,
+  /* The same per tile of 128 x 128: scales [ceil(rows/128)][ceil(cols/128)]. */
+  MXQ_FMT_FP8_TILE = 8
 } mxq_format;
+
+/* The gate of mxq_gemm_gated: g / (1 + e^-g), g (1 + erf(g / sqrt 2)) / 2, and
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2. */
+typedef enum mxq_activation { MXQ_ACT_SILU = 1, MXQ_ACT_GELU = 2, MXQ_ACT_GELU_TANH = 3 } mxq_activation;
 
 typedef enum mxq_dtype { MXQ_DT_F32 = 1, MXQ_DT_BF16 = 2 } mxq_dtype;
 
@@ -134,7 +154,8 @@ typedef struct mxq_qtensor {
   void* codes;           /* device; 16-byte aligned                         */
   int64_t ld_codes;      /* bytes between rows; multiple of 16              */
   void* scales;          /* device; 4-byte aligned                          */
-  int64_t ld_scales;     /* bytes between rows; multiple of 4               */
+  int64_t ld_scales;     /* bytes between rows (FP8: between K-blocks,
+                            FP8_TILE: between rows of tiles); multiple of 4 */
   float* tensor_scale;   /* NVFP4: device pointer to g; otherwise NULL      */
 } mxq_qtensor;
 
@@ -174,7 +195,8 @@ typedef struct mxq_qtensor {
  *  workspace   device scratch of mxq_workspace_size(MXQ_OP_QUANTIZE, ...)
  *              bytes (only dynamic NVFP4 needs any).
  * Returns MXQ_ERR_SHAPE when cols is not a multiple of 32 (for NVFP4 too:
- * its 16-blocks are quantized in pairs) or of hadamard_n.  rows == 0 or
+ * its 16-blocks are quantized in pairs) or of hadamard_n.  FP8 and FP8_TILE have
+ * no low-rank projection (MXQ_ERR_UNSUPPORTED).  rows == 0 or
  * cols == 0 is a no-op: MXQ_OK once the checks that need no data have passed
  * (dtype, out's format and sizes, hadamard_n, lr_rank's range, the column
  * multiples); pointers, alignment, the workspace and the conditions of the
@@ -246,7 +268,8 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  *
  *  a           quantized activations [M, K]: MXFP4, MXFP8 or NVFP4; or
  *              unquantized bf16 activations (MXQ_FMT_BF16), taken exactly; or
- *              INT8 (with INT8 weights only).
+ *              INT8 (with INT8 weights only); or FP8 (with FP8_TILE weights
+ *              only, no low-rank branch).
  *  w           quantized weights [N, K]: MXFP4, NVFP4 or INT4; or INT8 with
  *              INT8 activations (one scale per token and per output channel;
  *              the integer sum is exact).  Every other pair
@@ -260,6 +283,12 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  *              dequantizes exactly; in exchange MXFP8 blocks must have scale
  *              codes <= 236 (block amax below 2**117) and MXFP4 blocks codes
  *              <= 250 (amax below 2**126).
+ * FP8 x FP8_TILE runs on the E4M3 matrix cores, which add the products of one
+ * instruction to about 2**-15 of the largest: each K-block of 128 is summed by
+ * itself, scaled by its two scales and added in fp32.  Its bound is
+ * |y - y_exact| <= 2**-10 P + 1e-5 S + 2**-8 |y_exact| + 2**-133 with P the sum over
+ * K-blocks of the largest |a w| of each (on normal data the sums are 2e-5 of
+ * their rms off, a hundredth of the output rounding).
  * Error bound: |y - y_exact| <= 1e-5 (1 + 2**-8) S + 2**-8 |y_exact| + 2**-133
  * with S = alpha sum_k |a w| + sum_j |u_j L2_jn| (the last two terms are the
  * bf16 output rounding, 2**-133 covering subnormal outputs).
@@ -284,7 +313,8 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  *              within the same error bound).  Otherwise, and for every other
  *              route and with a low-rank branch, it is unused.
  * Requirements: a->cols == w->cols == K, K a multiple of 128; INT8: K a
- * multiple of 32, 32 .. 2**17, row strides at most 2**24 bytes.
+ * multiple of 32, 32 .. 2**17, row strides at most 2**24 bytes; FP8: K a multiple
+ * of 32, not 0, row strides at most 2**24 bytes.
  * M or N of 0 is a no-op.  Accumulation is fp32; long K is summed in slabs.
  */
 mxq_status mxq_gemm(const mxq_qtensor* a, const mxq_qtensor* w, const int32_t* w_out_col,
@@ -313,9 +343,10 @@ mxq_status mxq_gemm_mixed(const mxq_qtensor* a, const mxq_qtensor* w_groups, int
  * expert, each group of rows multiplied by its own weights,
  *   out[m] = RN_bf16(Q(a_m) Q(W_e)^T + bias_e)  for offsets[e] <= m < offsets[e+1].
  *
- *  a           activations [M, K]: INT8, MXFP4 or bf16 (MXQ_FMT_BF16).
+ *  a           activations [M, K]: INT8, MXFP4, bf16 (MXQ_FMT_BF16) or FP8.
  *  w           weights [n_groups * N, K], expert e in rows [e N, (e + 1) N):
- *              INT8 with INT8 activations, else MXFP4.  Other pairs are
+ *              INT8 with INT8 activations, FP8_TILE with FP8 ones (N a multiple of
+ *              128, so that no tile spans two experts), else MXFP4.  Other pairs are
  *              MXQ_ERR_UNSUPPORTED.  The domain of bf16 x MXFP4 is mxq_gemm's.
  *  n_groups    1 .. 65536; must divide w->rows (else MXQ_ERR_SHAPE).
  *  offsets     device int32 [n_groups + 1], non-decreasing, in [0, M]; read on
@@ -370,6 +401,84 @@ mxq_status mxq_qk_norm_rope(const void* x, int32_t dtype, int64_t tokens, int64_
                             void* q_out, int64_t q_token_stride, int64_t q_head_stride,
                             void* k_out, int64_t k_token_stride, int64_t k_head_stride,
                             void* stream);
+
+/*
+ * mxq_gemm_gated -- both projections of a gated feed-forward block, the
+ * activation and their product, in one kernel:
+ *   g = x Wg^T,  u = x Wu^T,  out = RN_bf16(f(g) * u).
+ *
+ *  x           activations [M, K]: FP8, or bf16 (MXQ_FMT_BF16).
+ *  w_gate, w_up  weights [N, K]: FP8_TILE with FP8 activations, bf16 with bf16
+ *              ones (other pairs are MXQ_ERR_UNSUPPORTED).  Parts of one matrix
+ *              are given as such: any row strides.
+ *  act         f, an mxq_activation.
+ *  saved       bf16 only (else MXQ_ERR_UNSUPPORTED): NULL, or device fp32
+ *              [2][M][N] that receives g and u for the backward pass.
+ *  out         device bf16 [M][ld_out], N columns; 2-byte aligned.
+ * K is not 0 and a multiple of 8 (FP8: of 32); row strides at most 2**24 bytes.
+ * M or N of 0 is a no-op.  g and u are fp32 sums (FP8: as in mxq_gemm); g, u and
+ * f(g) u are not rounded before the output.
+ */
+mxq_status mxq_gemm_gated(const mxq_qtensor* x, const mxq_qtensor* w_gate, const mxq_qtensor* w_up, int32_t act,
+                          float* saved, void* out, int64_t ld_out, void* stream);
+
+/*
+ * mxq_gemm_gated_backward -- the gradients of the bf16 form:
+ *   dg = dy u f'(g),  du = dy f(g),  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+ *
+ *  dy          device bf16 [M][ld_dy], N columns; 2-byte aligned.
+ *  x, w_gate, w_up, act  as in mxq_gemm_gated, bf16.
+ *  saved       what mxq_gemm_gated left there.
+ *  dx          device bf16 [M][ld_dx], K columns, or NULL.
+ *  dw_gate, dw_up  device bf16 [N][ld_dw], K columns; both or neither.
+ *  workspace   mxq_workspace_size(MXQ_OP_GATED_BACKWARD, M, N, 0) bytes of device
+ *              memory, 16-byte aligned: dg and du in bf16 (their one rounding
+ *              before the sums), which calls that overlap in time cannot share.
+ * Without terms (N = 0 for dx, M = 0 for the weights) a gradient is zero.  A
+ * padded row's gradients are zero where its dy is zero, provided its x, g and u
+ * are finite.
+ */
+mxq_status mxq_gemm_gated_backward(const void* dy, int64_t ld_dy, const mxq_qtensor* x, const mxq_qtensor* w_gate,
+                                   const mxq_qtensor* w_up, int32_t act, const float* saved, void* dx, int64_t ld_dx,
+                                   void* dw_gate, void* dw_up, int64_t ld_dw, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * mxq_layer_norm -- norm of every row of x [rows, cols]:
+ *   y = (x - mean) / sqrt(var + eps) * weight + bias,
+ * var the mean square of the deviations; all in fp32, one rounding to dtype.
+ *
+ *  x, y        device, dtype elements, row strides ldx, ldy (elements, >= cols);
+ *              y may be x with its stride.
+ *  weight, bias  device [cols] of dtype, or NULL for ones and zeros.
+ *  eps         >= 0.
+ *  stats       NULL, or device fp32 [rows][2], 8-byte aligned: mean and
+ *              1 / sqrt(var + eps) of each row, for the backward pass.
+ * Any cols up to 2**26; rows at 16-byte alignment with cols and strides multiples
+ * of 8 are the fast case.  rows or cols of 0 is a no-op.
+ */
+mxq_status mxq_layer_norm(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const void* weight,
+                          const void* bias, float eps, void* y, int64_t ldy, float* stats, void* stream);
+
+/*
+ * mxq_layer_norm_backward -- its gradients, with h = (x - mean) rstd, t = dy weight:
+ *   dx = rstd (t - mean(t) - h mean(t h)),  dweight = sum over rows of dy h,
+ *   dbias = sum over rows of dy.
+ *
+ *  dy, x, dx   device, dtype elements, row strides in elements; dx may be NULL, or
+ *              dy or x with its stride.
+ *  stats       what mxq_layer_norm left there.
+ *  weight      as given to mxq_layer_norm.
+ *  dweight, dbias  device [cols] of dtype, or NULL.  Zeros when rows is 0.
+ *  workspace   with dweight or dbias: mxq_workspace_size(MXQ_OP_LAYER_NORM_BACKWARD,
+ *              rows, cols, 0) bytes of device memory, 16-byte aligned (the sums of
+ *              each workgroup; added in a fixed order, so results are
+ *              deterministic); calls that overlap in time cannot share it.
+ */
+mxq_status mxq_layer_norm_backward(const void* dy, int64_t ld_dy, const void* x, int32_t dtype, int64_t rows,
+                                   int64_t cols, int64_t ldx, const float* stats, const void* weight, void* dx,
+                                   int64_t ld_dx, void* dweight, void* dbias, void* workspace, size_t ws_bytes,
+                                   void* stream);
 
 /*
  * mxq_conv3x3_gemm_mixed -- a 3x3, stride-1, zero-padding-1 convolution as the
@@ -498,17 +607,20 @@ int32_t mxq_act_format_for_step(const uint8_t* table, int32_t n_layers, int32_t 
 
 /* Operations for mxq_workspace_size. */
 enum { MXQ_OP_QUANTIZE = 1, MXQ_OP_GEMM = 2, MXQ_OP_SELECT = 3, MXQ_OP_QUANTIZE_MSE = 4,
-       MXQ_OP_LOWRANK_SPLIT = 5 };
+       MXQ_OP_LOWRANK_SPLIT = 5, MXQ_OP_GATED_BACKWARD = 6, MXQ_OP_LAYER_NORM_BACKWARD = 7 };
 
 /* Workspace bytes an operation needs for a [rows, cols] operand of format
  * fmt (0 when none); for MXQ_OP_GEMM rows = M, cols = N (weight rows) and
  * fmt = the weight format (the optional split-K workspace); for
- * MXQ_OP_LOWRANK_SPLIT rows = n, cols = k and fmt = the rank.  Returns -1 for
+ * MXQ_OP_LOWRANK_SPLIT rows = n, cols = k and fmt = the rank; for
+ * MXQ_OP_GATED_BACKWARD rows = M, cols = N; for MXQ_OP_LAYER_NORM_BACKWARD the
+ * norm's rows and cols (fmt is not read for these two).  Returns -1 for
  * unknown arguments.  Host-only. */
 int64_t mxq_workspace_size(int32_t op, int64_t rows, int64_t cols, int32_t fmt);
 
 /* Per-row storage of a format with cols elements per row: code bytes and
- * scale bytes (the minimum ld_codes / ld_scales).  Returns MXQ_ERR_SHAPE if
+ * scale bytes (the minimum ld_codes / ld_scales; FP8: the scales of one row, which
+ * lie apart, and for FP8_TILE those of one row of tiles).  Returns MXQ_ERR_SHAPE if
  * cols is not a multiple of the format's block.  Host-only. */
 mxq_status mxq_storage(int32_t fmt, int64_t cols, int64_t* code_bytes, int64_t* scale_bytes);
 
