@@ -32,6 +32,8 @@ Module map:
   hadamard  Sylvester block-diagonal Hadamard rotation
   gemm      dequantized fp64 linear layer (+ low-rank branch) and its tolerance
   int8      row-wise int8 quantizer
+  fp8       E4M3 quantizer with float32 scales per block of 128, product tolerance
+  feed_forward  gated projections and layer norm with their gradients
   heads     per-head RMS norm with the position rotation
   select    per-output-channel format choice by minimum reconstruction error
   mse_scales  least-squared-error block (and NVFP4 tensor) scales for weights
