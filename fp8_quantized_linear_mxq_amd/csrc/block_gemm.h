@@ -58,7 +58,7 @@ struct BlockP {
   const uint16_t* bias;
   uint16_t* out; int64_t ld_out; int n_out;
   // EP_GATED: pre-activations, fp32 [M][ld_saved] each, or null
-  float* gate; float* up; int64_t ld_saved;
+  float* gate; float* up; int64_t ld_saved; bool saved_vec;   // saved_vec: rows of whole, aligned quads
   int act;
   // EP_SPLIT: rows [0, m_split) go to out, the others to out2, m_rows of each
   uint16_t* out2; int m_split, m_rows;
@@ -68,8 +68,23 @@ struct BlockP {
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-// TI x TJ MFMA tiles of 32 x 32 per wave, WM x WN waves.
-template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN>
+// The tile product: TI x TJ MFMA tiles of 32 x 32 per wave, WM x WN waves, the
+// LDS a ring.
+//
+// DEEP = 0: five slots, each the A or the W half of a K-tile (equal halves: square
+// tiles).  K-tile t has A in slot 2t % 5 and W in slot (2t + 1) % 5; A is loaded two
+// K-tiles ahead, W one and a half.  DEEP = S: S slots of whole K-tiles, S - 1 on
+// their way, for grids that leave a compute unit one workgroup and no other that
+// would hide the way from memory.  The slots are arrays of their own and the loop
+// has as many K-tiles, so every read is visibly independent of the loads in flight
+// and the compiler adds no wait; the K-tiles left over follow it in line.
+//
+// A wave walks over its MFMA tiles row by row with the fragments of one row of a and
+// of all TJ rows of w in registers, reading those of the next row meanwhile.  By the
+// last tile of a K-tile every wave has read all of it: one barrier there releases
+// its slots and, with the next K-tile's loads waited for, opens that one, whose
+// first fragments are read under the last tile's MFMAs.
+template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN, int DEEP>
 struct BlockGemm {
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int TBM = 32 * TI * WM, TBN = 32 * TJ * WN;      // rows of a and of w in a tile
@@ -77,44 +92,106 @@ struct BlockGemm {
   static constexpr int SLOT_A = TBM * 128, SLOT_W = TBN * 128;
   static constexpr int LA = SLOT_A / 1024 / NW, LW = SLOT_W / 1024 / NW;   // loads per wave
   static constexpr int KT_ELEMS = EL == EL_FP8 ? 128 : 64;
-  static_assert(EP != EP_GATED || TJ % 2 == 0, "gate and up tiles in one wave");
+  static constexpr int SLOTS = DEEP ? DEEP : 5, SLOT = DEEP ? SLOT_A + SLOT_W : SLOT_A;
+  static constexpr int PER_EU = SLOTS * SLOT * 2 <= 160 * 1024 ? 2 * NW / 4 : NW / 4;   // waves of a SIMD
+  // the output tile in LDS: whole rows of bf16, this many to a slot
+  static constexpr int ROW_BYTES = 2 * OUT_N, ROWS = SLOT / ROW_BYTES / 32 * 32;
+  static_assert(TJ == 2 && WM == 2 && (TI % 2 == 0 || DEEP % 2 == 0), "the walk's fragment buffers");
+  static_assert(DEEP > 0 || TBM == TBN, "five equal slots");
+  static_assert(DEEP == 0 || DEEP >= 3, "one K-tile in use, one landed, others on their way");
   static_assert(EL == EL_BF16 || (AL == LAY_ROW && WL == LAY_ROW), "transposing reads are of 16-bit elements");
   static_assert((AL == LAY_ROW || TBM >= 128) && (WL == LAY_ROW || TBN >= 128), "four segments to swizzle");
   static_assert(SLOT_A % (1024 * NW) == 0 && SLOT_W % (1024 * NW) == 0, "whole loads");
+  static_assert(TBM <= ROWS * SLOTS, "the output tile fits the slots");
 
   struct Frag { v4i f[4]; };
 
-  static __device__ __forceinline__ Frag read_row(const uint8_t* slot, int row, const uint32_t (&c)[4]) {
+  // A lane's fragment from a slot.  `at` is its address of the first chunk (ROW) or
+  // K-row (COL) in MFMA tile 0 of the wave, relative to the slot; the others differ
+  // in bits that the swizzles flip.  It is made opaque at every read: left alone the
+  // compiler keeps the sums with every slot's address in registers, which spill.
+  template <int LAY, int TB>
+  static __device__ __forceinline__ Frag read(uint8_t* slot, uint32_t at, int tile) {
     Frag r;
+    asm volatile("" : "+v"(at));
+    if constexpr (LAY == LAY_ROW) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) r.f[q] = *reinterpret_cast<const v4i*>(slot + row * 128 + c[q]);
-    return r;
-  }
-
-  // Columns 32 tile .. 32 tile + 31 of a COL slot of TB columns.
-  template <int TB>
-  static __device__ __forceinline__ Frag read_col(uint8_t* slot, int tile, int lane) {
-    Frag r;
-    const int q = (lane >> 2) & 3;
-    const uint32_t at = (8 * (lane >> 5) + q) * (2 * TB) + ((tile ^ q) * 64) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t flip = EL == EL_FP8 ? 64 * (q >> 1) + 16 * (q & 1) : 32 * q;
+        r.f[q] = *reinterpret_cast<const v4i*>(slot + (at ^ flip) + tile * 4096);
+      }
+    } else {
+      at ^= tile * 64;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4s h[2];
+      for (int s = 0; s < 4; ++s) {
+        v4s h[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(slot + at + (16 * s + 4 * e) * (2 * TB)));
-      r.f[s] = __builtin_bit_cast(v4i, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        for (int e = 0; e < 2; ++e)
+          h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(slot + at + (16 * s + 4 * e) * (2 * TB)));
+        r.f[s] = __builtin_bit_cast(v4i, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      }
     }
     return r;
   }
+
+  // `at` for the MFMA tiles from tile0 (a multiple of their number in a wave) on.
+  template <int LAY, int TB>
+  static __device__ __forceinline__ uint32_t first(int tile0, int lane) {
+    const int l32 = lane & 31, half = lane >> 5;
+    if constexpr (LAY == LAY_ROW) {
+      return (tile0 * 32 + l32) * 128 + (((EL == EL_FP8 ? 2 * half : half) ^ swz<8>(l32)) * 16);
+    } else {
+      const int q = (lane >> 2) & 3;
+      return (8 * half + q) * (2 * TB) + ((tile0 ^ q) * 64) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    }
+  }
 };
 
-template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void block_gemm_kernel(BlockP p, int gm) {
-  using G = BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN>;
+// Stores the tile in LDS (at(r, c): the address of element c of row r) to the rows
+// that to(r) gives (null: not stored), columns n0 + [0, n_lim), in pieces of V
+// elements, neighbours by neighbouring threads; up to eight are read before they
+// are stored.
+template <int V, int ROWS, int COLS, int THREADS, class At, class To>
+__device__ __forceinline__ void store_tile(int n_lim, int tid, At at, To to) {
+  using Piece = std::conditional_t<V == 8, v4u, std::conditional_t<V == 4, uint2, std::conditional_t<V == 2, uint32_t, uint16_t>>>;
+  constexpr int PER = COLS / V, N = ROWS * PER / THREADS, U = N % 8 == 0 ? 8 : N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1;
+  static_assert(ROWS * PER % THREADS == 0, "whole rounds");
+  for (int t = 0; t < N; t += U) {
+    Piece v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int idx = (t + k) * THREADS + tid;
+      v[k] = *reinterpret_cast<const Piece*>(at(idx / PER, idx % PER * V));
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int idx = (t + k) * THREADS + tid, c = idx % PER * V;
+      uint16_t* const o = to(idx / PER);
+      if (!o || c >= n_lim) continue;
+      if (c + V <= n_lim) {
+        if constexpr (V == 8) __builtin_nontemporal_store(v[k], reinterpret_cast<Piece*>(o + c));
+        else *reinterpret_cast<Piece*>(o + c) = v[k];
+      } else {
+        uint16_t e[V];
+        __builtin_memcpy(e, &v[k], sizeof(Piece));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (c + i < n_lim) o[c + i] = e[i];
+      }
+    }
+  }
+}
+
+template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN, int DEEP>
+__global__ __launch_bounds__(64 * WM * WN, (BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP>::PER_EU))
+void block_gemm_kernel(BlockP p, int gm) {
+  using G = BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP>;
   using Frag = typename G::Frag;
   constexpr int NW = G::NW, TBM = G::TBM, TBN = G::TBN, OUT_N = G::OUT_N, LA = G::LA, LW = G::LW;
-  __shared__ __attribute__((aligned(16))) uint8_t a0[G::SLOT_A], w0[G::SLOT_W], a1[G::SLOT_A], w1[G::SLOT_W];
+  constexpr int S = G::SLOTS;
+  __shared__ __attribute__((aligned(16))) uint8_t s0[G::SLOT], s1[G::SLOT], s2[G::SLOT], s3[S > 3 ? G::SLOT : 16],
+      s4[S > 4 ? G::SLOT : 16];
+  uint8_t* const slots[5] = {s0, s1, s2, s3, s4};
 
   const int bid = (int)block_index();
   int tm, tn, m0;
@@ -231,20 +308,9 @@ __global__ __launch_bounds__(64 * WM * WN) void block_gemm_kernel(BlockP p, int 
   };
 
   // ---- fragments ----
-  uint32_t fc[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int c = EL == EL_FP8 ? 4 * (q >> 1) + 2 * half + (q & 1) : 2 * q + half;
-    fc[q] = ((c ^ swz<8>(l32)) * 16);
-  }
-  auto read_a = [&](uint8_t* slot, int i) __attribute__((always_inline)) {
-    if constexpr (AL == LAY_ROW) return G::read_row(slot, (wm * TI + i) * 32 + l32, fc);
-    else return G::template read_col<TBM>(slot, wm * TI + i, lane);
-  };
-  auto read_w = [&](uint8_t* slot, int j) __attribute__((always_inline)) {
-    if constexpr (WL == LAY_ROW) return G::read_row(slot, (wn * TJ + j) * 32 + l32, fc);
-    else return G::template read_col<TBN>(slot, wn * TJ + j, lane);
-  };
+  const uint32_t at_a = G::template first<AL, TBM>(wm * TI, lane), at_w = G::template first<WL, TBN>(wn * TJ, lane);
+  auto read_a = [&](uint8_t* slot, int i) __attribute__((always_inline)) { return G::template read<AL, TBM>(slot, at_a, i); };
+  auto read_w = [&](uint8_t* slot, int j) __attribute__((always_inline)) { return G::template read<WL, TBN>(slot, at_w, j); };
   // chunks past the end of K as zeros
   auto cut = [&](Frag& f) __attribute__((always_inline)) {
 #pragma unroll
@@ -279,127 +345,250 @@ __global__ __launch_bounds__(64 * WM * WN) void block_gemm_kernel(BlockP p, int 
 
   // FP8: the scales of a K-tile, one row of a per lane and MFMA tile, one block of
   // w's rows per wave (its 16 or 32 TJ rows lie in one block of 128)
-  float sa[TI], sw[2];
-  const float* as[TI];
-  const float *ws = nullptr, *ws2 = nullptr;
+  float sa[TI], sw[2], sa_next[TI], sw_next[2];
+  const float *as = nullptr, *ws = nullptr, *ws2 = nullptr;
   if constexpr (EL == EL_FP8) {
-#pragma unroll
-    for (int i = 0; i < TI; ++i) as[i] = p.as + min(m0 + (wm * TI + i) * 32 + l32, p.M - 1);
+    as = p.as + m0;
     const int nb = min(n0 + wn * (OUT_N / WN), p.N - 1) / 128;
     ws = p.ws + nb * p.ldws;
     if constexpr (EP == EP_GATED) ws2 = p.ws2 + nb * p.ldws2;
   }
   auto scales = [&](int kt) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
+    int r = wm * TI * 32 + l32, z = 0;
+    // opaque: offsets from uniform addresses, formed here and not held in registers;
+    // vector loads, since a scalar load in flight would drain every LDS wait
+    asm volatile("" : "+v"(r));
+    asm volatile("" : "+v"(z));
+    const float* const row = as + (int64_t)kt * p.ldas;
 #pragma unroll
-    for (int i = 0; i < TI; ++i) sa[i] = as[i][(int64_t)kt * p.ldas];
-    sw[0] = ws[kt];
-    sw[1] = EP == EP_GATED ? ws2[kt] : sw[0];
+    for (int i = 0; i < TI; ++i) sa_next[i] = row[(uint32_t)min(r + 32 * i, p.M - 1 - m0)];
+    sw_next[0] = ws[kt + z];
+    sw_next[1] = EP == EP_GATED ? ws2[kt + z] : sw_next[0];
+  };
+  auto scales_turn = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) sa[i] = sa_next[i];
+    sw[0] = sw_next[0];
+    sw[1] = sw_next[1];
   };
 
-  auto compute = [&](uint8_t* A, uint8_t* W, bool last) __attribute__((always_inline)) {
-    Frag fw[TJ];
+  Frag fa[2], fw[TJ];
+  // MFMA tile (i, j) of a K-tile on fragments a
+  auto tile = [&](int i, int j, const Frag& a) __attribute__((always_inline)) {
+    if constexpr (EL == EL_FP8) {
+      const v16f t = mma(fw[j], a, v16f{});
+      const float s = sa[i] * sw[EP == EP_GATED && j >= TJ / 2];
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      fw[j] = read_w(W, j);
-      if (last) cut(fw[j]);
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = fmaf(t[q], s, acc[i][j][q]);
+    } else {
+      acc[i][j] = mma(fw[j], a, acc[i][j]);
+    }
+  };
+  constexpr int PAR = TI & 1;   // a K-tile of one row leaves the next in the other buffer
+  // K-tile kt, number I of the loop's; fa[P] and fw[0] hold its first fragments
+  auto step = [&](auto number, int kt) __attribute__((always_inline)) {
+    constexpr int I = decltype(number)::value, P = PAR ? I & 1 : 0;
+    uint8_t* const A = DEEP ? slots[I % S] : slots[(2 * I) % 5];
+    uint8_t* const W = DEEP ? slots[I % S] + G::SLOT_A : slots[(2 * I + 1) % 5];
+    uint8_t* const A1 = DEEP ? slots[(I + 1) % S] : slots[(2 * I + 2) % 5];
+    uint8_t* const W1 = DEEP ? slots[(I + 1) % S] + G::SLOT_A : slots[(2 * I + 3) % 5];
+    if constexpr (EL == EL_FP8) {
+      scales_turn();
+      scales(kt + 1);
     }
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      Frag fa = read_a(A, i);
-      if (last) cut(fa);
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        if constexpr (EL == EL_FP8) {
-          const v16f t = mma(fw[j], fa, v16f{});
-          const float s = sa[i] * sw[EP == EP_GATED && j >= TJ / 2];
-#pragma unroll
-          for (int q = 0; q < 16; ++q) acc[i][j][q] = fmaf(t[q], s, acc[i][j][q]);
-        } else {
-          acc[i][j] = mma(fw[j], fa, acc[i][j]);
-        }
+      const Frag& a = fa[(i + P) & 1];
+      if (i == 0) {
+        fw[1] = read_w(W, 1);
+        if constexpr (!DEEP) issue_a(kt + 2, slots[(2 * I + 4) % 5]);
       }
+      if (i > 0 && i + 1 < TI) fa[(i + 1 + P) & 1] = read_a(A, i + 1);
+      tile(i, 0, a);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == 0 && TI > 1) fa[(1 + P) & 1] = read_a(A, 1);
+      if (i == TI - 1) {
+        // every fragment of K-tile kt is read and K-tile kt+1 has landed
+        wait_lgkmcnt0();
+        wait_vmcnt<DEEP ? (DEEP - 2) * (LA + LW) : LA>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (DEEP) {
+          issue_a(kt + DEEP, A);
+          issue_w(kt + DEEP, W);
+        } else {
+          issue_w(kt + 2, A);   // slot (2I + 5) % 5
+        }
+        fa[(TI + P) & 1] = read_a(A1, 0);
+        fw[0] = read_w(W1, 0);
+      }
+      tile(i, 1, a);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  issue_a(0, a0);
-  issue_w(0, w0);
-  for (int kt = 0; kt < KT; kt += 2) {
-    if constexpr (EL == EL_FP8) scales(kt);
-    wait_vmcnt<0>();
-    __syncthreads();
-    issue_a(kt + 1, a1);
-    issue_w(kt + 1, w1);
-    compute(a0, w0, kt == KF);
-    if (kt + 1 >= KT) break;
-    if constexpr (EL == EL_FP8) scales(kt + 1);
-    wait_vmcnt<0>();
-    __syncthreads();
-    issue_a(kt + 2, a0);
-    issue_w(kt + 2, w0);
-    compute(a1, w1, kt + 1 == KF);
+  if constexpr (EL == EL_FP8) scales(0);
+  if constexpr (DEEP) {
+#pragma unroll
+    for (int t = 0; t < DEEP; ++t) {
+      issue_a(t, slots[t]);
+      issue_w(t, slots[t] + G::SLOT_A);
+    }
+    wait_vmcnt<(DEEP - 1) * (LA + LW)>();
+  } else {
+    issue_a(0, s0);
+    issue_w(0, s1);
+    issue_a(1, s2);
+    issue_w(1, s3);
+    wait_vmcnt<LA + LW>();
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  if (KF > 0) {
+    fa[0] = read_a(s0, 0);
+    fw[0] = read_w(DEEP ? s0 + G::SLOT_A : s1, 0);
+    int kt = 0;
+    for (; kt + S <= KF; kt += S) {
+      step(std::integral_constant<int, 0>{}, kt);
+      step(std::integral_constant<int, 1>{}, kt + 1);
+      step(std::integral_constant<int, 2>{}, kt + 2);
+      if constexpr (S > 3) step(std::integral_constant<int, 3>{}, kt + 3);
+      if constexpr (S > 4) step(std::integral_constant<int, 4>{}, kt + 4);
+    }
+    if (kt < KF) step(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < KF) step(std::integral_constant<int, 1>{}, kt + 1);
+    if constexpr (S > 3) if (kt + 2 < KF) step(std::integral_constant<int, 2>{}, kt + 2);
+    if constexpr (S > 4) if (kt + 3 < KF) step(std::integral_constant<int, 3>{}, kt + 3);
   }
   wait_vmcnt<0>();
+  wait_lgkmcnt0();
+  __syncthreads();
+  if (AL == LAY_ROW && rest > 0) {   // a last K-tile that K ends in
+    const int ia = DEEP ? KF % S : (2 * KF) % 5, iw = DEEP ? ia : (2 * KF + 1) % 5;
+    auto at = [&](int i) __attribute__((always_inline)) { return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : i == 3 ? s3 : s4; };
+    uint8_t* const A = at(ia);
+    uint8_t* const W = at(iw) + (DEEP ? G::SLOT_A : 0);
+    if constexpr (EL == EL_FP8) scales_turn();
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      fw[j] = read_w(W, j);
+      cut(fw[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      Frag a = read_a(A, i);
+      cut(a);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) tile(i, j, a);
+    }
+    __syncthreads();
+  }
 
   // ---- epilogue ----
-  // lane: row i*32 + l32 of the wave, columns j*32 + 8 g + 4 half + [0, 4)
+  // lane: row i*32 + l32 of the wave, columns j*32 + 8 g + 4 half + [0, 4).  The
+  // tile goes through LDS in bf16, 16-byte chunks swizzled by the row, and leaves as
+  // whole rows.
   constexpr int OJ = EP == EP_GATED ? TJ / 2 : TJ;
-  const int n_lim = min(p.N, p.n_out);
+  constexpr int SWM = OUT_N / 8 < 16 ? OUT_N / 8 - 1 : 15;
+  const int n_lim = min(p.N, p.n_out) - n0;   // columns of the tile that exist
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    const int row = m0 + (wm * TI + i) * 32 + l32;
-    if (row >= p.M) continue;
-    uint16_t* orow = p.out + (int64_t)row * p.ld_out;
-    if constexpr (EP == EP_SPLIT) {
-      int r = row;
-      uint16_t* o = p.out;
-      if (r >= p.m_split) {
-        r -= p.m_split;
-        o = p.out2;
-      }
-      if (r >= p.m_rows) continue;
-      orow = o + (int64_t)r * p.ld_out;
-    }
+    uint8_t* const slot = wm ? slots[(TI + i) * 32 / G::ROWS] : slots[i * 32 / G::ROWS];
+    uint8_t* const row = slot + (((wm * TI + i) * 32) % G::ROWS + l32) * G::ROW_BYTES;
+    const int m = m0 + (wm * TI + i) * 32 + l32;
 #pragma unroll
     for (int j = 0; j < OJ; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int n = n0 + wn * (OUT_N / WN) + j * 32 + 8 * g + 4 * half;
+        const int c = wn * (OUT_N / WN) + j * 32 + 8 * g + 4 * half;
+        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int q = 4 * g + e, nn = n + e;
-          if (nn >= p.N) continue;
-          float v = acc[i][j][q];
-          int c = nn;
-          if constexpr (EP == EP_GATED) {
-            const float u = acc[i][j + OJ][q];
-            if (EL == EL_BF16 && p.gate) {
-              p.gate[(int64_t)row * p.ld_saved + nn] = v;
-              p.up[(int64_t)row * p.ld_saved + nn] = u;
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+        if constexpr (EP == EP_GATED) {
+          float u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[e] = acc[i][j + OJ][4 * g + e];
+          if (EL == EL_BF16 && p.gate && m < p.M && n0 + c < p.N) {
+            float* const gp = p.gate + (int64_t)m * p.ld_saved + n0 + c;
+            float* const up = p.up + (int64_t)m * p.ld_saved + n0 + c;
+            if (p.saved_vec) {   // N a multiple of 4: whole quads
+              *reinterpret_cast<v4f*>(gp) = v4f{v[0], v[1], v[2], v[3]};
+              *reinterpret_cast<v4f*>(up) = v4f{u[0], u[1], u[2], u[3]};
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n0 + c + e < p.N) {
+                  gp[e] = v[e];
+                  up[e] = u[e];
+                }
             }
-            v = activation<false>(p.act, v) * u;
-          } else if constexpr (EP == EP_LINEAR) {
-            if (p.col_map) c = p.col_map[nn];
-            if (c < 0 || c >= p.n_out) continue;
-            if (p.bias) v += bf16_bits_to_f32(p.bias[c]);
           }
-          orow[c] = (uint16_t)pack_bf16_rne(v, 0.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = activation<false>(p.act, v[e]) * u[e];
         }
+        if constexpr (EP == EP_LINEAR) {
+          if (p.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int n = min(n0 + c + e, p.N - 1), to = p.col_map ? p.col_map[n] : n;
+              if (to >= 0 && to < p.n_out) v[e] += bf16_bits_to_f32(p.bias[to]);
+            }
+          }
+        }
+        *reinterpret_cast<uint2*>(row + (((c >> 3) ^ (l32 & SWM)) * 16) + half * 8) =
+            make_uint2(pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3]));
       }
   }
-  (void)n_lim;
+  __syncthreads();
+  auto at = [&](int r, int c) __attribute__((always_inline)) {
+    const int q = r / G::ROWS;
+    uint8_t* const slot = G::ROWS >= TBM || q == 0 ? s0 : q == 1 ? s1 : q == 2 ? s2 : s3;
+    return slot + (r % G::ROWS) * G::ROW_BYTES + (((c >> 3) ^ (r & SWM)) * 16) + (c & 7) * 2;
+  };
+  if (EP == EP_LINEAR && p.col_map) {   // one column per thread
+    const int c = tid % OUT_N, to = n0 + c < p.N ? p.col_map[n0 + c] : -1;
+    if (to < 0 || to >= p.n_out) return;
+    const int rows = min(TBM, p.M - m0);
+#pragma unroll 8
+    for (int r = tid / OUT_N; r < rows; r += G::THREADS / OUT_N)
+      p.out[(int64_t)(m0 + r) * p.ld_out + to] = *reinterpret_cast<const uint16_t*>(at(r, c));
+    return;
+  }
+  uint16_t* const out = p.out + n0;
+  auto to = [&](int r) __attribute__((always_inline)) -> uint16_t* {
+    int row = m0 + r;
+    if (row >= p.M) return nullptr;
+    uint16_t* o = out;
+    if constexpr (EP == EP_SPLIT) {
+      if (row >= p.m_split) {
+        row -= p.m_split;
+        o = p.out2 + n0;
+      }
+      if (row >= p.m_rows) return nullptr;
+    }
+    return o + (int64_t)row * p.ld_out;
+  };
+  uint64_t low = (uint64_t)p.ld_out * 2 | reinterpret_cast<uintptr_t>(p.out);
+  if constexpr (EP == EP_SPLIT) low |= reinterpret_cast<uintptr_t>(p.out2);
+  if ((low & 15) == 0) store_tile<8, TBM, OUT_N, G::THREADS>(n_lim, tid, at, to);
+  else if ((low & 7) == 0) store_tile<4, TBM, OUT_N, G::THREADS>(n_lim, tid, at, to);
+  else if ((low & 3) == 0) store_tile<2, TBM, OUT_N, G::THREADS>(n_lim, tid, at, to);
+  else store_tile<1, TBM, OUT_N, G::THREADS>(n_lim, tid, at, to);
 }
 
-template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN>
+template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN, int DEEP = 0>
 hipError_t launch_block_gemm(BlockP p, hipStream_t s) {
-  using G = BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN>;
+  using G = BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP>;
   p.tiles_m = GRP ? (int)group_tiles_bound(p.M, p.groups, G::TBM) : (p.M + G::TBM - 1) / G::TBM;
   p.tiles_n = (p.N + G::OUT_N - 1) / G::OUT_N;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
   int gm = 1;
   while (gm * 2 <= p.tiles_m && (int64_t)gm * 2 * gm * 2 <= (tiles + 7) / 8) gm *= 2;
-  block_gemm_kernel<EL, AL, WL, EP, GRP, TI, TJ, WM, WN><<<grid_of(tiles), G::THREADS, 0, s>>>(p, gm);
+  block_gemm_kernel<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP><<<grid_of(tiles), G::THREADS, 0, s>>>(p, gm);
   return hipGetLastError();
 }
 
