@@ -213,7 +213,9 @@ void block_gemm_kernel(BlockP p, int gm) {
     tile_coords(bid, p.tiles_m, p.tiles_n, gm, tm, tn);
     m0 = tm * TBM;
   }
-  const int n0 = tn * OUT_N;
+  // uniform, but from divisions, which the vector units do
+  m0 = __builtin_amdgcn_readfirstlane(m0);
+  const int n0 = __builtin_amdgcn_readfirstlane(tn * OUT_N);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int l32 = lane & 31, half = lane >> 5;
@@ -268,9 +270,18 @@ void block_gemm_kernel(BlockP p, int gm) {
     wbase = p.w + (int64_t)n0 * 2;
     wbase2 = p.w2 + (int64_t)n0 * 2;
   }
+  // held in scalar registers: a kernel argument loaded again in the loop would, as a
+  // scalar load in flight, drain every LDS wait
+  uint32_t lda = (uint32_t)p.lda, ldw = (uint32_t)p.ldw, ldw2 = (uint32_t)p.ldw2;
+  int k_split = p.k_split, k_rows = p.k_rows;
+  if constexpr (AL == LAY_COL) asm volatile("" : "+s"(lda));
+  if constexpr (WL == LAY_COL) {
+    asm volatile("" : "+s"(ldw), "+s"(k_rows));
+    if constexpr (EP == EP_LINEAR) asm volatile("" : "+s"(ldw2), "+s"(k_split), "+s"(wbase2));
+  }
   auto issue_a = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
-    const uint8_t* b = abase + (AL == LAY_ROW ? (int64_t)kt * 128 : (int64_t)kt * 64 * p.lda);
+    const uint8_t* b = abase + (AL == LAY_ROW ? (int64_t)kt * 128 : (int64_t)kt * 64 * lda);
     // chunks past the end of K re-read the row's first chunk of the K-tile
     const uint32_t back = AL == LAY_ROW && kt == KF && lc >= rest * 16 ? lc : 0;
 #pragma unroll
@@ -293,17 +304,20 @@ void block_gemm_kernel(BlockP p, int gm) {
       }
     } else {
       int k0 = kt * 64;
-      const bool second = k0 >= p.k_split;
-      if (second) k0 -= p.k_split;
-      const uint8_t* b = second ? wbase2 + (int64_t)k0 * p.ldw2 : wbase + (int64_t)k0 * p.ldw;
-      const int rows = p.k_rows - k0;   // K-rows past the end re-read the K-tile's first
-      const uint32_t ld = (uint32_t)(second ? p.ldw2 : p.ldw);
-#pragma unroll
-      for (int t = 0; t < LW; ++t) {
-        const int kr = kw + (512 / TBN) * NW * t;
-        __builtin_amdgcn_global_load_lds(b + (uint64_t)((kr < rows ? (uint32_t)kr * ld : 0u) + cw),
-                                         (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
+      const uint8_t* b = wbase;
+      uint32_t ld = ldw;
+      if constexpr (EP == EP_LINEAR) {
+        const bool second = k0 >= k_split;
+        k0 -= second ? k_split : 0;
+        b = second ? wbase2 : wbase;
+        ld = second ? ldw2 : ldw;
       }
+      b += (int64_t)k0 * ld;
+      const int last = k_rows - 1 - k0;   // K-rows past the end re-read the last one
+#pragma unroll
+      for (int t = 0; t < LW; ++t)
+        __builtin_amdgcn_global_load_lds(b + (uint64_t)((uint32_t)min(kw + (512 / TBN) * NW * t, last) * ld + cw),
+                                         (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
     }
   };
 
@@ -349,22 +363,24 @@ void block_gemm_kernel(BlockP p, int gm) {
   const float *as = nullptr, *ws = nullptr, *ws2 = nullptr;
   if constexpr (EL == EL_FP8) {
     as = p.as + m0;
-    const int nb = min(n0 + wn * (OUT_N / WN), p.N - 1) / 128;
+    const int nb = __builtin_amdgcn_readfirstlane(min(n0 + wn * (OUT_N / WN), p.N - 1) / 128);
     ws = p.ws + nb * p.ldws;
     if constexpr (EP == EP_GATED) ws2 = p.ws2 + nb * p.ldws2;
   }
   auto scales = [&](int kt) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
-    int r = wm * TI * 32 + l32, z = 0;
-    // opaque: offsets from uniform addresses, formed here and not held in registers;
-    // vector loads, since a scalar load in flight would drain every LDS wait
+    uint32_t r = 4 * (wm * TI * 32 + l32), z = 0;
+    // opaque: byte offsets from uniform addresses, formed here and not held in
+    // registers; vector loads, since a scalar load in flight would drain every LDS wait
     asm volatile("" : "+v"(r));
     asm volatile("" : "+v"(z));
-    const float* const row = as + (int64_t)kt * p.ldas;
+    auto load = [](const float* base, uint32_t off) __attribute__((always_inline)) {
+      return *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(base) + off);
+    };
 #pragma unroll
-    for (int i = 0; i < TI; ++i) sa_next[i] = row[(uint32_t)min(r + 32 * i, p.M - 1 - m0)];
-    sw_next[0] = ws[kt + z];
-    sw_next[1] = EP == EP_GATED ? ws2[kt + z] : sw_next[0];
+    for (int i = 0; i < TI; ++i) sa_next[i] = load(as + (int64_t)kt * p.ldas, min(r + 128 * i, 4u * (p.M - 1 - m0)));
+    sw_next[0] = load(ws + kt, z);
+    sw_next[1] = EP == EP_GATED ? load(ws2 + kt, z) : sw_next[0];
   };
   auto scales_turn = [&]() __attribute__((always_inline)) {
 #pragma unroll
