@@ -26,7 +26,7 @@ PROBE_SRC = os.path.join(PKG, "probe", "mfma_probe.hip")
 PROBE_LIB = os.path.join(PKG, "probe", "libmxq_probe.so")
 SOURCES = ["api.cpp", "quantize.hip", "lowrank.hip", "gemm_mx.hip", "gemm_dq.hip", "gemm_dqp.hip",
            "mse.hip", "lowrank_split.hip", "quantize_i8.hip", "gemm_i8.hip", "gemm_few.hip",
-           "qk_norm.hip", "quantize_fp8.hip", "gemm_fp8.hip", "gated.hip", "layer_norm.hip"]
+           "qk_norm.hip", "quantize_fp8.hip", "gemm_fp8.hip", "gated.hip", "block_few.hip", "layer_norm.hip"]
 ARCH = "gfx950"
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 BINDING_LIB = os.path.join(PKG, "_torch_binding" + sysconfig.get_config_var("EXT_SUFFIX"))

@@ -65,6 +65,13 @@ struct BlockP {
   const int32_t* goff; int groups;
 };
 
+// Products of few rows (block_few.hip).
+hipError_t launch_block_few(const BlockP& p, int el, bool gated, hipStream_t s);
+inline bool block_few(const BlockP& p) {
+  const double rows = p.goff ? (double)p.M / p.groups : p.M;
+  return rows <= 16 || (!p.goff && (double)((p.M + 15) / 16) * ((p.N + 15) / 16) <= 512);
+}
+
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 

@@ -116,6 +116,7 @@ hipError_t launch_gated_bf16(const GatedArgs& a, hipStream_t s) {
   p.out = a.g.out; p.ld_out = a.g.ld_out; p.n_out = (int)a.g.N;
   p.gate = a.gate; p.up = a.up; p.ld_saved = a.ld_saved; p.act = a.act;
   p.saved_vec = p.N % 4 == 0 && al16(a.gate);
+  if (block_few(p)) return launch_block_few(p, EL_BF16, true, s);
   if (gemm_tiles(a.g, 256, 128) >= 200)
     return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 2, 2, 4>(p, s);
   return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 2, 2, 2, 2>(p, s);
