@@ -14,17 +14,19 @@
 // four K-rows of 16 columns and each gets the four K of its column), whose four
 // rows then fall on different banks.
 //
-// Fragments.  Lane l of a 32-row MFMA operand holds row l % 32 and, of a K-tile,
-// 64 bytes: for bf16 step s (16 K) the chunk 2 s + l / 32, for E4M3 step s (64 K)
-// the chunks 4 s + 2 (l / 32) + {0, 1} (any order of K is right that both operands
-// share).  The MFMAs compute D^T = W A^T: a lane holds four consecutive output
-// columns of one row, so the row's scale is one register.
+// Fragments.  bf16: 32 x 32 x 16 MFMAs; lane l holds row l % 32 and, of step s of a
+// K-tile's four, the chunk 2 s + l / 32.  E4M3: 16 x 16 x 128 MFMAs, a K-tile each;
+// lane l holds row l % 16 and the chunks 2 (l / 16) + {0, 1}.  (Any order of K is
+// right that both operands share.)  The MFMAs compute D^T = W A^T: a lane holds four
+// consecutive output columns of one row, so the row's scale is one register.
 //
 // E4M3 sums.  Within one MFMA the hardware adds products to about 2**-15 of the
 // largest (measured: at most 2**-11.3 of it over 64 products, without bias, 1.3e-5
 // of the sum's rms on normal data; profiles/mfma_probe.md).  Each block of 128 is
 // therefore summed from a zero accumulator and enters the fp32 sum scaled,
-// acc += (sa sw) * sum, so the error stays relative to the block's own products.
+// acc += (sa sw) * sum, so the error stays relative to the block's own products;
+// that takes the vector units half as long as the MFMA the matrix cores, and runs
+// under the MFMAs after it.
 // Converting the codes to bf16 would be exact at 2.4 times the MFMA time.
 #pragma once
 
@@ -75,26 +77,29 @@ inline bool block_few(const BlockP& p) {
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
-// The tile product: TI x TJ MFMA tiles of 32 x 32 per wave, WM x WN waves, the
-// LDS a ring.
+// The tile product: TI x TJ MFMA tiles of R x R per wave, WM x WN waves, the LDS a
+// ring.
 //
 // DEEP = 0: five slots, each the A or the W half of a K-tile (equal halves: square
-// tiles).  K-tile t has A in slot 2t % 5 and W in slot (2t + 1) % 5; A is loaded two
-// K-tiles ahead, W one and a half.  DEEP = S: S slots of whole K-tiles, S - 1 on
-// their way, for grids that leave a compute unit one workgroup and no other that
-// would hide the way from memory.  The slots are arrays of their own and the loop
-// has as many K-tiles, so every read is visibly independent of the loads in flight
-// and the compiler adds no wait; the K-tiles left over follow it in line.
+// tiles).  K-tile t has A in slot 2t % 5 and W in slot (2t + 1) % 5; W is loaded one
+// K-tile ahead, A nearly two.  DEEP = S: S slots of whole K-tiles, S - 1 on their way,
+// for grids that leave a compute unit one workgroup and no other that would hide the
+// way from memory.  The slots are arrays of their own and the loop has as many
+// K-tiles, so every read is visibly independent of the loads in flight and the
+// compiler adds no wait; the K-tiles left over follow it in line.
 //
 // A wave walks over its MFMA tiles row by row with the fragments of one row of a and
 // of all TJ rows of w in registers, reading those of the next row meanwhile.  By the
-// last tile of a K-tile every wave has read all of it: one barrier there releases
-// its slots and, with the next K-tile's loads waited for, opens that one, whose
-// first fragments are read under the last tile's MFMAs.
+// last row of a K-tile every wave has read all of it: one barrier there releases its
+// slots and, with the next K-tile's loads waited for, opens that one, whose first
+// fragments are read under the last row's MFMAs.  Loads go out one or two to a row or
+// tile: all of a slot's at once fill the queue to memory, and the wave that issues
+// them stands still with its MFMAs behind them (8192^3 FP8: a fifth of the time).
 template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN, int DEEP>
 struct BlockGemm {
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
-  static constexpr int TBM = 32 * TI * WM, TBN = 32 * TJ * WN;      // rows of a and of w in a tile
+  static constexpr int R = EL == EL_FP8 ? 16 : 32;                  // rows of an MFMA tile
+  static constexpr int TBM = R * TI * WM, TBN = R * TJ * WN;        // rows of a and of w in a tile
   static constexpr int OUT_N = EP == EP_GATED ? TBN / 2 : TBN;      // output columns
   static constexpr int SLOT_A = TBM * 128, SLOT_W = TBN * 128;
   static constexpr int LA = SLOT_A / 1024 / NW, LW = SLOT_W / 1024 / NW;   // loads per wave
@@ -103,7 +108,19 @@ struct BlockGemm {
   static constexpr int PER_EU = SLOTS * SLOT * 2 <= 160 * 1024 ? 2 * NW / 4 : NW / 4;   // waves of a SIMD
   // the output tile in LDS: whole rows of bf16, this many to a slot
   static constexpr int ROW_BYTES = 2 * OUT_N, ROWS = SLOT / ROW_BYTES / 32 * 32;
-  static_assert(TJ == 2 && WM == 2 && (TI % 2 == 0 || DEEP % 2 == 0), "the walk's fragment buffers");
+  // Steps of a K-tile that loads are dealt to: rows (E4M3) or MFMA tiles; the
+  // barrier is before step `OPEN`.
+  static constexpr int STEPS = EL == EL_FP8 ? TI : TI * TJ, OPEN = EL == EL_FP8 ? TI - 1 : (TI - 1) * TJ;
+  // W loads go out two to a step, then the A loads one or two, the first at step OPEN
+  static constexpr int W_STEPS = (LW + 1) / 2, PER_A = (LA + STEPS - W_STEPS - 1) / (STEPS - W_STEPS);
+  static constexpr int turn(int t) { return t >= OPEN ? t - OPEN : t + STEPS - OPEN; }   // steps since the barrier
+  static constexpr int first_w(int t) { return turn(t) < W_STEPS ? 2 * turn(t) : LW; }
+  static constexpr int last_w(int t) { return turn(t) < W_STEPS && 2 * turn(t) + 2 < LW ? 2 * turn(t) + 2 : LW; }
+  static constexpr int first_a(int t) { return turn(t) < W_STEPS ? 0 : (turn(t) - W_STEPS) * PER_A < LA ? (turn(t) - W_STEPS) * PER_A : LA; }
+  static constexpr int last_a(int t) { return turn(t) < W_STEPS ? 0 : (turn(t) - W_STEPS + 1) * PER_A < LA ? (turn(t) - W_STEPS + 1) * PER_A : LA; }
+  // W loads of the K-tile after next that are out before K-tile 0 begins
+  static constexpr int AHEAD_W = last_w(STEPS - 1), AHEAD_A = last_a(STEPS - 1);
+  static_assert(WM == 2 && TJ >= 2 && (EL == EL_BF16 ? TI % 2 == 0 || DEEP % 2 == 0 : TI % 4 == 0 && TJ == 4), "the walk's fragment buffers");
   static_assert(DEEP > 0 || TBM == TBN, "five equal slots");
   static_assert(DEEP == 0 || DEEP >= 3, "one K-tile in use, one landed, others on their way");
   static_assert(EL == EL_BF16 || (AL == LAY_ROW && WL == LAY_ROW), "transposing reads are of 16-bit elements");
@@ -111,22 +128,23 @@ struct BlockGemm {
   static_assert(SLOT_A % (1024 * NW) == 0 && SLOT_W % (1024 * NW) == 0, "whole loads");
   static_assert(TBM <= ROWS * SLOTS, "the output tile fits the slots");
 
-  struct Frag { v4i f[4]; };
+  struct Frag { v4i f[EL == EL_FP8 ? 2 : 4]; };
 
-  // A lane's fragment from a slot.  `at` is its address of the first chunk (ROW) or
-  // K-row (COL) in MFMA tile 0 of the wave, relative to the slot; the others differ
-  // in bits that the swizzles flip.  It is made opaque at every read: left alone the
-  // compiler keeps the sums with every slot's address in registers, which spill.
+  // A lane's fragment of MFMA tile `tile` of the wave.  `at` is its address of the
+  // first chunk (ROW) or K-row (COL) in the wave's tile 0, relative to the slot; the
+  // others differ in bits that the swizzles flip.  It is made opaque at every read:
+  // left alone the compiler keeps the sums with every slot's address in registers,
+  // which spill.
   template <int LAY, int TB>
   static __device__ __forceinline__ Frag read(uint8_t* slot, uint32_t at, int tile) {
     Frag r;
     asm volatile("" : "+v"(at));
-    if constexpr (LAY == LAY_ROW) {
+    if constexpr (EL == EL_FP8) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t flip = EL == EL_FP8 ? 64 * (q >> 1) + 16 * (q & 1) : 32 * q;
-        r.f[q] = *reinterpret_cast<const v4i*>(slot + (at ^ flip) + tile * 4096);
-      }
+      for (int q = 0; q < 2; ++q) r.f[q] = *reinterpret_cast<const v4i*>(slot + (at ^ (16 * q)) + tile * 2048);
+    } else if constexpr (LAY == LAY_ROW) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r.f[q] = *reinterpret_cast<const v4i*>(slot + (at ^ (32 * q)) + tile * 4096);
     } else {
       at ^= tile * 64;
 #pragma unroll
@@ -144,12 +162,12 @@ struct BlockGemm {
   // `at` for the MFMA tiles from tile0 (a multiple of their number in a wave) on.
   template <int LAY, int TB>
   static __device__ __forceinline__ uint32_t first(int tile0, int lane) {
-    const int l32 = lane & 31, half = lane >> 5;
+    const int r = lane % R, part = lane / R;
     if constexpr (LAY == LAY_ROW) {
-      return (tile0 * 32 + l32) * 128 + (((EL == EL_FP8 ? 2 * half : half) ^ swz<8>(l32)) * 16);
+      return (tile0 * R + r) * 128 + (((EL == EL_FP8 ? 2 * part : part) ^ swz<8>(r)) * 16);
     } else {
       const int q = (lane >> 2) & 3;
-      return (8 * half + q) * (2 * TB) + ((tile0 ^ q) * 64) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+      return (8 * part + q) * (2 * TB) + ((tile0 ^ q) * 64) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     }
   }
 };
@@ -225,7 +243,8 @@ void block_gemm_kernel(BlockP p, int gm) {
   const int n0 = __builtin_amdgcn_readfirstlane(tn * OUT_N);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int l32 = lane & 31, half = lane >> 5;
+  constexpr int R = G::R;
+  const int rl = lane % R, part = lane / R;
   const int KF = p.K / G::KT_ELEMS;                       // whole K-tiles
   const int rest = (p.K % G::KT_ELEMS) * (EL == EL_FP8 ? 1 : 2) / 16;   // 16-byte chunks of a last one
   const int KT = KF + (rest > 0);
@@ -259,9 +278,9 @@ void block_gemm_kernel(BlockP p, int gm) {
     for (int t = 0; t < LW; ++t) {
       const int r = 8 * NW * t + lr;
       if constexpr (EP == EP_GATED) {
-        // 32 TJ rows per wave column: its gate rows, then its up rows
-        const int wc = r / (32 * TJ), in = r % (32 * TJ), n = n0 + wc * 16 * TJ + in % (16 * TJ);
-        const bool second = in >= 16 * TJ;
+        // R TJ rows per wave column: its gate rows, then its up rows
+        const int wc = r / (R * TJ), in = r % (R * TJ), n = n0 + wc * (R * TJ / 2) + in % (R * TJ / 2);
+        const bool second = in >= R * TJ / 2;
         vw[t] = (uint32_t)(min(n, p.N - 1) - n0) * (uint32_t)(second ? p.ldw2 : p.ldw) + lc;
       } else {
         vw[t] = (uint32_t)(min(n0 + r, p.N - 1) - n0) * (uint32_t)p.ldw + lc;
@@ -286,26 +305,29 @@ void block_gemm_kernel(BlockP p, int gm) {
     asm volatile("" : "+s"(ldw), "+s"(k_rows));
     if constexpr (EP == EP_LINEAR) asm volatile("" : "+s"(ldw2), "+s"(k_split), "+s"(wbase2));
   }
-  auto issue_a = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
+  // loads [t0, t1) of a K-tile's A or W; chunks past the end of K re-read the row's
+  // first chunk of the K-tile, K-rows past it the last K-row
+  auto issue_a = [&](int kt, uint8_t* slot, int t0, int t1) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
     const uint8_t* b = abase + (AL == LAY_ROW ? (int64_t)kt * 128 : (int64_t)kt * 64 * lda);
-    // chunks past the end of K re-read the row's first chunk of the K-tile
     const uint32_t back = AL == LAY_ROW && kt == KF && lc >= rest * 16 ? lc : 0;
 #pragma unroll
     for (int t = 0; t < LA; ++t)
-      __builtin_amdgcn_global_load_lds(b + (uint64_t)(va[t] - back), (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
+      if (t >= t0 && t < t1)
+        __builtin_amdgcn_global_load_lds(b + (uint64_t)(va[t] - back), (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
   };
-  auto issue_w = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
+  auto issue_w = [&](int kt, uint8_t* slot, int t0, int t1) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
     if constexpr (WL == LAY_ROW) {
       const int64_t k = (int64_t)kt * 128;
       const uint32_t back = kt == KF && lc >= rest * 16 ? lc : 0;
 #pragma unroll
       for (int t = 0; t < LW; ++t) {
+        if (t < t0 || t >= t1) continue;
         const uint8_t* b = wbase;
         if constexpr (EP == EP_GATED) {
           const int r = 8 * (NW * t + wave);   // a load's eight rows lie on one side
-          if (r % (32 * TJ) >= 16 * TJ) b = wbase2;
+          if (r % (R * TJ) >= R * TJ / 2) b = wbase2;
         }
         __builtin_amdgcn_global_load_lds(b + k + (uint64_t)(vw[t] - back), (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
       }
@@ -320,11 +342,12 @@ void block_gemm_kernel(BlockP p, int gm) {
         ld = second ? ldw2 : ldw;
       }
       b += (int64_t)k0 * ld;
-      const int last = k_rows - 1 - k0;   // K-rows past the end re-read the last one
+      const int last = k_rows - 1 - k0;
 #pragma unroll
       for (int t = 0; t < LW; ++t)
-        __builtin_amdgcn_global_load_lds(b + (uint64_t)((uint32_t)min(kw + (512 / TBN) * NW * t, last) * ld + cw),
-                                         (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
+        if (t >= t0 && t < t1)
+          __builtin_amdgcn_global_load_lds(b + (uint64_t)((uint32_t)min(kw + (512 / TBN) * NW * t, last) * ld + cw),
+                                           (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
     }
   };
 
@@ -333,40 +356,26 @@ void block_gemm_kernel(BlockP p, int gm) {
   auto read_a = [&](uint8_t* slot, int i) __attribute__((always_inline)) { return G::template read<AL, TBM>(slot, at_a, i); };
   auto read_w = [&](uint8_t* slot, int j) __attribute__((always_inline)) { return G::template read<WL, TBN>(slot, at_w, j); };
   // chunks past the end of K as zeros
-  auto cut = [&](Frag& f) __attribute__((always_inline)) {
+  auto cut = [&](Frag f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = EL == EL_FP8 ? 4 * (q >> 1) + 2 * half + (q & 1) : 2 * q + half;
-      if (c >= rest) f.f[q] = v4i{};
-    }
+    for (int q = 0; q < (int)(sizeof(f.f) / 16); ++q)
+      if ((EL == EL_FP8 ? 2 * part + q : 2 * q + part) >= rest) f.f[q] = v4i{};
+    return f;
   };
 
-  v16f acc[TI][TJ];
+  using Acc = std::conditional_t<EL == EL_FP8, v4f, v16f>;
+  Acc acc[TI][TJ];
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = v16f{};
+    for (int j = 0; j < TJ; ++j) acc[i][j] = Acc{};
 
-  auto join = [](const v4i& a, const v4i& b) __attribute__((always_inline)) {
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  auto mma = [&](const Frag& w, const Frag& a, v16f c) __attribute__((always_inline)) {
-    if constexpr (EL == EL_FP8) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(w.f[2 * s], w.f[2 * s + 1]), join(a.f[2 * s], a.f[2 * s + 1]),
-                                                            c, 0, 0, 0, 127, 0, 127);
-    } else {
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w.f[s]), __builtin_bit_cast(v8bf, a.f[s]), c, 0, 0, 0);
-    }
-    return c;
-  };
-
-  // FP8: the scales of a K-tile, one row of a per lane and MFMA tile, one block of
-  // w's rows per wave (its 16 or 32 TJ rows lie in one block of 128)
-  float sa[TI], sw[2], sa_next[TI], sw_next[2];
+  // FP8 scales.  Of a K-tile a lane loads those of the rows 64 r + lane of the wave
+  // (one line each, the rows of a K-block lie together) and swaps quarters of the
+  // wave when it comes to them; the wave's columns lie in one block of w's rows, and
+  // lane l holds that block's scale of the loop's K-tile l.
+  constexpr int RAW = EL == EL_FP8 ? TI / 4 : 1;
+  float raw[RAW], raw_next[RAW], sa[4], sw_of[2], sw_next[2], sw[2], row_scale[2] = {0.f, 0.f}, old_scale[2] = {0.f, 0.f};
   const float *as = nullptr, *ws = nullptr, *ws2 = nullptr;
   if constexpr (EL == EL_FP8) {
     as = p.as + m0;
@@ -374,63 +383,106 @@ void block_gemm_kernel(BlockP p, int gm) {
     ws = p.ws + nb * p.ldws;
     if constexpr (EP == EP_GATED) ws2 = p.ws2 + nb * p.ldws2;
   }
-  auto scales = [&](int kt) __attribute__((always_inline)) {
+  auto row_scales = [&](int kt) __attribute__((always_inline)) {   // into raw_next
     kt = kt < KT ? kt : KT - 1;
-    uint32_t r = 4 * (wm * TI * 32 + l32), z = 0;
-    // opaque: byte offsets from uniform addresses, formed here and not held in
-    // registers; vector loads, since a scalar load in flight would drain every LDS wait
-    asm volatile("" : "+v"(r));
-    asm volatile("" : "+v"(z));
-    auto load = [](const float* base, uint32_t off) __attribute__((always_inline)) {
-      return *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(base) + off);
-    };
+    const uint8_t* const b = reinterpret_cast<const uint8_t*>(as + (int64_t)kt * p.ldas);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) sa_next[i] = load(as + (int64_t)kt * p.ldas, min(r + 128 * i, 4u * (p.M - 1 - m0)));
-    sw_next[0] = load(ws + kt, z);
-    sw_next[1] = EP == EP_GATED ? load(ws2 + kt, z) : sw_next[0];
+    for (int r = 0; r < RAW; ++r) {
+      uint32_t off = 4 * (wm * TI * 16 + 64 * r + lane);
+      raw_next[r] = *reinterpret_cast<const float*>(b + min(off, 4u * (uint32_t)(p.M - 1 - m0)));
+    }
   };
-  auto scales_turn = [&]() __attribute__((always_inline)) {
+  auto block_scales = [&](int kt) __attribute__((always_inline)) {   // K-tiles kt and on, into sw_next
+    const int k = min(kt + lane, KT - 1);
+    sw_next[0] = ws[k];
+    if constexpr (EP == EP_GATED) sw_next[1] = ws2[k];
+  };
+  auto open_scales = [&](int number) __attribute__((always_inline)) {   // of K-tile `number` of the loop's
 #pragma unroll
-    for (int i = 0; i < TI; ++i) sa[i] = sa_next[i];
-    sw[0] = sw_next[0];
-    sw[1] = sw_next[1];
+    for (int r = 0; r < RAW; ++r) raw[r] = raw_next[r];
+#pragma unroll
+    for (int h = 0; h < (EP == EP_GATED ? 2 : 1); ++h)
+      sw[h] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw_of[h]), number));
+  };
+  auto turn_scales = [&](int kt) __attribute__((always_inline)) {   // the loop begins at K-tile kt
+    sw_of[0] = sw_next[0];
+    sw_of[1] = sw_next[1];
+    block_scales(kt + S);
+  };
+  // the scales of rows 64 r + 16 e + lane % 16 from those of rows 64 r + lane
+  auto spread = [&](float v) __attribute__((always_inline)) {
+    const uint32_t u = __float_as_uint(v);
+    const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);       // quarters 0 1 0 1, 2 3 2 3
+    const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    sa[0] = __uint_as_float(lo[0]);
+    sa[1] = __uint_as_float(lo[1]);
+    sa[2] = __uint_as_float(hi[0]);
+    sa[3] = __uint_as_float(hi[1]);
   };
 
   Frag fa[2], fw[TJ];
+  // FP8: the block sums of the last two MFMA tiles, added under the next ones
+  v4f blk[4] = {v4f{}, v4f{}, v4f{}, v4f{}};
+  auto add_block = [&](int n) __attribute__((always_inline)) {   // MFMA tile n of the K-tile (negative: the one before)
+    const int t = n < 0 ? n + TI * TJ : n, i = t / TJ, j = t % TJ;
+    const float s = (n < 0 || j >= TJ - 2 ? old_scale : row_scale)[EP == EP_GATED && j >= TJ / 2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(blk[t % 4][e], s, acc[i][j][e]);
+  };
   // MFMA tile (i, j) of a K-tile on fragments a
   auto tile = [&](int i, int j, const Frag& a) __attribute__((always_inline)) {
     if constexpr (EL == EL_FP8) {
-      const v16f t = mma(fw[j], a, v16f{});
-      const float s = sa[i] * sw[EP == EP_GATED && j >= TJ / 2];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = fmaf(t[q], s, acc[i][j][q]);
+      const int n = i * TJ + j;
+      if (j == 0) {
+        if (i % 4 == 0) spread(raw[i / 4]);
+        old_scale[0] = row_scale[0];
+        row_scale[0] = sa[i % 4] * sw[0];
+        if constexpr (EP == EP_GATED) {
+          old_scale[1] = row_scale[1];
+          row_scale[1] = sa[i % 4] * sw[1];
+        }
+      }
+      const v8i wv = __builtin_shufflevector(fw[j].f[0], fw[j].f[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const v8i av = __builtin_shufflevector(a.f[0], a.f[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      blk[n % 4] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, v4f{}, 0, 0, 0, 127, 0, 127);
+      add_block(n - 2);
     } else {
-      acc[i][j] = mma(fw[j], a, acc[i][j]);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fw[j].f[s]),
+                                                            __builtin_bit_cast(v8bf, a.f[s]), acc[i][j], 0, 0, 0);
     }
   };
+
   constexpr int PAR = TI & 1;   // a K-tile of one row leaves the next in the other buffer
-  // K-tile kt, number I of the loop's; fa[P] and fw[0] hold its first fragments
+  // K-tile kt, number I of the loop's; fa[P] and all but the last of fw hold its first fragments
   auto step = [&](auto number, int kt) __attribute__((always_inline)) {
     constexpr int I = decltype(number)::value, P = PAR ? I & 1 : 0;
     uint8_t* const A = DEEP ? slots[I % S] : slots[(2 * I) % 5];
     uint8_t* const W = DEEP ? slots[I % S] + G::SLOT_A : slots[(2 * I + 1) % 5];
     uint8_t* const A1 = DEEP ? slots[(I + 1) % S] : slots[(2 * I + 2) % 5];
     uint8_t* const W1 = DEEP ? slots[(I + 1) % S] + G::SLOT_A : slots[(2 * I + 3) % 5];
+    // loads of step t: what the last barrier released
+    auto issue = [&](int t) __attribute__((always_inline)) {
+      if constexpr (DEEP) {
+        uint8_t* const to = t >= G::OPEN ? A : slots[(I + S - 1) % S];
+        const int k = t >= G::OPEN ? kt + DEEP : kt + DEEP - 1;
+        issue_w(k, to + G::SLOT_A, G::first_w(t), G::last_w(t));
+        issue_a(k, to, G::first_a(t), G::last_a(t));
+      } else {
+        issue_w(t >= G::OPEN ? kt + 2 : kt + 1, t >= G::OPEN ? A : W1, G::first_w(t), G::last_w(t));
+        issue_a(t >= G::OPEN ? kt + 3 : kt + 2, t >= G::OPEN ? W : slots[(2 * I + 4) % 5], G::first_a(t), G::last_a(t));
+      }
+    };
     if constexpr (EL == EL_FP8) {
-      scales_turn();
-      scales(kt + 1);
+      if constexpr (I == 0) turn_scales(kt);
+      open_scales(I);
+      row_scales(kt + 1);
     }
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const Frag& a = fa[(i + P) & 1];
-      if (i == 0) {
-        fw[1] = read_w(W, 1);
-        if constexpr (!DEEP) issue_a(kt + 2, slots[(2 * I + 4) % 5]);
-      }
-      if (i > 0 && i + 1 < TI) fa[(i + 1 + P) & 1] = read_a(A, i + 1);
-      tile(i, 0, a);
-      __builtin_amdgcn_sched_barrier(0);
-      if (i == 0 && TI > 1) fa[(1 + P) & 1] = read_a(A, 1);
       if (i == TI - 1) {
         // every fragment of K-tile kt is read and K-tile kt+1 has landed
         wait_lgkmcnt0();
@@ -439,40 +491,47 @@ void block_gemm_kernel(BlockP p, int gm) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (DEEP) {
-          issue_a(kt + DEEP, A);
-          issue_w(kt + DEEP, W);
-        } else {
-          issue_w(kt + 2, A);   // slot (2I + 5) % 5
-        }
-        fa[(TI + P) & 1] = read_a(A1, 0);
-        fw[0] = read_w(W1, 0);
       }
-      tile(i, 1, a);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        if (i == 0 && j == 0) fw[TJ - 1] = read_w(W, TJ - 1);
+        if (j == 0) fa[(i + 1 + P) & 1] = i + 1 < TI ? read_a(A, i + 1) : read_a(A1, 0);
+        if (i == TI - 1 && j > 0) fw[j - 1] = read_w(W1, j - 1);
+        if (EL == EL_BF16) issue(i * TJ + j);
+        else if (j == 1) issue(i);
+        tile(i, j, a);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
 
-  if constexpr (EL == EL_FP8) scales(0);
+  if constexpr (EL == EL_FP8) {
+    row_scales(0);
+    block_scales(0);
+  }
   if constexpr (DEEP) {
 #pragma unroll
-    for (int t = 0; t < DEEP; ++t) {
-      issue_a(t, slots[t]);
-      issue_w(t, slots[t] + G::SLOT_A);
+    for (int t = 0; t + 1 < DEEP; ++t) {
+      issue_w(t, slots[t] + G::SLOT_A, 0, LW);
+      issue_a(t, slots[t], 0, LA);
     }
-    wait_vmcnt<(DEEP - 1) * (LA + LW)>();
+    issue_w(DEEP - 1, slots[DEEP - 1] + G::SLOT_A, 0, G::AHEAD_W);
+    issue_a(DEEP - 1, slots[DEEP - 1], 0, G::AHEAD_A);
+    wait_vmcnt<(DEEP - 2) * (LA + LW) + G::AHEAD_W + G::AHEAD_A>();
   } else {
-    issue_a(0, s0);
-    issue_w(0, s1);
-    issue_a(1, s2);
-    issue_w(1, s3);
-    wait_vmcnt<LA + LW>();
+    issue_a(0, s0, 0, LA);
+    issue_w(0, s1, 0, LW);
+    issue_a(1, s2, 0, LA);
+    issue_w(1, s3, 0, G::AHEAD_W);
+    issue_a(2, s4, 0, G::AHEAD_A);
+    wait_vmcnt<LA + G::AHEAD_W + G::AHEAD_A>();
   }
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   if (KF > 0) {
     fa[0] = read_a(s0, 0);
-    fw[0] = read_w(DEEP ? s0 + G::SLOT_A : s1, 0);
+#pragma unroll
+    for (int j = 0; j + 1 < TJ; ++j) fw[j] = read_w(DEEP ? s0 + G::SLOT_A : s1, j);
     int kt = 0;
     for (; kt + S <= KF; kt += S) {
       step(std::integral_constant<int, 0>{}, kt);
@@ -494,39 +553,43 @@ void block_gemm_kernel(BlockP p, int gm) {
     auto at = [&](int i) __attribute__((always_inline)) { return i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : i == 3 ? s3 : s4; };
     uint8_t* const A = at(ia);
     uint8_t* const W = at(iw) + (DEEP ? G::SLOT_A : 0);
-    if constexpr (EL == EL_FP8) scales_turn();
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      fw[j] = read_w(W, j);
-      cut(fw[j]);
+    if constexpr (EL == EL_FP8) {
+      if (KF % S == 0) turn_scales(KF);
+      open_scales(KF % S);
     }
 #pragma unroll
+    for (int j = 0; j < TJ; ++j) fw[j] = cut(read_w(W, j));
+#pragma unroll
     for (int i = 0; i < TI; ++i) {
-      Frag a = read_a(A, i);
-      cut(a);
+      const Frag a = cut(read_a(A, i));
 #pragma unroll
       for (int j = 0; j < TJ; ++j) tile(i, j, a);
     }
     __syncthreads();
   }
+  if constexpr (EL == EL_FP8) {   // the last two block sums
+    old_scale[0] = row_scale[0];
+    old_scale[1] = row_scale[1];
+    add_block(-2);
+    add_block(-1);
+  }
 
   // ---- epilogue ----
-  // lane: row i*32 + l32 of the wave, columns j*32 + 8 g + 4 half + [0, 4).  The
-  // tile goes through LDS in bf16, 16-byte chunks swizzled by the row, and leaves as
-  // whole rows.
+  // A lane holds quads of four consecutive columns of one row.  The tile goes through
+  // LDS in bf16, 16-byte chunks swizzled by the row, and leaves as whole rows.
   constexpr int OJ = EP == EP_GATED ? TJ / 2 : TJ;
   constexpr int SWM = OUT_N / 8 < 16 ? OUT_N / 8 - 1 : 15;
   const int n_lim = min(p.N, p.n_out) - n0;   // columns of the tile that exist
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    uint8_t* const slot = wm ? slots[(TI + i) * 32 / G::ROWS] : slots[i * 32 / G::ROWS];
-    uint8_t* const row = slot + (((wm * TI + i) * 32) % G::ROWS + l32) * G::ROW_BYTES;
-    const int m = m0 + (wm * TI + i) * 32 + l32;
+    uint8_t* const slot = wm ? slots[(TI + i) * R / G::ROWS] : slots[i * R / G::ROWS];
+    uint8_t* const row = slot + (((wm * TI + i) * R) % G::ROWS + rl) * G::ROW_BYTES;
+    const int m = m0 + (wm * TI + i) * R + rl;
 #pragma unroll
     for (int j = 0; j < OJ; ++j)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int c = wn * (OUT_N / WN) + j * 32 + 8 * g + 4 * half;
+      for (int g = 0; g < R * R / 256; ++g) {
+        const int c = wn * (OUT_N / WN) + j * R + (EL == EL_FP8 ? 0 : 8 * g) + 4 * part;
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
@@ -561,7 +624,7 @@ void block_gemm_kernel(BlockP p, int gm) {
             }
           }
         }
-        *reinterpret_cast<uint2*>(row + (((c >> 3) ^ (l32 & SWM)) * 16) + half * 8) =
+        *reinterpret_cast<uint2*>(row + (((c >> 3) ^ (rl & SWM)) * 16) + (c & 4) * 2) =
             make_uint2(pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3]));
       }
   }

@@ -31,8 +31,8 @@ hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t s) {
   const BlockP p = params(a);
   if (block_few(p)) return launch_block_few(p, EL_FP8, false, s);
   const bool big = gemm_tiles(a, 256, 256) >= 200;
-  if (a.goff) return big ? linear<true, 4, 2, 2, 4>(p, s) : linear<true, 2, 2, 2, 2>(p, s);
-  return big ? linear<false, 4, 2, 2, 4>(p, s) : linear<false, 2, 2, 2, 2>(p, s);
+  if (a.goff) return big ? linear<true, 8, 4, 2, 4>(p, s) : linear<true, 4, 4, 2, 2>(p, s);
+  return big ? linear<false, 8, 4, 2, 4>(p, s) : linear<false, 4, 4, 2, 2>(p, s);
 }
 
 hipError_t launch_gated_fp8(const GatedArgs& a, hipStream_t s) {
@@ -42,8 +42,8 @@ hipError_t launch_gated_fp8(const GatedArgs& a, hipStream_t s) {
   p.gate = a.gate; p.up = a.up; p.ld_saved = a.ld_saved; p.act = a.act;
   if (block_few(p)) return launch_block_few(p, EL_FP8, true, s);
   if (gemm_tiles(a.g, 256, 128) >= 200)
-    return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 2, 2, 4>(p, s);
-  return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_GATED, false, 2, 2, 2, 2>(p, s);
+    return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_GATED, false, 8, 4, 2, 4>(p, s);
+  return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 4, 2, 2>(p, s);
 }
 
 }  // namespace mxq
