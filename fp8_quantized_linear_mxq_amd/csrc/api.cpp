@@ -5,6 +5,7 @@
 // asynchronous on the caller's stream; the library holds no state.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -164,9 +165,9 @@ int64_t mxq_workspace_size(int32_t op, int64_t rows, int64_t cols, int32_t fmt) 
       if (fmt < 1 || fmt > 128 || fmt > rows || fmt > cols) return -1;
       return lowrank_split_workspace(rows, cols, fmt);
     case MXQ_OP_GATED_BACKWARD:
-      // rows = M, cols = N
-      if (rows > INT32_MAX / 2 || cols > kMaxLd / 4 - 64) return -1;
-      return gated_backward_workspace(rows, cols);
+      // rows = M, cols = N, fmt = K or 0
+      if (rows > INT32_MAX / 2 || cols > kMaxLd / 4 - 64 || fmt < 0) return -1;
+      return gated_backward_workspace(rows, cols, fmt);
     case MXQ_OP_LAYER_NORM_BACKWARD:
       if (cols > kMaxNormCols) return -1;
       return (int64_t)kLayerNormGroups * 2 * cols * 4;
@@ -618,7 +619,7 @@ mxq_status mxq_gemm_gated_backward(const void* dy, int64_t ld_dy, const mxq_qten
   if (!empty) {
     if (!dy || ld_dy < n || !saved) return MXQ_ERR_INVALID_ARG;
     if (!aligned(dy, 2) || !aligned(saved, 4)) return MXQ_ERR_ALIGNMENT;
-    if (!workspace || ws_bytes < (size_t)gated_backward_workspace(m, n) || !aligned(workspace, 16))
+    if (!workspace || ws_bytes < (size_t)gated_backward_workspace(m, n, 0) || !aligned(workspace, 16))
       return MXQ_ERR_WORKSPACE;
   }
   unsigned* dbg = nullptr;
@@ -646,6 +647,7 @@ mxq_status mxq_gemm_gated_backward(const void* dy, int64_t ld_dy, const mxq_qten
   g.dwu = static_cast<uint16_t*>(dw_up);
   g.ld_dw = ld_dw;
   g.ws = workspace;
+  g.ws_bytes = (int64_t)std::min<size_t>(ws_bytes, INT64_MAX);
   return from_hip(launch_gated_backward(g, as_stream(stream)));
 }
 

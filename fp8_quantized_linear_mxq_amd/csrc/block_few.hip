@@ -148,6 +148,16 @@ hipError_t by_waves(BlockP p, hipStream_t s) {
 
 }  // namespace
 
+// Where this kernel is the faster one, weights from HBM: up to 16 rows (gated: 32),
+// by expert on average, and wherever its 16 x 16 tiles fit the GPU about once (FP8, K =
+// 1152 / 4096: 32 x 4096 7.0 / 11.2 us against 7.1 / 15.8 on the tiled kernels, 128 x 1024
+// 5.7 against 6.2, 64 x 4608 10.0 / 7.2; gated, 32 x 4096 x 4096 18.1 / 22, bf16 30 / 33, 64 rows
+// 28.6 / 22.0, 51 / 34).
+bool block_few(const BlockP& p, bool gated) {
+  if (p.goff) return p.M <= 16 * (int64_t)p.groups;
+  return p.M <= (gated ? 32 : 16) || (double)((p.M + 15) / 16) * ((p.N + 15) / 16) <= (gated ? 320 : 576);
+}
+
 hipError_t launch_block_few(const BlockP& p, int el, bool gated, hipStream_t s) {
   if (el == EL_BF16) return by_waves<EL_BF16, true, false>(p, s);
   if (gated) return by_waves<EL_FP8, true, false>(p, s);

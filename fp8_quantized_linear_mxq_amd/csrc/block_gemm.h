@@ -37,6 +37,8 @@
 #include "grouped.h"
 #include "kernels.h"
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace mxq {
@@ -65,14 +67,31 @@ struct BlockP {
   // EP_SPLIT: rows [0, m_split) go to out, the others to out2, m_rows of each
   uint16_t* out2; int m_split, m_rows;
   const int32_t* goff; int groups;
+  // COL W: K split over this many workgroups of k_per K-tiles each; with part the sums
+  // of split s go there as fp32 [splits][M][N]
+  int splits, k_per;
+  float* part;
 };
+
+// Estimated time (us) of tile kernels: a workgroup alone (its K-tiles come at the
+// latency of the way from memory), and rounds of as many as fit the GPU, of which
+// the last may be partly filled.
+struct TileCost {
+  double lat0, lat1, fix, per;
+  int slots;
+  bool whole;   // one workgroup to a compute unit: rounds do not overlap
+};
+inline double tile_time(const TileCost& c, double tiles, double kt) {
+  const double lat = c.lat0 + c.lat1 * kt, full = c.fix + c.per * kt, r = tiles / c.slots, n = std::floor(r);
+  const double more = full > lat ? full - lat : 0.;
+  if (r <= 1) return lat + more * r;
+  if (c.whole) return n * full + (r > n ? lat + more * (r - n) : 0.) + 2.5;
+  return std::max(r, std::ceil(r) - 0.4) * full + 2.5;
+}
 
 // Products of few rows (block_few.hip).
 hipError_t launch_block_few(const BlockP& p, int el, bool gated, hipStream_t s);
-inline bool block_few(const BlockP& p) {
-  const double rows = p.goff ? (double)p.M / p.groups : p.M;
-  return rows <= 16 || (!p.goff && (double)((p.M + 15) / 16) * ((p.N + 15) / 16) <= 512);
-}
+bool block_few(const BlockP& p, bool gated);
 
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -111,16 +130,18 @@ struct BlockGemm {
   // Steps of a K-tile that loads are dealt to: rows (E4M3) or MFMA tiles; the
   // barrier is before step `OPEN`.
   static constexpr int STEPS = EL == EL_FP8 ? TI : TI * TJ, OPEN = EL == EL_FP8 ? TI - 1 : (TI - 1) * TJ;
-  // W loads go out two to a step, then the A loads one or two, the first at step OPEN
-  static constexpr int W_STEPS = (LW + 1) / 2, PER_A = (LA + STEPS - W_STEPS - 1) / (STEPS - W_STEPS);
+  // The W loads go out first, two to a step where there are enough, then the A loads,
+  // the first at step OPEN.
+  static constexpr int W_STEPS = (LW + 1) / 2 < (STEPS + 1) / 2 ? (LW + 1) / 2 : (STEPS + 1) / 2;
+  static constexpr int PER_W = (LW + W_STEPS - 1) / W_STEPS, PER_A = (LA + STEPS - W_STEPS - 1) / (STEPS - W_STEPS);
   static constexpr int turn(int t) { return t >= OPEN ? t - OPEN : t + STEPS - OPEN; }   // steps since the barrier
-  static constexpr int first_w(int t) { return turn(t) < W_STEPS ? 2 * turn(t) : LW; }
-  static constexpr int last_w(int t) { return turn(t) < W_STEPS && 2 * turn(t) + 2 < LW ? 2 * turn(t) + 2 : LW; }
+  static constexpr int first_w(int t) { return turn(t) < W_STEPS ? PER_W * turn(t) : LW; }
+  static constexpr int last_w(int t) { return turn(t) < W_STEPS && PER_W * turn(t) + PER_W < LW ? PER_W * turn(t) + PER_W : LW; }
   static constexpr int first_a(int t) { return turn(t) < W_STEPS ? 0 : (turn(t) - W_STEPS) * PER_A < LA ? (turn(t) - W_STEPS) * PER_A : LA; }
   static constexpr int last_a(int t) { return turn(t) < W_STEPS ? 0 : (turn(t) - W_STEPS + 1) * PER_A < LA ? (turn(t) - W_STEPS + 1) * PER_A : LA; }
   // W loads of the K-tile after next that are out before K-tile 0 begins
   static constexpr int AHEAD_W = last_w(STEPS - 1), AHEAD_A = last_a(STEPS - 1);
-  static_assert(WM == 2 && TJ >= 2 && (EL == EL_BF16 ? TI % 2 == 0 || DEEP % 2 == 0 : TI % 4 == 0 && TJ == 4), "the walk's fragment buffers");
+  static_assert(WM == 2 && TJ >= 2 && (EL == EL_BF16 ? TI % 2 == 0 || DEEP % 2 == 0 : TI % 2 == 0 && TI * TJ % 4 == 0), "the walk's fragment buffers");
   static_assert(DEEP > 0 || TBM == TBN, "five equal slots");
   static_assert(DEEP == 0 || DEEP >= 3, "one K-tile in use, one landed, others on their way");
   static_assert(EL == EL_BF16 || (AL == LAY_ROW && WL == LAY_ROW), "transposing reads are of 16-bit elements");
@@ -218,7 +239,13 @@ void block_gemm_kernel(BlockP p, int gm) {
       s4[S > 4 ? G::SLOT : 16];
   uint8_t* const slots[5] = {s0, s1, s2, s3, s4};
 
-  const int bid = (int)block_index();
+  int bid = (int)block_index(), split = 0;
+  if constexpr (WL == LAY_COL) {
+    const int tiles = p.tiles_m * p.tiles_n;
+    split = bid / tiles;
+    bid -= split * tiles;
+    if (split >= p.splits) return;
+  }
   int tm, tn, m0;
   if constexpr (GRP) {
     const GroupScan gs(p.goff, p.groups, p.M, TBM);
@@ -245,7 +272,12 @@ void block_gemm_kernel(BlockP p, int gm) {
   const int wm = wave / WN, wn = wave % WN;
   constexpr int R = G::R;
   const int rl = lane % R, part = lane / R;
-  const int KF = p.K / G::KT_ELEMS;                       // whole K-tiles
+  int KF = p.K / G::KT_ELEMS;                             // whole K-tiles
+  int k_first = 0;                                        // the first of this workgroup's
+  if constexpr (WL == LAY_COL) {
+    k_first = __builtin_amdgcn_readfirstlane(split * p.k_per);
+    KF = min(p.k_per, KF - k_first);
+  }
   const int rest = (p.K % G::KT_ELEMS) * (EL == EL_FP8 ? 1 : 2) / 16;   // 16-byte chunks of a last one
   const int KT = KF + (rest > 0);
 
@@ -309,8 +341,9 @@ void block_gemm_kernel(BlockP p, int gm) {
   // first chunk of the K-tile, K-rows past it the last K-row
   auto issue_a = [&](int kt, uint8_t* slot, int t0, int t1) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
-    const uint8_t* b = abase + (AL == LAY_ROW ? (int64_t)kt * 128 : (int64_t)kt * 64 * lda);
-    const uint32_t back = AL == LAY_ROW && kt == KF && lc >= rest * 16 ? lc : 0;
+    const int k = kt + k_first;
+    const uint8_t* b = abase + (AL == LAY_ROW ? (int64_t)k * 128 : (int64_t)k * 64 * lda);
+    const uint32_t back = WL == LAY_ROW && AL == LAY_ROW && kt == KF && lc >= rest * 16 ? lc : 0;
 #pragma unroll
     for (int t = 0; t < LA; ++t)
       if (t >= t0 && t < t1)
@@ -332,7 +365,7 @@ void block_gemm_kernel(BlockP p, int gm) {
         __builtin_amdgcn_global_load_lds(b + k + (uint64_t)(vw[t] - back), (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
       }
     } else {
-      int k0 = kt * 64;
+      int k0 = (kt + k_first) * 64;
       const uint8_t* b = wbase;
       uint32_t ld = ldw;
       if constexpr (EP == EP_LINEAR) {
@@ -374,7 +407,7 @@ void block_gemm_kernel(BlockP p, int gm) {
   // (one line each, the rows of a K-block lie together) and swaps quarters of the
   // wave when it comes to them; the wave's columns lie in one block of w's rows, and
   // lane l holds that block's scale of the loop's K-tile l.
-  constexpr int RAW = EL == EL_FP8 ? TI / 4 : 1;
+  constexpr int RAW = EL == EL_FP8 ? (TI + 3) / 4 : 1;
   float raw[RAW], raw_next[RAW], sa[4], sw_of[2], sw_next[2], sw[2], row_scale[2] = {0.f, 0.f}, old_scale[2] = {0.f, 0.f};
   const float *as = nullptr, *ws = nullptr, *ws2 = nullptr;
   if constexpr (EL == EL_FP8) {
@@ -388,7 +421,7 @@ void block_gemm_kernel(BlockP p, int gm) {
     const uint8_t* const b = reinterpret_cast<const uint8_t*>(as + (int64_t)kt * p.ldas);
 #pragma unroll
     for (int r = 0; r < RAW; ++r) {
-      uint32_t off = 4 * (wm * TI * 16 + 64 * r + lane);
+      const uint32_t off = 4 * (wm * TI * 16 + 64 * r + (TI < 4 ? lane & 31 : lane));
       raw_next[r] = *reinterpret_cast<const float*>(b + min(off, 4u * (uint32_t)(p.M - 1 - m0)));
     }
   };
@@ -578,6 +611,25 @@ void block_gemm_kernel(BlockP p, int gm) {
   // A lane holds quads of four consecutive columns of one row.  The tile goes through
   // LDS in bf16, 16-byte chunks swizzled by the row, and leaves as whole rows.
   constexpr int OJ = EP == EP_GATED ? TJ / 2 : TJ;
+  if constexpr (WL == LAY_COL) {
+    if (p.part) {   // N is a multiple of 8: whole quads
+      float* const sums = p.part + (int64_t)split * p.M * p.N;
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        const int m = m0 + (wm * TI + i) * R + rl;
+#pragma unroll
+        for (int j = 0; j < OJ; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int c = n0 + wn * (OUT_N / WN) + j * R + 8 * g + 4 * part;
+            if (m < p.M && c < p.N)
+              *reinterpret_cast<v4f*>(sums + (int64_t)m * p.N + c) =
+                  v4f{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+          }
+      }
+      return;
+    }
+  }
   constexpr int SWM = OUT_N / 8 < 16 ? OUT_N / 8 - 1 : 15;
   const int n_lim = min(p.N, p.n_out) - n0;   // columns of the tile that exist
 #pragma unroll
@@ -670,11 +722,11 @@ hipError_t launch_block_gemm(BlockP p, hipStream_t s) {
   using G = BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP>;
   p.tiles_m = GRP ? (int)group_tiles_bound(p.M, p.groups, G::TBM) : (p.M + G::TBM - 1) / G::TBM;
   p.tiles_n = (p.N + G::OUT_N - 1) / G::OUT_N;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  if (tiles > INT32_MAX) return hipErrorInvalidValue;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, blocks = tiles * std::max(p.splits, 1);
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
   int gm = 1;
   while (gm * 2 <= p.tiles_m && (int64_t)gm * 2 * gm * 2 <= (tiles + 7) / 8) gm *= 2;
-  block_gemm_kernel<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP><<<grid_of(tiles), G::THREADS, 0, s>>>(p, gm);
+  block_gemm_kernel<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP><<<grid_of(blocks), G::THREADS, 0, s>>>(p, gm);
   return hipGetLastError();
 }
 

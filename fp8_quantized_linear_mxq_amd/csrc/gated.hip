@@ -99,13 +99,137 @@ hipError_t zero_rows(uint16_t* p, int64_t ld, int64_t rows, int64_t cols, hipStr
   return hipGetLastError();
 }
 
+// Times of the tile kernels, fits as in gemm_fp8.hip: 256 x 256, 128 x 128, and with whole
+// K-tiles in flight 64 x 128 (M x K x N 4096 x 4096 x 4096 gated 218 / 269 / 451 us, 512 x 4096 x
+// 4096 81 / 55 / 62, 256 x 4096 x 4096 82 / 53 / 34).
+constexpr TileCost kBig = {7.3, 1.1, 8.0, 1.6, 256, true}, kMid = {0.5, 0.84, 4.0, 1.02, 512, false},
+                   kSmall = {1.0, 0.5, 2.0, 0.48, 256, false};
+
+double tiles_of(const BlockP& p, int tm, int tn) { return (double)((p.M + tm - 1) / tm) * ((p.N + tn - 1) / tn); }
+
+hipError_t gated_tiles(const BlockP& p, hipStream_t s) {
+  const double kt = (p.K + 63) / 64;
+  const double t1 = tile_time(kSmall, tiles_of(p, 64, 64), kt), t2 = tile_time(kMid, tiles_of(p, 128, 64), kt),
+               t4 = tile_time(kBig, tiles_of(p, 256, 128), kt);
+  if (t4 < t2 && t4 < t1) return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 2, 2, 4>(p, s);
+  if (t2 < t1) return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 2, 2, 2, 2>(p, s);
+  return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 1, 2, 2, 2, 4>(p, s);
+}
+
+// A gradient's product: the tile shape and over how many workgroups its K-tiles are
+// split (fp32 sums in the workspace, added in order by a second kernel): dx has few
+// tiles where there are few rows, and 2 N of K.
+struct GradPlan { int shape, splits; };
+
+GradPlan grad_plan(const BlockP& p, bool dw, int64_t room) {
+  const double kt = p.K / 64, mn = (double)p.M * p.N;
+  GradPlan best{4, 1};
+  double least = 1e30;
+  for (int shape : {4, 2, 1}) {
+    const int tm = shape == 4 ? 256 : shape == 2 || dw ? 128 : 64, tn = shape == 4 ? 256 : 128;
+    // the weights' gradients take no 64-row tiles (four swizzled segments to a K-row)
+    if (shape == 1 && dw) continue;
+    const TileCost& c = shape == 4 ? kBig : shape == 2 ? kMid : kSmall;
+    for (int s = 1; s <= 16 && s * 4 <= std::max(kt, 4.); s *= 2) {
+      if (s > 1 && (double)s * mn * 4 > (double)room) break;
+      // the sums: written, read and rounded at some 4 TB/s, and a launch
+      const double t = tile_time(c, tiles_of(p, tm, tn) * s, std::ceil(kt / s)) + (s > 1 ? 3.0 + s * mn * 8 / 4e6 : 0.);
+      if (t < least) {
+        least = t;
+        best = {shape, s};
+      }
+    }
+  }
+  return best;
+}
+
+struct SumP {
+  const float* part;
+  int M, N, splits;
+  uint16_t* out; uint16_t* out2; int64_t ld_out;
+  int m_split, m_rows;
+};
+
+// Rows of out (and from m_split on of out2) from the splits' sums, four columns to a thread.
+__global__ __launch_bounds__(kGradThreads) void split_sum_kernel(SumP p) {
+  const int64_t t = (int64_t)block_index() * kGradThreads + threadIdx.x, quads = p.N / 4;
+  if (t >= p.M * quads) return;
+  int64_t row = t / quads;
+  const int c = (int)(t % quads) * 4;
+  uint16_t* o = p.out;
+  const float* const from = p.part + row * p.N + c;
+  if (row >= p.m_split) {
+    row -= p.m_split;
+    o = p.out2;
+  }
+  if (row >= p.m_rows) return;
+  v4f s = *reinterpret_cast<const v4f*>(from);
+  for (int k = 1; k < p.splits; ++k) s += *reinterpret_cast<const v4f*>(from + (int64_t)k * p.M * p.N);
+  o += row * p.ld_out + c;
+  const uint32_t lo = pack_bf16_rne(s[0], s[1]), hi = pack_bf16_rne(s[2], s[3]);
+  if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+  } else {
+    o[0] = (uint16_t)lo;
+    o[1] = (uint16_t)(lo >> 16);
+    o[2] = (uint16_t)hi;
+    o[3] = (uint16_t)(hi >> 16);
+  }
+}
+
+template <int AL, int EP>
+hipError_t grad_product(BlockP p, float* part, int64_t room, hipStream_t s) {
+  constexpr bool dw = EP == EP_SPLIT;
+  const GradPlan plan = grad_plan(p, dw, room);
+  const int kt = p.K / 64;
+  p.k_per = (kt + plan.splits - 1) / plan.splits;
+  p.splits = (kt + p.k_per - 1) / p.k_per;
+  p.part = p.splits > 1 ? part : nullptr;
+  hipError_t e;
+  if (plan.shape == 4) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 4, 2, 2, 4>(p, s);
+  else if (plan.shape == 2 || dw) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 2, 2, 2, 2>(p, s);
+  else if constexpr (!dw) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 1, 2, 2, 2, 4>(p, s);
+  if (e != hipSuccess || !p.part) return e;
+  SumP q{p.part, p.M, p.N, p.splits, p.out, p.out2, p.ld_out, dw ? p.m_split : p.M, dw ? p.m_rows : p.M};
+  split_sum_kernel<<<grid_of(((int64_t)p.M * (p.N / 4) + kGradThreads - 1) / kGradThreads), kGradThreads, 0, s>>>(q);
+  return hipGetLastError();
+}
+
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
-int64_t gated_backward_workspace(int64_t M, int64_t N) { return pad64(M) * 2 * pad64(N) * 2; }
+namespace {
+
+// P; then, shared by the two products in turn, the splits' sums: both shapes are
+// known, so this is what grad_plan() asks for given any room.
+int64_t p_bytes(int64_t M, int64_t N) { return pad64(M) * 2 * pad64(N) * 2; }
+
+BlockP dx_shape(int64_t M, int64_t N, int64_t K) {
+  BlockP p{};
+  p.M = (int)M; p.N = p.n_out = (int)K; p.K = (int)(2 * pad64(N));
+  return p;
+}
+
+BlockP dw_shape(int64_t M, int64_t N, int64_t K) {
+  BlockP p{};
+  p.M = (int)(2 * pad64(N)); p.N = p.n_out = (int)K; p.K = (int)pad64(M);
+  return p;
+}
+
+int64_t split_bytes(const BlockP& p, bool dw) {
+  const int s = grad_plan(p, dw, INT64_MAX).splits;
+  return s > 1 ? (int64_t)s * p.M * p.N * 4 : 0;
+}
+
+}  // namespace
+
+int64_t gated_backward_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0 || K == 0) return p_bytes(M, N);
+  return p_bytes(M, N) + std::max(split_bytes(dx_shape(M, N, K), false), split_bytes(dw_shape(M, N, K), true));
+}
 
 hipError_t launch_gated_bf16(const GatedArgs& a, hipStream_t s) {
   BlockP p{};
@@ -116,10 +240,8 @@ hipError_t launch_gated_bf16(const GatedArgs& a, hipStream_t s) {
   p.out = a.g.out; p.ld_out = a.g.ld_out; p.n_out = (int)a.g.N;
   p.gate = a.gate; p.up = a.up; p.ld_saved = a.ld_saved; p.act = a.act;
   p.saved_vec = p.N % 4 == 0 && al16(a.gate);
-  if (block_few(p)) return launch_block_few(p, EL_BF16, true, s);
-  if (gemm_tiles(a.g, 256, 128) >= 200)
-    return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 2, 2, 4>(p, s);
-  return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 2, 2, 2, 2>(p, s);
+  if (block_few(p, true)) return launch_block_few(p, EL_BF16, true, s);
+  return gated_tiles(p, s);
 }
 
 hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t s) {
@@ -142,29 +264,25 @@ hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t s) {
   else gated_grad_kernel<false><<<grid, kGradThreads, 0, s>>>(g, pieces);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const int64_t room = a.ws_bytes - p_bytes(a.M, a.N);
+  float* const part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + p_bytes(a.M, a.N));
   if (a.dx) {   // P [M, 2 np] x [Wg; Wu]
-    BlockP p{};
-    p.a = reinterpret_cast<const uint8_t*>(a.ws); p.lda = 4 * np;
+    BlockP p = dx_shape(a.M, a.N, a.K);
+    p.a = static_cast<const uint8_t*>(a.ws); p.lda = 4 * np;
     p.w = a.wg; p.ldw = a.ldw; p.w2 = a.wu; p.ldw2 = a.ldw2;
-    p.M = (int)a.M; p.N = p.n_out = (int)a.K; p.K = (int)(2 * np);
     p.k_split = (int)np; p.k_rows = (int)a.N;
     p.out = a.dx; p.ld_out = a.ld_dx;
-    const double tiles = (double)((p.M + 255) / 256) * ((p.N + 255) / 256);
-    e = tiles >= 200 ? launch_block_gemm<EL_BF16, LAY_ROW, LAY_COL, EP_LINEAR, false, 4, 2, 2, 4>(p, s)
-                     : launch_block_gemm<EL_BF16, LAY_ROW, LAY_COL, EP_LINEAR, false, 2, 2, 2, 2>(p, s);
+    e = grad_product<LAY_ROW, EP_LINEAR>(p, part, room, s);
     if (e != hipSuccess) return e;
   }
   if (a.dwg) {   // P^T [2 np, M] x x
-    BlockP p{};
-    p.a = reinterpret_cast<const uint8_t*>(a.ws); p.lda = 4 * np;
+    BlockP p = dw_shape(a.M, a.N, a.K);
+    p.a = static_cast<const uint8_t*>(a.ws); p.lda = 4 * np;
     p.w = p.w2 = a.x; p.ldw = p.ldw2 = a.ldx;
-    p.M = (int)(2 * np); p.N = p.n_out = (int)a.K; p.K = (int)mp;
     p.k_split = (int)mp; p.k_rows = (int)a.M;
     p.out = a.dwg; p.out2 = a.dwu; p.ld_out = a.ld_dw;
     p.m_split = (int)np; p.m_rows = (int)a.N;
-    const double tiles = (double)((p.M + 255) / 256) * ((p.N + 255) / 256);
-    e = tiles >= 200 ? launch_block_gemm<EL_BF16, LAY_COL, LAY_COL, EP_SPLIT, false, 4, 2, 2, 4>(p, s)
-                     : launch_block_gemm<EL_BF16, LAY_COL, LAY_COL, EP_SPLIT, false, 2, 2, 2, 2>(p, s);
+    e = grad_product<LAY_COL, EP_SPLIT>(p, part, room, s);
   }
   return e;
 }

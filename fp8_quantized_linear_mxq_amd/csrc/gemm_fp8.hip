@@ -20,19 +20,29 @@ BlockP params(const GemmArgs& a) {
   return p;
 }
 
-template <bool GRP, int TI, int TJ, int WM, int WN>
-hipError_t linear(const BlockP& p, hipStream_t s) {
-  return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_LINEAR, GRP, TI, TJ, WM, WN>(p, s);
+// The tile kernels: 256 x 256, 128 x 128, and 64 x 64 with whole K-tiles in flight.
+// Larger tiles load fewer bytes per product, smaller ones fill the GPU: M x K x N 4096^3
+// 72 / 85 / 157 us, 1024 x 4096 x 4096 51 / 27 / 36, 256 x 4096 x 4096 50 / 24 / 16, 2048 x
+// 1152 x 1024 20 / 11.2 / 8.7.  The constants are fits to 32 .. 8192 rows, 512 .. 4608
+// columns and K = 512 .. 8192, operands from HBM, within some 20%.
+template <int EP, bool GRP>
+hipError_t tiles(const BlockP& p, const GemmArgs& a, hipStream_t s) {
+  const int half = EP == EP_GATED ? 2 : 1;
+  const double kt = (p.K + 127) / 128;
+  const double t1 = tile_time({2.2, 0.5, 1.5, 0.55, 512, false}, gemm_tiles(a, 64, 64 / half), kt);
+  const double t2 = tile_time({3.4, 0.7, 5.5, 1.19, 512, false}, gemm_tiles(a, 128, 128 / half), kt);
+  const double t4 = tile_time({6.5, 1.4, 6.0, 1.95, 256, true}, gemm_tiles(a, 256, 256 / half), kt);
+  if (t4 < t2 && t4 < t1) return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 8, 4, 2, 4>(p, s);
+  if (t2 < t1) return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 4, 4, 2, 2>(p, s);
+  return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 2, 2, 2, 2, 4>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t s) {
   const BlockP p = params(a);
-  if (block_few(p)) return launch_block_few(p, EL_FP8, false, s);
-  const bool big = gemm_tiles(a, 256, 256) >= 200;
-  if (a.goff) return big ? linear<true, 8, 4, 2, 4>(p, s) : linear<true, 4, 4, 2, 2>(p, s);
-  return big ? linear<false, 8, 4, 2, 4>(p, s) : linear<false, 4, 4, 2, 2>(p, s);
+  if (block_few(p, false)) return launch_block_few(p, EL_FP8, false, s);
+  return a.goff ? tiles<EP_LINEAR, true>(p, a, s) : tiles<EP_LINEAR, false>(p, a, s);
 }
 
 hipError_t launch_gated_fp8(const GatedArgs& a, hipStream_t s) {
@@ -40,10 +50,8 @@ hipError_t launch_gated_fp8(const GatedArgs& a, hipStream_t s) {
   p.w2 = a.w2_codes; p.ldw2 = a.ldw2;
   p.ws2 = reinterpret_cast<const float*>(a.w2_scales); p.ldws2 = a.ld_ws2 / 4;
   p.gate = a.gate; p.up = a.up; p.ld_saved = a.ld_saved; p.act = a.act;
-  if (block_few(p)) return launch_block_few(p, EL_FP8, true, s);
-  if (gemm_tiles(a.g, 256, 128) >= 200)
-    return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_GATED, false, 8, 4, 2, 4>(p, s);
-  return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 4, 2, 2>(p, s);
+  if (block_few(p, true)) return launch_block_few(p, EL_FP8, true, s);
+  return tiles<EP_GATED, false>(p, a.g, s);
 }
 
 }  // namespace mxq

@@ -162,9 +162,10 @@ struct GatedBwdArgs {
   int act;
   uint16_t* dx; int64_t ld_dx;
   uint16_t* dwg; uint16_t* dwu; int64_t ld_dw;
-  void* ws;                                      // gated_backward_workspace() bytes
+  void* ws; int64_t ws_bytes;                    // at least those for K = 0
 };
-int64_t gated_backward_workspace(int64_t M, int64_t N);
+// dg and du, and with K given the fp32 sums of products whose K is split.
+int64_t gated_backward_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t s);
 
 // Layer norm of the rows of a matrix; weight, bias and stats may be null.

@@ -508,7 +508,7 @@ PyObject* gemm_gated_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     };
     if (!gradient(dx, mx, want_dx, rows) || !gradient(dg, mg, want_dw, outs) || !gradient(du, mu, want_dw, outs)) return nullptr;
     if (dg && outs > 1 && ld(*dg) != ld(*du)) return refuse("dw_gate and dw_up have one row stride");
-    const int64_t need = g_ws_size(MXQ_OP_GATED_BACKWARD, rows, outs, 0);
+    const int64_t need = g_ws_size(MXQ_OP_GATED_BACKWARD, rows, outs, (int32_t)std::min<int64_t>(k, INT32_MAX));
     if (!ws && need > 0) {
       mw = at::empty({need}, x.t_codes.options().dtype(at::kByte).requires_grad(false));
       ws = &mw;

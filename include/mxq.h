@@ -432,8 +432,12 @@ mxq_status mxq_gemm_gated(const mxq_qtensor* x, const mxq_qtensor* w_gate, const
  *  dx          device bf16 [M][ld_dx], K columns, or NULL.
  *  dw_gate, dw_up  device bf16 [N][ld_dw], K columns; both or neither.
  *  workspace   mxq_workspace_size(MXQ_OP_GATED_BACKWARD, M, N, 0) bytes of device
- *              memory, 16-byte aligned: dg and du in bf16 (their one rounding
- *              before the sums), which calls that overlap in time cannot share.
+ *              memory at least, 16-byte aligned: dg and du in bf16 (their one
+ *              rounding before the sums), which calls that overlap in time cannot
+ *              share.  With (M, N, K) in place of (M, N, 0) there is room for the
+ *              fp32 sums of products with few output tiles, whose K is then split
+ *              over more workgroups and added in a fixed order; results are
+ *              deterministic for a given workspace size.
  * Without terms (N = 0 for dx, M = 0 for the weights) a gradient is zero.  A
  * padded row's gradients are zero where its dy is zero, provided its x, g and u
  * are finite.
@@ -613,8 +617,8 @@ enum { MXQ_OP_QUANTIZE = 1, MXQ_OP_GEMM = 2, MXQ_OP_SELECT = 3, MXQ_OP_QUANTIZE_
  * fmt (0 when none); for MXQ_OP_GEMM rows = M, cols = N (weight rows) and
  * fmt = the weight format (the optional split-K workspace); for
  * MXQ_OP_LOWRANK_SPLIT rows = n, cols = k and fmt = the rank; for
- * MXQ_OP_GATED_BACKWARD rows = M, cols = N; for MXQ_OP_LAYER_NORM_BACKWARD the
- * norm's rows and cols (fmt is not read for these two).  Returns -1 for
+ * MXQ_OP_GATED_BACKWARD rows = M, cols = N and fmt = K or 0; for
+ * MXQ_OP_LAYER_NORM_BACKWARD the norm's rows and cols.  Returns -1 for
  * unknown arguments.  Host-only. */
 int64_t mxq_workspace_size(int32_t op, int64_t rows, int64_t cols, int32_t fmt);
 
