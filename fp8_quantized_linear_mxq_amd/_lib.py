@@ -304,7 +304,7 @@ def quantize(x, fmt: int, hadamard: int = 0, static_tensor_scale=None, l1t=None,
     rows, cols = x.shape
     dt = DT_BF16 if x.dtype == torch.bfloat16 else DT_F32
     if out is None:
-        out = (QTensor(INT8, rows, cols, *_fast.empty_int8(x)) if fmt == INT8 and cols % 32 == 0
+        out = (QTensor(fmt, rows, cols, *_fast.empty_rows(x, fmt)) if fmt in (INT8, FP8, FP8_TILE) and cols % 32 == 0
                else empty_qtensor(fmt, rows, cols, x.device))
     if workspace is None:
         n = workspace_size(OP_QUANTIZE, rows, cols, fmt) if fmt == NVFP4 else 0   # the one that needs any

@@ -29,48 +29,53 @@ struct GradP {
   int M, N, np, act;
 };
 
-// A thread takes 8 columns of a row.  VEC: rows of dy, g and u at 16-byte alignment.
-template <bool VEC>
+// A thread takes V columns of a row: 8, with rows of dy, g and u at 16-byte alignment
+// and N a multiple of 8, else 2 (a wave's loads then are runs of a row, whatever its
+// alignment: 1111 x 2003 17 us with 8).
+template <int V>
 __global__ __launch_bounds__(kGradThreads) void gated_grad_kernel(GradP a, int64_t pieces) {
   const int64_t t = (int64_t)block_index() * kGradThreads + threadIdx.x;
   if (t >= pieces) return;
-  const int per = a.np / 8;
+  const uint32_t per = a.np / V;
   const int64_t row = t / per;
-  const int c = (int)(t % per) * 8;
-  float dg[8], du[8];
+  const int c = (int)(t % per) * V;
+  float dg[V], du[V];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dg[e] = du[e] = 0.f;
-  if (row < a.M) {
-    float dy[8], g[8], u[8];
+  for (int e = 0; e < V; ++e) dg[e] = du[e] = 0.f;
+  if (row < a.M && c < a.N) {
+    float dy[V], g[V], u[V];
     const uint16_t* const y = a.dy + row * a.ld_dy + c;
     const float* const gr = a.gate + row * a.ld_saved + c;
     const float* const ur = a.up + row * a.ld_saved + c;
-    if (VEC && c < a.N) {   // N is a multiple of 8
-      const uint4 v = *reinterpret_cast<const uint4*>(y);
-      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (V == 8) {
+      const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(y));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        dy[2 * e] = __uint_as_float(d[e] << 16);
-        dy[2 * e + 1] = __uint_as_float(d[e] & 0xFFFF0000u);
+        dy[2 * e] = __uint_as_float(v[e] << 16);
+        dy[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const v4f gv = *reinterpret_cast<const v4f*>(gr + 4 * h), uv = *reinterpret_cast<const v4f*>(ur + 4 * h);
+        const v4f gv = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(gr + 4 * h));
+        const v4f uv = __builtin_nontemporal_load(reinterpret_cast<const v4f*>(ur + 4 * h));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           g[4 * h + e] = gv[e];
           u[4 * h + e] = uv[e];
         }
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int k = c + e < a.N ? e : 0;
+        dy[e] = bf16_bits_to_f32(y[k]);
+        g[e] = gr[k];
+        u[e] = ur[k];
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (c + e >= a.N) continue;
-      if (!VEC) {
-        dy[e] = bf16_bits_to_f32(y[e]);
-        g[e] = gr[e];
-        u[e] = ur[e];
-      }
+    for (int e = 0; e < V; ++e) {
+      if (V == 2 && c + e >= a.N) continue;
       float d;
       const float f = activation<true>(a.act, g[e], &d);
       dg[e] = dy[e] * u[e] * d;
@@ -78,12 +83,19 @@ __global__ __launch_bounds__(kGradThreads) void gated_grad_kernel(GradP a, int64
     }
   }
   uint16_t* const o = a.p + row * 2 * a.np + c;
-  auto pack = [](const float (&v)[8]) {
-    return make_uint4(pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3]), pack_bf16_rne(v[4], v[5]),
-                      pack_bf16_rne(v[6], v[7]));
-  };
-  *reinterpret_cast<uint4*>(o) = pack(dg);
-  *reinterpret_cast<uint4*>(o + a.np) = pack(du);
+  uint32_t pg[V / 2], pu[V / 2];
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) {
+    pg[e] = pack_bf16_rne(dg[2 * e], dg[2 * e + 1]);
+    pu[e] = pack_bf16_rne(du[2 * e], du[2 * e + 1]);
+  }
+  if constexpr (V == 8) {
+    *reinterpret_cast<uint4*>(o) = make_uint4(pg[0], pg[1], pg[2], pg[3]);
+    *reinterpret_cast<uint4*>(o + a.np) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+  } else {
+    *reinterpret_cast<uint32_t*>(o) = pg[0];
+    *reinterpret_cast<uint32_t*>(o + a.np) = pu[0];
+  }
 }
 
 // [rows][cols] bf16 zeros: the gradients of a product without terms.
@@ -257,11 +269,11 @@ hipError_t launch_gated_backward(const GatedBwdArgs& a, hipStream_t s) {
   g.gate = a.gate; g.up = a.up; g.ld_saved = a.ld_saved;
   g.p = static_cast<uint16_t*>(a.ws);
   g.M = (int)a.M; g.N = (int)a.N; g.np = (int)np; g.act = a.act;
-  const int64_t pieces = mp * (np / 8);
   const bool vec = a.N % 8 == 0 && a.ld_dy % 8 == 0 && a.ld_saved % 4 == 0 && al16(a.dy) && al16(a.gate) && al16(a.up);
+  const int64_t pieces = mp * (np / (vec ? 8 : 2));
   const dim3 grid = grid_of((pieces + kGradThreads - 1) / kGradThreads);
-  if (vec) gated_grad_kernel<true><<<grid, kGradThreads, 0, s>>>(g, pieces);
-  else gated_grad_kernel<false><<<grid, kGradThreads, 0, s>>>(g, pieces);
+  if (vec) gated_grad_kernel<8><<<grid, kGradThreads, 0, s>>>(g, pieces);
+  else gated_grad_kernel<2><<<grid, kGradThreads, 0, s>>>(g, pieces);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t room = a.ws_bytes - p_bytes(a.M, a.N);

@@ -179,7 +179,7 @@ struct LayerNormArgs {
 };
 hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
 
-constexpr int kLayerNormGroups = 512;   // workgroups of the backward pass, at most
+constexpr int kLayerNormGroups = 256;   // workgroups of the backward pass, at most
 // Null gradients are left out; partial (null without dweight and dbias):
 // kLayerNormGroups * 2 * cols floats.
 struct LayerNormBwdArgs {

@@ -153,12 +153,12 @@ __global__ __launch_bounds__(kFwdThreads) void layer_norm_kernel(LayerNormArgs a
 
 // ---- backward -------------------------------------------------------------
 
-constexpr int kBwdThreads = 512;
+constexpr int kBwdThreads = 1024;   // one workgroup to a compute unit: as few rows of sums as there are units
 
 // A wave's W-wave group takes rows group, group + groups, ...; all groups of the
 // grid make the same number of steps, so that barriers are met by every wave.
 template <int DT, int V, int J, int W>
-__global__ __launch_bounds__(kBwdThreads, J * V > 16 ? 1 : 2) void layer_norm_bwd_kernel(LayerNormBwdArgs a) {
+__global__ __launch_bounds__(kBwdThreads) void layer_norm_bwd_kernel(LayerNormBwdArgs a) {
   constexpr int GR = kBwdThreads / 64 / W, STEP = W * 64 * V, P = J > 0 ? J : 1;
   __shared__ float red[2][2][kBwdThreads / 64];
   __shared__ float fold[J > 0 && GR > 1 ? GR * P * STEP : 1];
@@ -324,8 +324,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void layer_norm_sum_kernel(const fl
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (c < 2 * (int64_t)C)
+  if (c < 2 * (int64_t)C) {
+#pragma unroll 8
     for (int g = wave; g < groups; g += kSumWaves) s += partial[(int64_t)g * 2 * C + c];
+  }
   red[wave][lane] = s;
   __syncthreads();
   if (wave != 0 || c >= 2 * (int64_t)C) return;
@@ -361,8 +363,8 @@ hipError_t bwd_shape(int64_t cols, F f) {
   if (cols <= 2 * J * one) return f(I<J>{}, I<2>{});
   if (cols <= 4 * J * one) return f(I<J>{}, I<4>{});
   if (cols <= 8 * J * one) return f(I<J>{}, I<8>{});
-  if (cols <= 16 * J * one) return f(I<2 * J>{}, I<8>{});
-  return f(I<0>{}, I<8>{});
+  if (cols <= 16 * J * one) return f(I<J>{}, I<16>{});
+  return f(I<0>{}, I<16>{});
 }
 
 template <int DT, int V>

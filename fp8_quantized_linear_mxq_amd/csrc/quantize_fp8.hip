@@ -5,8 +5,8 @@
 //   s = RN_fp32(max over the block |r| / 448),  q = RNE_E4M3(r / s)
 //
 // decided on the exact real quotient (s = 0 gives zeros).  The quotient is formed
-// as t = r * (1 / s), whose two roundings move it by less than 2.2 units of its
-// last place, and converted by the hardware.  A code can only be wrong where t
+// as t = r * (1 / s), which the hardware's reciprocal (one unit) and the product move
+// by at most 3 units of its last place, and converted by the hardware.  A code can only be wrong where t
 // lies within 4 units of the middle between two codes (bits 0x80000 below the
 // three that E4M3 keeps) or is subnormal in E4M3 (below 2**-6, where the middles
 // lie elsewhere); a lane that holds such an element compares it with the middle
@@ -96,7 +96,12 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return (float)((double)amax / 448.0); }
+// RN_fp32(amax / 448): the compiler's fp32 division is correctly rounded; quotients
+// that are subnormal, where it may flush, take float64 (whose rounding to fp32 is
+// right for a quotient of two fp32 values).
+__device__ __forceinline__ float scale_of(float amax) {
+  return amax >= 0x1p-100f ? amax / 448.0f : (float)((double)amax / 448.0);
+}
 
 // A workgroup takes 32 rows x 4 blocks: lane group l / 16 of a wave one block of
 // the row, so a wave's load is one contiguous kilobyte of bf16, eight rows in
@@ -128,7 +133,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(Fp8Params p) {
     const bool fast = s >= 0x1p-100f;
     if ((lane & 15) == 0) sc[lane >> 4][r] = s;
     if (c < p.cols)
-      *reinterpret_cast<uint2*>(p.codes + (row0 + r) * p.ld_codes + c) = encode8(f, s, fast ? 1.0f / s : 0.f, fast);
+      *reinterpret_cast<uint2*>(p.codes + (row0 + r) * p.ld_codes + c) = encode8(f, s, fast ? __builtin_amdgcn_rcpf(s) : 0.f, fast);
   }
   __syncthreads();
   const int t = threadIdx.x, kb = t / kRows, r = t % kRows;
@@ -166,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_tile_kernel(Fp8Params p
   const float s = scale_of(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
   if (threadIdx.x == 0) *reinterpret_cast<float*>(p.scales + (int64_t)tr * p.ld_scales + (int64_t)tc * 4) = s;
   const bool fast = s >= 0x1p-100f;
-  const float inv = fast ? 1.0f / s : 0.f;
+  const float inv = fast ? __builtin_amdgcn_rcpf(s) : 0.f;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     float f[8];

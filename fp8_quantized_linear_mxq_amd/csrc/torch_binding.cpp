@@ -245,18 +245,23 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// empty_int8(x) -> (codes uint8 [rows, cols], scales float32 [rows, 1]) for a quantized x
-PyObject* empty_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// empty_rows(x, fmt) -> (codes uint8 [rows, cols], scales float32) for a quantized x:
+// int8 [rows, 1], FP8 [cols / 128, rows], FP8_TILE [rows / 128, cols / 128]
+PyObject* empty_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const at::Tensor* x;
-    if (!count(n, 1) || !to_tensor(a[0], &x, "x is a tensor")) return nullptr;
+    int64_t fmt;
+    if (!count(n, 2) || !to_tensor(a[0], &x, "x is a tensor") || !to_i64(a[1], &fmt)) return nullptr;
     if (!x || x->dim() != 2) {
       fail("quantize needs a 2-D tensor");
       return nullptr;
     }
     const auto opt = x->options().requires_grad(false);
+    const int64_t rows = x->size(0), blocks = (x->size(1) + 127) / 128;
+    const int64_t shape[2] = {fmt == MXQ_FMT_FP8 ? blocks : fmt == MXQ_FMT_FP8_TILE ? (rows + 127) / 128 : rows,
+                              fmt == MXQ_FMT_FP8 ? rows : fmt == MXQ_FMT_FP8_TILE ? blocks : 1};
     PyObject* c = THPVariable_Wrap(at::empty(x->sizes(), opt.dtype(at::kByte).memory_format(at::MemoryFormat::Contiguous)));
-    PyObject* s = THPVariable_Wrap(at::empty({x->size(0), 1}, opt.dtype(at::kFloat)));
+    PyObject* s = THPVariable_Wrap(at::empty(at::IntArrayRef(shape, 2), opt.dtype(at::kFloat)));
     PyObject* r = c && s ? PyTuple_Pack(2, c, s) : nullptr;
     Py_XDECREF(c);
     Py_XDECREF(s);
@@ -664,7 +669,7 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {
-    method<bind>("bind"), method<quantize>("quantize"), method<empty_int8>("empty_int8"), method<gemm>("gemm"),
+    method<bind>("bind"), method<quantize>("quantize"), method<empty_rows>("empty_rows"), method<gemm>("gemm"),
     method<gemm_grouped>("gemm_grouped"), method<qk_norm_rope>("qk_norm_rope"), method<gemm_gated>("gemm_gated"),
     method<gemm_gated_backward>("gemm_gated_backward"), method<layer_norm>("layer_norm"),
     method<layer_norm_backward>("layer_norm_backward"), {nullptr, nullptr, 0, nullptr}};
