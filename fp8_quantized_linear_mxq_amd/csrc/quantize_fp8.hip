@@ -8,9 +8,8 @@
 // as t = r * (1 / s), which the hardware's reciprocal (one unit) and the product move
 // by at most 3 units of its last place, and converted by the hardware.  A code can only be wrong where t
 // lies within 4 units of the middle between two codes (bits 0x80000 below the
-// three that E4M3 keeps) or is subnormal in E4M3 (below 2**-6, where the middles
-// lie elsewhere); a lane that holds such an element compares it with the middle
-// exactly: fma(-middle, s, r) has the sign of r / s - middle.  bf16 inputs tie
+// three that E4M3 keeps; below 2**-6, where codes are 2**-9 apart, of t + 2**-6); a
+// lane that holds such an element compares it with the middle exactly: fma(-middle, s, r) has the sign of r / s - middle.  bf16 inputs tie
 // often (both mantissas are short), so this path costs no float64.  Scales below
 // 2**-100, where the remainder could underflow, take float64 quotients.
 //
@@ -25,7 +24,6 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 32;   // rows of a workgroup of the row-wise format: 8 per wave
 
 struct Fp8Params {
   const void* x;
@@ -38,78 +36,108 @@ struct Fp8Params {
   unsigned* dbg;
 };
 
-// Codes of two values.
-__device__ __forceinline__ uint32_t cvt2(float a, float b) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false) & 0xFFFFu;
-}
-
-// t, whose true value is f / s, moved off the middle between two codes to the side
-// that f / s lies on.
-__device__ __forceinline__ float settle(float t, float f, float s) {
-  const uint32_t b = __float_as_uint(t);
-  const float a = fabsf(t), m = fabsf(f);
-  if (a >= 0x1p-6f) {
-    if (((b - 0x7FFFCu) & 0xFFFFFu) > 8u) return t;
-    const uint32_t mid = (b & ~0xFFFFFu) | 0x80000u;
-    const float r = __builtin_fmaf(-fabsf(__uint_as_float(mid)), s, m);
-    return __uint_as_float(r > 0.f ? mid + 1u : r < 0.f ? mid - 1u : mid);
-  }
-  // subnormal codes: multiples of 2**-9, 2**-6 among them
-  const float fl = floorf(a * 512.f), mid = (fl + 0.5f) * 0x1p-9f;
-  const float r = __builtin_fmaf(-mid, s, m);
-  const bool up = r > 0.f || (r == 0.f && ((int)fl & 1));
-  return copysignf((fl + (up ? 1.f : 0.f)) * 0x1p-9f, t);
-}
-
 // 8 codes of values with scale s (inv = 1 / s, usable when `fast`).
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv, bool fast) {
+  if (!fast) {
+    uint32_t q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      q[e] = s == 0.f ? 0u : e4m3_encode_f64(fabs((double)f[e] / (double)s));
+      q[e] |= (__float_as_uint(f[e]) >> 24) & 0x80u;
+    }
+    return make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+  }
   float t[8];
-  uint32_t mid = ~0u, low = ~0u;   // smallest distance to a middle, smallest nonzero magnitude
+  uint32_t v[8], near = ~0u;   // smallest distance to a middle
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     t[e] = f[e] * inv;
-    const uint32_t b = __float_as_uint(t[e]);
-    mid = min(mid, (b - 0x7FFFCu) & 0xFFFFFu);
-    low = min(low, (b & 0x7FFFFFFFu) - 1u);
+    // subnormal codes are as far apart as those of the first binade, 2**-6 on
+    const float a = fabsf(t[e]);
+    v[e] = __float_as_uint(a < 0x1p-6f ? a + 0x1p-6f : a);
+    near = min(near, (v[e] - 0x7FFFCu) & 0xFFFFFu);
   }
-  uint32_t c[4];
-  if (!fast) {
+  if (near <= 8u) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t q[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float v = f[2 * e + k];
-        q[k] = s == 0.f ? 0u : e4m3_encode_f64(fabs((double)v / (double)s));
-        q[k] |= (__float_as_uint(v) >> 24) & 0x80u;
-      }
-      c[e] = q[0] | q[1] << 8;
+    for (int e = 0; e < 8; ++e) {
+      // f / s against the middle, exactly; t goes to the side it lies on, or onto the
+      // middle, from which the conversion rounds to even
+      const float m = __uint_as_float((v[e] & ~0xFFFFFu) | 0x80000u), mid = fabsf(t[e]) < 0x1p-6f ? m - 0x1p-6f : m;
+      const float r = __builtin_fmaf(-mid, s, fabsf(f[e]));
+      const float to = r > 0.f ? mid * 1.0009765625f : r < 0.f ? mid * 0.9990234375f : mid;
+      if (((v[e] - 0x7FFFCu) & 0xFFFFFu) <= 8u) t[e] = copysignf(to, t[e]);
     }
-  } else {
-    if (mid <= 8u || low < 0x3C7FFFFFu) {   // 2**-6 - 1 unit
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = settle(t[e], f[e], s);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = cvt2(t[2 * e], t[2 * e + 1]);
   }
-  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// RN_fp32(amax / 448): the compiler's fp32 division is correctly rounded; quotients
-// that are subnormal, where it may flush, take float64 (whose rounding to fp32 is
-// right for a quotient of two fp32 values).
+// RN_fp32(amax / 448) from the product with the reciprocal and its exact remainder
+// (right for every mantissa: compared over all 2**23); amax whose remainder could
+// underflow takes float64, whose quotient of two fp32 values rounds rightly.
 __device__ __forceinline__ float scale_of(float amax) {
-  return amax >= 0x1p-100f ? amax / 448.0f : (float)((double)amax / 448.0);
+  if (!(amax >= 0x1p-90f)) return (float)((double)amax / 448.0);
+  constexpr float r = 1.0f / 448.0f;
+  const float q = amax * r;
+  return __builtin_fmaf(__builtin_fmaf(-q, 448.0f, amax), r, q);
 }
 
-// A workgroup takes 32 rows x 4 blocks: lane group l / 16 of a wave one block of
-// the row, so a wave's load is one contiguous kilobyte of bf16, eight rows in
+// Largest magnitude of a lane's elements as bits: an integer maximum, packed for bf16
+// (NaNs aside, magnitudes are in the order of their bits).
+template <int DT>
+__device__ __forceinline__ uint32_t amax_bits(const Raw<DT>& w) {
+  if constexpr (DT == DT_BF16) {
+    typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+    const uint32_t d[4] = {w.lo.x, w.lo.y, w.lo.z, w.lo.w};
+    v2us m = __builtin_bit_cast(v2us, d[0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2us, d[i] & 0x7FFF7FFFu));
+    return (uint32_t)max(m.x, m.y) << 16;
+  } else {
+    const uint32_t d[8] = {w.lo.x, w.lo.y, w.lo.z, w.lo.w, w.hi.x, w.hi.y, w.hi.z, w.hi.w};
+    uint32_t m = d[0] & 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max(m, d[i] & 0x7FFFFFFFu);
+    return m;
+  }
+}
+
+// Maximum over G consecutive lanes.
+template <int G>
+__device__ __forceinline__ float lanes_max(uint32_t b) {
+  b = max(b, (uint32_t)xor_lane<1>((int)b));
+  b = max(b, (uint32_t)xor_lane<2>((int)b));
+  b = max(b, (uint32_t)xor_lane<4>((int)b));
+  b = max(b, (uint32_t)xor_lane<8>((int)b));
+  if constexpr (G == 64) {
+    b = max(b, (uint32_t)xor_lane<16>((int)b));
+    b = max(b, (uint32_t)xor_lane<32>((int)b));
+  }
+  return __uint_as_float(b);
+}
+
+// The lane's values, rotated with HAD > 0, and the bits of their largest magnitude.
+template <int DT, int HAD>
+__device__ __forceinline__ uint32_t values(const Raw<DT>& w, float (&f)[8], int lane, unsigned* dbg) {
+  unpack8<DT>(w, f);
+  flag_nonfinite(f, dbg);
+  if constexpr (HAD > 0) {
+    hadamard8<HAD>(f, lane);
+    return __float_as_uint(amax8(f));
+  } else {
+    return amax_bits<DT>(w);
+  }
+}
+
+// A workgroup takes 4 U rows x 4 blocks: lane group l / 16 of a wave one block of
+// the row, so a wave's load is one contiguous kilobyte of bf16, U rows in
 // flight.  The scales of a K-block lie together for all rows (the matrix product
 // reads one per lane), so they leave through LDS as 128-byte runs.
-template <int DT, int HAD>
+template <int DT, int HAD, int U>
 __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(Fp8Params p) {
-  constexpr int U = kRows / 4;
+  constexpr int kRows = 4 * U;
   __shared__ float sc[4][kRows];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t bid = block_index();
@@ -126,10 +154,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(Fp8Params p) {
     const int r = u * 4 + wave;
     if (r >= live) continue;
     float f[8];
-    unpack8<DT>(raw[u], f);
-    flag_nonfinite(f, p.dbg);
-    if constexpr (HAD > 0) hadamard8<HAD>(f, lane);
-    const float s = scale_of(group_max<16>(amax8(f)));
+    const float s = scale_of(lanes_max<16>(values<DT, HAD>(raw[u], f, lane, p.dbg)));
     const bool fast = s >= 0x1p-100f;
     if ((lane & 15) == 0) sc[lane >> 4][r] = s;
     if (c < p.cols)
@@ -156,16 +181,13 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_tile_kernel(Fp8Params p
   Raw<DT> raw[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) raw[u] = load8<DT>(p.x, min(r0 + 16 * u, p.rows - 1) * p.ldx, c, p.cols);
-  float m = 0.f;
+  uint32_t bits = 0;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {   // rows past the end repeat the last one
     float f[8];
-    unpack8<DT>(raw[u], f);
-    flag_nonfinite(f, p.dbg);
-    if constexpr (HAD > 0) hadamard8<HAD>(f, lane);
-    m = fmaxf(m, amax8(f));
+    bits = max(bits, values<DT, HAD>(raw[u], f, lane, p.dbg));
   }
-  m = group_max<64>(m);
+  const float m = lanes_max<64>(bits);
   if (lane == 0) red[wave] = m;
   __syncthreads();
   const float s = scale_of(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
@@ -190,7 +212,12 @@ hipError_t go(Fp8Params p, bool tile, hipStream_t s) {
     quantize_fp8_tile_kernel<DT, HAD><<<grid_of((p.rows + 127) / 128 * p.col_groups), kThreads, 0, s>>>(p);
   } else {
     p.col_groups = (p.cols + 511) / 512;
-    quantize_fp8_kernel<DT, HAD><<<grid_of((p.rows + kRows - 1) / kRows * p.col_groups), kThreads, 0, s>>>(p);
+    // one row to a wave while that leaves compute units idle (37 x 1184 11.2 us with
+    // eight)
+    if ((p.rows + 3) / 4 * p.col_groups <= 2048)
+      quantize_fp8_kernel<DT, HAD, 1><<<grid_of((p.rows + 3) / 4 * p.col_groups), kThreads, 0, s>>>(p);
+    else
+      quantize_fp8_kernel<DT, HAD, 2><<<grid_of((p.rows + 7) / 8 * p.col_groups), kThreads, 0, s>>>(p);
   }
   return hipGetLastError();
 }
