@@ -14,3 +14,10 @@ from ._lib import (  # noqa: F401
     pack_l1t, qk_norm_rope, quantize, quantize_mse,
     select_format, storage, workspace_size,
 )
+
+
+def __getattr__(name):   # torch is imported with the differentiable functions only
+    if name == "autograd":
+        import importlib
+        return importlib.import_module(".autograd", __name__)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
