@@ -22,7 +22,7 @@
 //
 // E4M3 sums.  Within one MFMA the hardware adds products to about 2**-15 of the
 // largest (measured: at most 2**-11.3 of it over 64 products, without bias, 1.3e-5
-// of the sum's rms on normal data; profiles/mfma_probe.md).  Each block of 128 is
+// of the sum's rms on normal data).  Each block of 128 is
 // therefore summed from a zero accumulator and enters the fp32 sum scaled,
 // acc += (sa sw) * sum, so the error stays relative to the block's own products;
 // that takes the vector units half as long as the MFMA the matrix cores, and runs
@@ -57,7 +57,8 @@ struct BlockP {
   const float* ws2; int64_t ldws2;
   int M, N, K;          // rows of a, output columns, K (COL: a whole number of K-tiles)
   int k_split, k_rows;  // COL W: K-rows of each of w and w2, and how many of them exist
-  int tiles_m, tiles_n;
+  // this launch's part of the outputs, from row m_base and column n_base on
+  int m_base, n_base, tiles_m, tiles_n;
   const int32_t* col_map;
   const uint16_t* bias;
   uint16_t* out; int64_t ld_out; int n_out;
@@ -68,7 +69,7 @@ struct BlockP {
   uint16_t* out2; int m_split, m_rows;
   const int32_t* goff; int groups;
   // COL W: K split over this many workgroups of k_per K-tiles each; with part the sums
-  // of split s go there as fp32 [splits][M][N]
+  // of split s go there as fp32 [splits][M - m_base][N - n_base]
   int splits, k_per;
   float* part;
 };
@@ -87,6 +88,41 @@ inline double tile_time(const TileCost& c, double tiles, double kt) {
   if (r <= 1) return lat + more * r;
   if (c.whole) return n * full + (r > n ? lat + more * (r - n) : 0.) + 2.5;
   return std::max(r, std::ceil(r) - 0.4) * full + 2.5;
+}
+
+// Tile shapes to choose from, and a product as one launch or two: whole rounds of the
+// largest tiles on its first columns (or rows), the rest, which would fill another
+// round in part, in the shape that is best for it.  The order of every sum is that of
+// K whatever the shape, so nothing but the time depends on this.
+struct TileShape { TileCost cost; int rows, cols; };
+struct TileChoice { double time; int shape, splits; };
+struct TilePart { int m0, n0, m1, n1; int shape, splits; };
+struct TilePlan { TilePart part[2]; int parts; };
+
+// best(M, N): the choice for a product of this size in one launch.
+template <class Best>
+TilePlan tile_plan(int M, int N, const TileShape& big, double kt, Best best) {
+  const TileChoice one = best(M, N);
+  TilePlan plan{{{0, 0, M, N, one.shape, one.splits}, {}}, 1};
+  // Only for a clear gain, a second launch's some 6 us counted: the estimate takes a
+  // round filled in part for slower than it is (fewer units at work run at a higher
+  // clock).  In one and in two launches: dW 11264 x 8192 x 2048 with its first pass 475 /
+  // 430 us, 8832 x 2304 x 4104 210 / 196, dx 4400 x 10112 x 4104 459 / 395, FP8 4096 x 4096
+  // x 6000 120 / 111; where less is estimated nothing was won (gated FP8 4096 x 4096 x
+  // 11008 385 / 385).
+  double least = 0.95 * one.time - 6;
+  const int64_t tm = (M + big.rows - 1) / big.rows, tn = (N + big.cols - 1) / big.cols, rounds = tm * tn / big.cost.slots;
+  for (int rows = 0; rows < 2; ++rows) {
+    const int64_t across = rows ? tn : tm, n = rounds * big.cost.slots / across;
+    if (n == 0 || n >= (rows ? tm : tn)) continue;
+    const int m1 = rows ? (int)n * big.rows : M, n1 = rows ? N : (int)n * big.cols, m0 = rows ? m1 : 0, n0 = rows ? 0 : n1;
+    const TileChoice rest = best(M - m0, N - n0);
+    const double t = tile_time(big.cost, (double)(n * across), kt) + rest.time;
+    if (t >= least) continue;
+    least = t;
+    plan = {{{0, 0, m1, n1, 0, 1}, {m0, n0, M, N, rest.shape, rest.splits}}, 2};
+  }
+  return plan;
 }
 
 // Products of few rows (block_few.hip).
@@ -263,11 +299,11 @@ void block_gemm_kernel(BlockP p, int gm) {
   } else {
     if (bid >= p.tiles_m * p.tiles_n) return;
     tile_coords(bid, p.tiles_m, p.tiles_n, gm, tm, tn);
-    m0 = tm * TBM;
+    m0 = p.m_base + tm * TBM;
   }
   // uniform, but from divisions, which the vector units do
   m0 = __builtin_amdgcn_readfirstlane(m0);
-  const int n0 = __builtin_amdgcn_readfirstlane(tn * OUT_N);
+  const int n0 = __builtin_amdgcn_readfirstlane(p.n_base + tn * OUT_N);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   constexpr int R = G::R;
@@ -613,7 +649,8 @@ void block_gemm_kernel(BlockP p, int gm) {
   constexpr int OJ = EP == EP_GATED ? TJ / 2 : TJ;
   if constexpr (WL == LAY_COL) {
     if (p.part) {   // N is a multiple of 8: whole quads
-      float* const sums = p.part + (int64_t)split * p.M * p.N;
+      const int64_t rows = p.M - p.m_base, cols = p.N - p.n_base;
+      float* const sums = p.part + (split * rows - p.m_base) * cols - p.n_base;
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         const int m = m0 + (wm * TI + i) * R + rl;
@@ -623,7 +660,7 @@ void block_gemm_kernel(BlockP p, int gm) {
           for (int g = 0; g < 4; ++g) {
             const int c = n0 + wn * (OUT_N / WN) + j * R + 8 * g + 4 * part;
             if (m < p.M && c < p.N)
-              *reinterpret_cast<v4f*>(sums + (int64_t)m * p.N + c) =
+              *reinterpret_cast<v4f*>(sums + m * cols + c) =
                   v4f{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
           }
       }
@@ -631,10 +668,11 @@ void block_gemm_kernel(BlockP p, int gm) {
     }
   }
   if constexpr (EP == EP_GATED && EL == EL_BF16) {
-    // Pre-activations of whole, aligned quads: MFMA tiles of 32 x 32 pass through a
-    // part of a slot that is the wave's own and leave as 128-byte runs (a lane's
-    // quads stored from its registers are 32 bytes of a row: 23% more bytes written).
-    if (p.gate && p.saved_vec) {
+    // Pre-activations: MFMA tiles of 32 x 32 pass through a part of a slot that is the
+    // wave's own and leave as 128-byte runs, a quad to a lane where rows are whole,
+    // aligned quads, else a number (a lane's quads stored from its registers are 32
+    // bytes of a row: 23% more bytes written).
+    if (p.gate) {
       constexpr int PER_SLOT = G::SLOT / (32 * 144);   // rows of 128 bytes, 16 apart
       static_assert(PER_SLOT * (S - 1) >= NW, "a part for every wave, beside the slots of the output");
       const int at = wave / PER_SLOT;
@@ -645,6 +683,7 @@ void block_gemm_kernel(BlockP p, int gm) {
         for (int i = 0; i < TI; ++i)
 #pragma unroll
           for (int j = 0; j < OJ; ++j) {
+            const int mt = m0 + (wm * TI + i) * R, ct = n0 + wn * (OUT_N / WN) + j * R;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               v4f q;
@@ -652,11 +691,20 @@ void block_gemm_kernel(BlockP p, int gm) {
               for (int e = 0; e < 4; ++e) q[e] = side ? acc[i][j + OJ][4 * g + e] : acc[i][j][4 * g + e];
               *reinterpret_cast<v4f*>(own + rl * 144 + (8 * g + 4 * part) * 4) = q;
             }
+            // rows of the tile from the lane's first on, its columns among those that exist
+            const bool vec = p.saved_vec;
+            const int r0 = vec ? lane >> 3 : lane >> 5, c = vec ? (lane & 7) * 4 : lane & 31;
+            const int rows = ct + c < p.N ? p.M - mt - r0 : 0;
+            float* o = to + (int64_t)(mt + r0) * p.ld_saved + (ct + c);
+            const uint8_t* from = own + r0 * 144 + c * 4;
+            if (vec) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const int r = 8 * t + (lane >> 3), m = m0 + (wm * TI + i) * R + r, c = n0 + wn * (OUT_N / WN) + j * R + (lane & 7) * 4;
-              const v4f q = *reinterpret_cast<const v4f*>(own + r * 144 + (lane & 7) * 16);
-              if (m < p.M && c < p.N) __builtin_nontemporal_store(q, reinterpret_cast<v4f*>(to + (int64_t)m * p.ld_saved + c));
+              for (int t = 0; t < 4; ++t, o += 8 * p.ld_saved)
+                if (8 * t < rows) __builtin_nontemporal_store(*reinterpret_cast<const v4f*>(from + t * 8 * 144), reinterpret_cast<v4f*>(o));
+            } else {
+#pragma unroll 8
+              for (int t = 0; t < 16; ++t, o += 2 * p.ld_saved)
+                if (2 * t < rows) *o = *reinterpret_cast<const float*>(from + t * 2 * 144);
             }
           }
       }
@@ -668,7 +716,6 @@ void block_gemm_kernel(BlockP p, int gm) {
   for (int i = 0; i < TI; ++i) {
     uint8_t* const slot = wm ? slots[(TI + i) * R / G::ROWS] : slots[i * R / G::ROWS];
     uint8_t* const row = slot + (((wm * TI + i) * R) % G::ROWS + rl) * G::ROW_BYTES;
-    const int m = m0 + (wm * TI + i) * R + rl;
 #pragma unroll
     for (int j = 0; j < OJ; ++j)
 #pragma unroll
@@ -681,16 +728,6 @@ void block_gemm_kernel(BlockP p, int gm) {
           float u[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) u[e] = acc[i][j + OJ][4 * g + e];
-          if (EL == EL_BF16 && p.gate && !p.saved_vec && m < p.M) {
-            float* const gp = p.gate + (int64_t)m * p.ld_saved + n0 + c;
-            float* const up = p.up + (int64_t)m * p.ld_saved + n0 + c;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n0 + c + e < p.N) {
-                gp[e] = v[e];
-                up[e] = u[e];
-              }
-          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = activation<false>(p.act, v[e]) * u[e];
         }
@@ -745,10 +782,12 @@ void block_gemm_kernel(BlockP p, int gm) {
 }
 
 template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN, int DEEP = 0>
-hipError_t launch_block_gemm(BlockP p, hipStream_t s) {
+hipError_t launch_block_gemm(BlockP p, const TilePart& part, hipStream_t s) {
   using G = BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP>;
-  p.tiles_m = GRP ? (int)group_tiles_bound(p.M, p.groups, G::TBM) : (p.M + G::TBM - 1) / G::TBM;
-  p.tiles_n = (p.N + G::OUT_N - 1) / G::OUT_N;
+  p.m_base = part.m0;
+  p.n_base = part.n0;
+  p.tiles_m = GRP ? (int)group_tiles_bound(p.M, p.groups, G::TBM) : (part.m1 - part.m0 + G::TBM - 1) / G::TBM;
+  p.tiles_n = (part.n1 - part.n0 + G::OUT_N - 1) / G::OUT_N;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, blocks = tiles * std::max(p.splits, 1);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   int gm = 1;

@@ -114,69 +114,69 @@ hipError_t zero_rows(uint16_t* p, int64_t ld, int64_t rows, int64_t cols, hipStr
 // Times of the tile kernels, fits as in gemm_fp8.hip: 256 x 256, 128 x 128, and with whole
 // K-tiles in flight 64 x 128 (M x K x N 4096 x 4096 x 4096 gated 218 / 269 / 451 us, 512 x 4096 x
 // 4096 81 / 55 / 62, 256 x 4096 x 4096 82 / 53 / 34).
-constexpr TileCost kBig = {7.3, 1.1, 8.0, 1.6, 256, true}, kMid = {0.5, 0.84, 4.0, 1.02, 512, false},
-                   kSmall = {1.0, 0.5, 2.0, 0.48, 256, false};
+constexpr TileShape kForward[] = {{{7.3, 1.1, 8.0, 1.6, 256, true}, 256, 128},
+                                  {{0.5, 0.84, 4.0, 1.02, 512, false}, 128, 64},
+                                  {{1.0, 0.5, 2.0, 0.48, 256, false}, 64, 64}};
 
-double tiles_of(const BlockP& p, int tm, int tn) { return (double)((p.M + tm - 1) / tm) * ((p.N + tn - 1) / tn); }
+double tiles_of(const TileShape& t, int M, int N) { return (double)((M + t.rows - 1) / t.rows) * ((N + t.cols - 1) / t.cols); }
 
+// In one launch (8300 x 2056 x 2200 in one and in two, as the gradients, 181 / 182 us).
 hipError_t gated_tiles(const BlockP& p, hipStream_t s) {
   const double kt = (p.K + 63) / 64;
-  const double t1 = tile_time(kSmall, tiles_of(p, 64, 64), kt), t2 = tile_time(kMid, tiles_of(p, 128, 64), kt),
-               t4 = tile_time(kBig, tiles_of(p, 256, 128), kt);
-  if (t4 < t2 && t4 < t1) return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 2, 2, 4>(p, s);
-  if (t2 < t1) return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 2, 2, 2, 2>(p, s);
-  return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 1, 2, 2, 2, 4>(p, s);
+  double time[3];
+  for (int i = 0; i < 3; ++i) time[i] = tile_time(kForward[i].cost, tiles_of(kForward[i], p.M, p.N), kt);
+  const TilePart all{0, 0, p.M, p.N, 0, 1};
+  if (time[0] < time[1] && time[0] < time[2])
+    return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 4, 2, 2, 4>(p, all, s);
+  if (time[1] < time[2]) return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 2, 2, 2, 2>(p, all, s);
+  return launch_block_gemm<EL_BF16, LAY_ROW, LAY_ROW, EP_GATED, false, 1, 2, 2, 2, 4>(p, all, s);
 }
 
-// A gradient's product: the tile shape and over how many workgroups its K-tiles are
+// A gradient's product: its tile shapes and over how many workgroups its K-tiles are
 // split (fp32 sums in the workspace, added in order by a second kernel): dx has few
-// tiles where there are few rows, and 2 N of K.
-struct GradPlan { int shape, splits; };
-
-GradPlan grad_plan(const BlockP& p, bool dw, int64_t room) {
-  const double kt = p.K / 64, mn = (double)p.M * p.N;
-  GradPlan best{4, 1};
-  double least = 1e30;
-  for (int shape : {4, 2, 1}) {
-    const int tm = shape == 4 ? 256 : shape == 2 || dw ? 128 : 64, tn = shape == 4 ? 256 : 128;
+// tiles where there are few rows, and 2 N of K.  Only a last part is ever split.
+TilePlan grad_plan(const BlockP& p, bool dw, int64_t room) {
+  const TileShape shapes[] = {{kForward[0].cost, 256, 256}, {kForward[1].cost, 128, 128}, {kForward[2].cost, 64, 128}};
+  const double kt = p.K / 64;
+  return tile_plan(p.M, p.N, shapes[0], kt, [&](int M, int N) {
+    TileChoice best{1e30, 0, 1};
+    const double mn = (double)M * N;
     // the weights' gradients take no 64-row tiles (four swizzled segments to a K-row)
-    if (shape == 1 && dw) continue;
-    const TileCost& c = shape == 4 ? kBig : shape == 2 ? kMid : kSmall;
-    for (int s = 1; s <= 16 && s * 4 <= std::max(kt, 4.); s *= 2) {
-      if (s > 1 && (double)s * mn * 4 > (double)room) break;
-      // the sums: written, read and rounded at some 4 TB/s, and a launch
-      const double t = tile_time(c, tiles_of(p, tm, tn) * s, std::ceil(kt / s)) + (s > 1 ? 3.0 + s * mn * 8 / 4e6 : 0.);
-      if (t < least) {
-        least = t;
-        best = {shape, s};
+    for (int i = 0; i < (dw ? 2 : 3); ++i)
+      for (int s = 1; s <= 16 && s * 4 <= std::max(kt, 4.); s *= 2) {
+        if (s > 1 && (double)s * mn * 4 > (double)room) break;
+        // the sums: written, read and rounded at some 4 TB/s, and a launch
+        const double t = tile_time(shapes[i].cost, tiles_of(shapes[i], M, N) * s, std::ceil(kt / s)) +
+                         (s > 1 ? 3.0 + s * mn * 8 / 4e6 : 0.);
+        if (t < best.time) best = {t, i, s};
       }
-    }
-  }
-  return best;
+    return best;
+  });
 }
 
 struct SumP {
   const float* part;
-  int M, N, splits;
+  int m0, n0, M, N, splits;   // rows [m0, M), columns [n0, N)
   uint16_t* out; uint16_t* out2; int64_t ld_out;
   int m_split, m_rows;
 };
 
 // Rows of out (and from m_split on of out2) from the splits' sums, four columns to a thread.
 __global__ __launch_bounds__(kGradThreads) void split_sum_kernel(SumP p) {
-  const int64_t t = (int64_t)block_index() * kGradThreads + threadIdx.x, quads = p.N / 4;
-  if (t >= p.M * quads) return;
-  int64_t row = t / quads;
-  const int c = (int)(t % quads) * 4;
+  const int64_t t = (int64_t)block_index() * kGradThreads + threadIdx.x, cols = p.N - p.n0, rows = p.M - p.m0, quads = cols / 4;
+  if (t >= rows * quads) return;
+  const int64_t in = t / quads;
+  const int c = p.n0 + (int)(t % quads) * 4;
+  const float* const from = p.part + in * cols + (c - p.n0);
+  int64_t row = p.m0 + in;
   uint16_t* o = p.out;
-  const float* const from = p.part + row * p.N + c;
   if (row >= p.m_split) {
     row -= p.m_split;
     o = p.out2;
   }
   if (row >= p.m_rows) return;
   v4f s = *reinterpret_cast<const v4f*>(from);
-  for (int k = 1; k < p.splits; ++k) s += *reinterpret_cast<const v4f*>(from + (int64_t)k * p.M * p.N);
+  for (int k = 1; k < p.splits; ++k) s += *reinterpret_cast<const v4f*>(from + k * rows * cols);
   o += row * p.ld_out + c;
   const uint32_t lo = pack_bf16_rne(s[0], s[1]), hi = pack_bf16_rne(s[2], s[3]);
   if ((reinterpret_cast<uintptr_t>(o) & 7) == 0) {
@@ -192,19 +192,26 @@ __global__ __launch_bounds__(kGradThreads) void split_sum_kernel(SumP p) {
 template <int AL, int EP>
 hipError_t grad_product(BlockP p, float* part, int64_t room, hipStream_t s) {
   constexpr bool dw = EP == EP_SPLIT;
-  const GradPlan plan = grad_plan(p, dw, room);
+  const TilePlan plan = grad_plan(p, dw, room);
   const int kt = p.K / 64;
-  p.k_per = (kt + plan.splits - 1) / plan.splits;
-  p.splits = (kt + p.k_per - 1) / p.k_per;
-  p.part = p.splits > 1 ? part : nullptr;
-  hipError_t e;
-  if (plan.shape == 4) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 4, 2, 2, 4>(p, s);
-  else if (plan.shape == 2 || dw) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 2, 2, 2, 2>(p, s);
-  else if constexpr (!dw) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 1, 2, 2, 2, 4>(p, s);
-  if (e != hipSuccess || !p.part) return e;
-  SumP q{p.part, p.M, p.N, p.splits, p.out, p.out2, p.ld_out, dw ? p.m_split : p.M, dw ? p.m_rows : p.M};
-  split_sum_kernel<<<grid_of(((int64_t)p.M * (p.N / 4) + kGradThreads - 1) / kGradThreads), kGradThreads, 0, s>>>(q);
-  return hipGetLastError();
+  for (int i = 0; i < plan.parts; ++i) {
+    const TilePart& t = plan.part[i];
+    p.k_per = (kt + t.splits - 1) / t.splits;
+    p.splits = (kt + p.k_per - 1) / p.k_per;
+    p.part = p.splits > 1 ? part : nullptr;
+    hipError_t e;
+    if (t.shape == 0) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 4, 2, 2, 4>(p, t, s);
+    else if (t.shape == 1 || dw) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 2, 2, 2, 2>(p, t, s);
+    else if constexpr (!dw) e = launch_block_gemm<EL_BF16, AL, LAY_COL, EP, false, 1, 2, 2, 2, 4>(p, t, s);
+    if (e != hipSuccess) return e;
+    if (!p.part) continue;
+    const SumP q{p.part, t.m0, t.n0, p.M, p.N, p.splits, p.out, p.out2, p.ld_out, dw ? p.m_split : p.M, dw ? p.m_rows : p.M};
+    const int64_t pieces = (int64_t)(p.M - t.m0) * ((p.N - t.n0) / 4);
+    split_sum_kernel<<<grid_of((pieces + kGradThreads - 1) / kGradThreads), kGradThreads, 0, s>>>(q);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
@@ -232,8 +239,9 @@ BlockP dw_shape(int64_t M, int64_t N, int64_t K) {
 }
 
 int64_t split_bytes(const BlockP& p, bool dw) {
-  const int s = grad_plan(p, dw, INT64_MAX).splits;
-  return s > 1 ? (int64_t)s * p.M * p.N * 4 : 0;
+  const TilePlan plan = grad_plan(p, dw, INT64_MAX);
+  const TilePart& t = plan.part[plan.parts - 1];
+  return t.splits > 1 ? (int64_t)t.splits * (p.M - t.m0) * (p.N - t.n0) * 4 : 0;
 }
 
 }  // namespace

@@ -27,14 +27,36 @@ BlockP params(const GemmArgs& a) {
 // columns and K = 512 .. 8192, operands from HBM, within some 20%.
 template <int EP, bool GRP>
 hipError_t tiles(const BlockP& p, const GemmArgs& a, hipStream_t s) {
-  const int half = EP == EP_GATED ? 2 : 1;
+  constexpr int half = EP == EP_GATED ? 2 : 1;
+  constexpr TileShape shapes[] = {{{6.5, 1.4, 6.0, 1.95, 256, true}, 256, 256 / half},
+                                  {{3.4, 0.7, 5.5, 1.19, 512, false}, 128, 128 / half},
+                                  {{2.2, 0.5, 1.5, 0.55, 512, false}, 64, 64 / half}};
   const double kt = (p.K + 127) / 128;
-  const double t1 = tile_time({2.2, 0.5, 1.5, 0.55, 512, false}, gemm_tiles(a, 64, 64 / half), kt);
-  const double t2 = tile_time({3.4, 0.7, 5.5, 1.19, 512, false}, gemm_tiles(a, 128, 128 / half), kt);
-  const double t4 = tile_time({6.5, 1.4, 6.0, 1.95, 256, true}, gemm_tiles(a, 256, 256 / half), kt);
-  if (t4 < t2 && t4 < t1) return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 8, 4, 2, 4>(p, s);
-  if (t2 < t1) return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 4, 4, 2, 2>(p, s);
-  return launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 2, 2, 2, 2, 4>(p, s);
+  const auto best = [&](int M, int N) {
+    TileChoice c{1e30, 0, 1};
+    for (int i = 0; i < 3; ++i) {
+      const TileShape& t = shapes[i];
+      const double tn = (N + t.cols - 1) / t.cols;
+      const double n = GRP ? (double)group_tiles_bound(M, a.groups, t.rows) * tn : (double)((M + t.rows - 1) / t.rows) * tn;
+      const double time = tile_time(t.cost, n, kt);
+      if (time < c.time) c = {time, i, 1};
+    }
+    return c;
+  };
+  // Two launches for a K of 4096 and more: with short sums the outputs' way out weighs
+  // more than the estimate says (4400 x 1024 x 4400 in one and in two 38 / 42 us); not
+  // for groups, whose rows are known to the GPU only.
+  TilePlan plan{{{0, 0, p.M, p.N, best(p.M, p.N).shape, 1}, {}}, 1};
+  if (!GRP && kt >= 32) plan = tile_plan(p.M, p.N, shapes[0], kt, best);
+  for (int i = 0; i < plan.parts; ++i) {
+    const TilePart& t = plan.part[i];
+    hipError_t e;
+    if (t.shape == 0) e = launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 8, 4, 2, 4>(p, t, s);
+    else if (t.shape == 1) e = launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 4, 4, 2, 2>(p, t, s);
+    else e = launch_block_gemm<EL_FP8, LAY_ROW, LAY_ROW, EP, GRP, 2, 2, 2, 2, 4>(p, t, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
