@@ -12,6 +12,10 @@
 // scales, or K = 64 on two v_mfma_f32_16x16x32_bf16 (any order of K is right that
 // both operands share).  Rows past the end of an operand re-read its last row and
 // are never stored; pieces past the end of K count as zeros.
+//
+// One token, weights from HBM: FP8 4096 -> 8192 10.2 us, 3.3 TB/s, and 4096 -> 11008 gated
+// 20.2, 4.5 TB/s, of 6.5 and 17.5 at a large copy's rate (the launch and one trip to
+// memory are some 3 us of each).
 #include "block_gemm.h"
 
 namespace mxq {

@@ -1,6 +1,8 @@
 // Products of E4M3 codes with fp32 block scales (block_gemm.h): the FP8 layer
 //   y[m][n] = RN_bf16(sum over K-blocks b of sa[b][m] sw[n / 128][b] sum_{k in b} a[m][k] w[n][k] + bias[n]),
-// the same grouped by expert, and the gated pair of projections.
+// the same grouped by expert, and the gated pair of projections.  8192^3 takes 479 us
+// (2.30 PFLOP/s), 4096 x 4096 x 11008 gated 375 (1.97: 5.4 rounds of tiles take six), 777 x
+// 1184 x 1001 7.8.
 #include "block_gemm.h"
 
 namespace mxq {
