@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t values(const Raw<DT>& w, float (&f)[8], int 
 // A workgroup takes 4 U rows x 4 blocks: lane group l / 16 of a wave one block of
 // the row, so a wave's load is one contiguous kilobyte of bf16, U rows in
 // flight.  The scales of a K-block lie together for all rows (the matrix product
-// reads one per lane), so they leave through LDS as 128-byte runs.
+// reads one per lane), so they leave through LDS as runs of 4 U.
 template <int DT, int HAD, int U>
 __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(Fp8Params p) {
   constexpr int kRows = 4 * U;

@@ -288,7 +288,8 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  * itself, scaled by its two scales and added in fp32.  Its bound is
  * |y - y_exact| <= 2**-10 P + 1e-5 S + 2**-8 |y_exact| + 2**-133 with P the sum over
  * K-blocks of the largest |a w| of each (on normal data the sums are 2e-5 of
- * their rms off, a hundredth of the output rounding).
+ * their rms off, a hundredth of the output rounding); past K = 16384, where the
+ * K / 128 additions alone may round by more, 2**-30 K S in place of 1e-5 S.
  * Error bound: |y - y_exact| <= 1e-5 (1 + 2**-8) S + 2**-8 |y_exact| + 2**-133
  * with S = alpha sum_k |a w| + sum_j |u_j L2_jn| (the last two terms are the
  * bf16 output rounding, 2**-133 covering subnormal outputs).
