@@ -464,8 +464,9 @@ void block_gemm_kernel(BlockP p, int gm) {
     const uint8_t* const b = reinterpret_cast<const uint8_t*>(as + (int64_t)kt * p.ldas);
 #pragma unroll
     for (int r = 0; r < RAW; ++r) {
-      const uint32_t off = 4 * (wm * TI * 16 + 64 * r + (TI < 4 ? lane & 31 : lane));
-      raw_next[r] = *reinterpret_cast<const float*>(b + min(off, 4u * (uint32_t)(p.M - 1 - m0)));
+      // clamped before the product with 4, which for a last row past 2**30 is no 32-bit number
+      const uint32_t row = wm * TI * 16 + 64 * r + (TI < 4 ? lane & 31 : lane);
+      raw_next[r] = *reinterpret_cast<const float*>(b + 4 * min(row, (uint32_t)(p.M - 1 - m0)));
     }
   };
   auto block_scales = [&](int kt) __attribute__((always_inline)) {   // K-tiles kt and on, into sw_next

@@ -1,0 +1,43 @@
+"""FP8 operands near the largest numbers of rows and columns: indexes that pass 2**30
+and 2**31 in rows, columns and bytes."""
+import pytest
+import torch
+
+import fp8_quantized_linear_mxq_amd as mxq
+from tests import gpu_util as gu
+from tests.test_gpu_many_workgroups import memory, room, same_blocks   # noqa: F401 (memory: a fixture of every test)
+
+pytestmark = pytest.mark.gpu
+
+BLOCK = 1 << 20
+
+
+def rows_of(m, k):
+    """(operand of m rows that repeat the same 2**20, that block's float64 values)"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m % 1000)
+    v = torch.randint(-3, 4, (BLOCK, k), generator=g, device="cuda").float()
+    s = torch.exp2(torch.randint(-3, 4, (BLOCK,), generator=g, device="cuda").float())
+    reps = -(-m // BLOCK)
+    codes = v.to(torch.float8_e4m3fn).view(torch.uint8).repeat(reps, 1)[:m]
+    return mxq.fp8_operand(codes, s.repeat(reps)[None, :m]), v.double() * s.double()[:, None]
+
+
+def weights(n, k):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    v = torch.randint(-3, 4, (n, k), generator=g, device="cuda").float()
+    return mxq.fp8_operand(v.to(torch.float8_e4m3fn), torch.ones(((n + 127) // 128, 1), device="cuda"), tile=True), v.double()
+
+
+@pytest.mark.parametrize("m,n", [((1 << 30) + 30, 8)])
+def test_products_of_many_rows(m, n):
+    """Every row has the scale of its own: the first tile is 2**30 rows and more from the last."""
+    room(110)
+    gu.say(f"fp8 {m} x {n} x 32")
+    (a, av), (w, wv) = rows_of(m, 32), weights(n, 32)
+    y = mxq.gemm(a, w)
+    want = (av @ wv.t()).float().bfloat16()
+    same_blocks(y, want)
+    rest = m % BLOCK
+    assert torch.equal(y[m - rest:], want[:rest])
