@@ -29,8 +29,10 @@ __device__ __forceinline__ float activation(int act, float g, float* d = nullptr
   }
   // g (1 + tanh z) / 2 = g s, s = logistic(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3);
   // f' = s + g 2 z' s (1 - s).  Past |g| = 30 s (1 - s) is 0 in fp32, and g is held
-  // there so that no power of it overflows.
-  const float c = fminf(fmaxf(g, -30.f), 30.f);
+  // there so that no power of it overflows.  A NaN is held too by the minimum and maximum
+  // (one instruction): f is NaN by its factor g, but f' has none, so there it passes.
+  float c = fminf(fmaxf(g, -30.f), 30.f);
+  if constexpr (DERIV) c = g == g ? c : g;
   const float s = logistic(1.59576912f * c * fmaf(0.044715f * c, c, 1.f));
   if constexpr (DERIV) *d = fmaf(1.59576912f * c * fmaf(0.134145f * c, c, 1.f), s * (1.f - s), s);
   return g * s;
