@@ -381,7 +381,7 @@ void block_gemm_kernel(BlockP p, int gm) {
     if constexpr (EP == EP_LINEAR) asm volatile("" : "+s"(ldw2), "+s"(k_split), "+s"(wbase2));
   }
   // loads [t0, t1) of a K-tile's A or W; chunks past the end of K re-read the row's
-  // first chunk of the K-tile, K-rows past it the last K-row
+  // first chunk of the K-tile, K-rows past it the last K-row (and are cut below)
   auto issue_a = [&](int kt, uint8_t* slot, int t0, int t1) __attribute__((always_inline)) {
     kt = kt < KT ? kt : KT - 1;
     const int k = kt + k_first;
@@ -424,6 +424,30 @@ void block_gemm_kernel(BlockP p, int gm) {
         if (t >= t0 && t < t1)
           __builtin_amdgcn_global_load_lds(b + (uint64_t)((uint32_t)min(kw + (512 / TBN) * NW * t, last) * ld + cw),
                                            (lds_void_t*)(slot + (t * NW + wave) * 1024), 16, 0, 0);
+    }
+  };
+
+  // COL W: the K-tiles that end in a half's last K-row, of this workgroup's the next one.  Its
+  // K-rows past the end, by each wave those that it has loaded, become zeros before the barrier
+  // that opens it: A's are zeros, but the row in their place may hold an infinity.  (As
+  // loads from a row of zeros, which take addresses of 64 bits to a lane, 3% slower.)
+  int cut_kt = -1, cut_later = -1;
+  if constexpr (WL == LAY_COL) {
+    if (k_rows % 64) {
+      cut_kt = k_rows / 64 - k_first;
+      if constexpr (EP == EP_LINEAR) cut_later = cut_kt + k_split / 64;
+      if (cut_kt < 0) cut_kt = cut_later;
+    }
+    asm volatile("" : "+s"(cut_kt), "+s"(cut_later));
+  }
+  auto cut_rows = [&](int kt, uint8_t* slot) __attribute__((always_inline)) {
+    if constexpr (WL == LAY_COL) {
+      if (__builtin_expect(kt != cut_kt, 1)) return;
+#pragma unroll
+      for (int t = 0; t < LW; ++t)
+        if (kw + (512 / TBN) * NW * t >= k_rows % 64) *reinterpret_cast<v4i*>(slot + (t * NW + wave) * 1024 + lane * 16) = v4i{};
+      wait_lgkmcnt0();
+      cut_kt = cut_later;
     }
   };
 
@@ -566,6 +590,7 @@ void block_gemm_kernel(BlockP p, int gm) {
         wait_lgkmcnt0();
         wait_vmcnt<DEEP ? (DEEP - 2) * (LA + LW) : LA>();
         asm volatile("" ::: "memory");
+        cut_rows(kt + 1, W1);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
@@ -603,6 +628,8 @@ void block_gemm_kernel(BlockP p, int gm) {
     issue_a(2, s4, 0, G::AHEAD_A);
     wait_vmcnt<LA + G::AHEAD_W + G::AHEAD_A>();
   }
+  asm volatile("" ::: "memory");
+  cut_rows(0, DEEP ? s0 + G::SLOT_A : s1);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   if (KF > 0) {

@@ -1,15 +1,22 @@
-"""NaN in the gated products and their gradients: what the formulas give, and nothing in
-rows and columns beside them."""
+"""NaN and infinities in the gated products and their gradients: what the formulas give,
+and nothing in rows and columns beside them."""
 import pytest
 import torch
 
 import fp8_quantized_linear_mxq_amd as mxq
+from tests import gpu_util as gu
+from tests.test_gpu_fp8 import bf16
 from tests.test_gpu_gated import exact_case
 
 pytestmark = pytest.mark.gpu
 
 ACTS = ["silu", "gelu", "gelu_tanh"]
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
+
+
+def same(got, want):
+    """Equal, NaN where the other is NaN."""
+    return torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -40,3 +47,37 @@ def test_nan_input(m, act):
     others = torch.arange(m, device="cuda") != 1
     assert bool(y[1].isnan().all()) and bool(saved[:, 1].isnan().all())
     assert torch.equal(y[others], clean[others]) and bool(saved[:, others].isfinite().all())
+
+
+def with_infinite_row(a, b, col):
+    """a^T-like product a [r, t] @ b [t, c] whose last row of b is infinite in column col, the rest finite."""
+    finite = b.clone()
+    finite[-1, col] = 0
+    want = a @ finite
+    want[:, col] += a[:, -1] * b[-1, col]
+    return bf16(want)
+
+
+# a few rows, one and several tiles, K split over workgroups, the largest tiles; all with padded rows and outputs
+@pytest.mark.parametrize("m,n,k", [(5, 9, 72), (70, 90, 136), (300, 100, 520), (1111, 203, 160), (2300, 1030, 264),
+                                   (8200, 2100, 2056), (64, 128, 136)])
+def test_infinite_last_rows(m, n, k):
+    """Infinities in the last row of x and of the weights, behind which the operands end
+    inside a K-tile: the gradients are infinite (NaN where the formula has 0 x inf)."""
+    gu.say(f"gradients {m}x{n}x{k}, infinite last rows")
+    x, wg, wu, dy, gate, up = exact_case(m, n, k)
+    saved = torch.stack([gate, up]).float()
+    dg, du = dy.double() * up, dy.double() * gate
+    x[-1, 3], wg[-1, 4], wu[-1, 5] = INF, -INF, INF
+    ops = [mxq.bf16_operand(t.bfloat16()) for t in (x, wg, wu)]
+    dx, dwg, dwu = mxq.gemm_gated_backward(dy.bfloat16(), *ops, saved)
+    xd, gd, ud = x.double(), wg.double(), wu.double()
+    both = torch.cat([dg, du], 1)
+    gd0, ud0 = gd.clone(), ud.clone()
+    gd0[-1, 4] = ud0[-1, 5] = 0
+    want = both @ torch.cat([gd0, ud0])
+    want[:, 4] += dg[:, -1] * gd[-1, 4]
+    want[:, 5] += du[:, -1] * ud[-1, 5]
+    assert same(dx, bf16(want)), "dx"
+    assert same(dwg, with_infinite_row(dg.t(), xd, 3)), "dWg"
+    assert same(dwu, with_infinite_row(du.t(), xd, 3)), "dWu"
