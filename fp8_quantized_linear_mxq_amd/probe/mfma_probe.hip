@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
@@ -75,7 +76,9 @@ __global__ __launch_bounds__(512) void mfma_rate_kernel(int iters, int zero, flo
 // a_scl / b_scl: one E8M0 code per lane (scaled kinds).
 //   KIND 0: scaled E4M3 x E2M1 32x32x64    1: scaled E2M1 x E2M1 32x32x64
 //        2: scaled E4M3 x E4M3 32x32x64    3: E4M3 x E4M3 32x32x16
-//        4: bf16 x bf16 32x32x16
+//        4: bf16 x bf16 32x32x16           5: scaled E4M3 x E4M3 16x16x128
+// Kind 5: lane l carries row l % 16 and, of each row, K = 32 (l / 16) + [0, 32) in 8
+// dwords; its scales are 1; d holds 4 floats of a lane's 16.
 template <int KIND>
 __global__ __launch_bounds__(64) void mfma_sum_kernel(const int* a_ops, const int* b_ops,
                                                       const int* a_scl, const int* b_scl, float* d) {
@@ -85,6 +88,12 @@ __global__ __launch_bounds__(64) void mfma_sum_kernel(const int* a_ops, const in
   for (int i = 0; i < 8; ++i) { a[i] = a_ops[l * 8 + i]; b[i] = b_ops[l * 8 + i]; }
   const int sa = a_scl[l], sb = b_scl[l];
   v16f acc = v16f{};
+  if constexpr (KIND == 5) {
+    const v4f sum = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, v4f{}, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[l * 16 + q] = sum[q];
+    return;
+  }
   if constexpr (KIND == 0)
     acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 4, 0, sa, 0, sb);
   else if constexpr (KIND == 1)
@@ -178,7 +187,7 @@ int probe_mfma_rate(int kind, int blocks, int waves, int iters, int zero, float*
   return (int)hipGetLastError();
 }
 
-// One MFMA of `kind` (0-4, see mfma_sum_kernel).  Device pointers: a_ops,
+// One MFMA of `kind` (0-5, see mfma_sum_kernel).  Device pointers: a_ops,
 // b_ops 64 x 8 ints; a_scl, b_scl 64 ints; d 64 x 16 floats, lane l's
 // accumulator registers in order.  Returns a hipError_t.
 int probe_mfma_sum(int kind, const int* a_ops, const int* b_ops, const int* a_scl, const int* b_scl,
@@ -191,6 +200,7 @@ int probe_mfma_sum(int kind, const int* a_ops, const int* b_ops, const int* a_sc
     case 2: mfma_sum_kernel<2><<<1, 64, 0, s>>>(a_ops, b_ops, a_scl, b_scl, d); break;
     case 3: mfma_sum_kernel<3><<<1, 64, 0, s>>>(a_ops, b_ops, a_scl, b_scl, d); break;
     case 4: mfma_sum_kernel<4><<<1, 64, 0, s>>>(a_ops, b_ops, a_scl, b_scl, d); break;
+    case 5: mfma_sum_kernel<5><<<1, 64, 0, s>>>(a_ops, b_ops, a_scl, b_scl, d); break;
     default: return (int)hipErrorInvalidValue;
   }
   return (int)hipGetLastError();
