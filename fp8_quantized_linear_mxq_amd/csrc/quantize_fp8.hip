@@ -14,6 +14,9 @@
 // (both mantissas are short), so this path costs no float64.  Scales below 2**-100,
 // where the remainder could underflow, take float64 quotients.
 //
+// A block with an infinity has an infinite scale; its quotients in float64 are 0, and
+// 448 for the infinite ones (with the reciprocal they would be NaN).
+//
 // Bound by memory: 2 (bf16) or 4 (fp32) bytes read and one written per element; a
 // block is held in registers between its maximum and its codes.  A lane takes 8
 // consecutive elements, 16 lanes a row's block, and the maxima are those of the bit
@@ -39,6 +42,9 @@ struct Fp8Params {
   int64_t ld_scales;   // bytes between K-blocks (FP8) or row blocks (FP8_TILE)
   unsigned* dbg;
 };
+
+// Whether r * (1 / s) and the exact remainder decide a code.
+__device__ __forceinline__ bool fast_scale(float s) { return s >= 0x1p-100f && s <= 0x1.fffffep127f; }
 
 // 8 codes of values with scale s (inv = 1 / s, usable when `fast`).
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv, bool fast) {
@@ -80,16 +86,17 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s, float inv
 
 // RN_fp32(amax / 448) from the product with the reciprocal and its exact remainder
 // (right for every mantissa: compared over all 2**23); amax whose remainder could
-// underflow takes float64, whose quotient of two fp32 values rounds rightly.
+// underflow, or is infinite (the remainder would be NaN), takes float64, whose
+// quotient of two fp32 values rounds rightly.
 __device__ __forceinline__ float scale_of(float amax) {
-  if (!(amax >= 0x1p-90f)) return (float)((double)amax / 448.0);
+  if (!(amax >= 0x1p-90f && amax <= 0x1.fffffep127f)) return (float)((double)amax / 448.0);
   constexpr float r = 1.0f / 448.0f;
   const float q = amax * r;
   return __builtin_fmaf(__builtin_fmaf(-q, 448.0f, amax), r, q);
 }
 
 // Largest magnitude of a lane's elements as bits: an integer maximum, packed for bf16
-// (NaNs aside, magnitudes are in the order of their bits).
+// (magnitudes are in the order of their bits, a NaN above all).
 template <int DT>
 __device__ __forceinline__ uint32_t amax_bits(const Raw<DT>& w) {
   if constexpr (DT == DT_BF16) {
@@ -110,7 +117,7 @@ __device__ __forceinline__ uint32_t amax_bits(const Raw<DT>& w) {
 
 // Maximum over G consecutive lanes.
 template <int G>
-__device__ __forceinline__ float lanes_max(uint32_t b) {
+__device__ __forceinline__ uint32_t lanes_max(uint32_t b) {
   b = max(b, (uint32_t)xor_lane<1>((int)b));
   b = max(b, (uint32_t)xor_lane<2>((int)b));
   b = max(b, (uint32_t)xor_lane<4>((int)b));
@@ -119,7 +126,7 @@ __device__ __forceinline__ float lanes_max(uint32_t b) {
     b = max(b, (uint32_t)xor_lane<16>((int)b));
     b = max(b, (uint32_t)xor_lane<32>((int)b));
   }
-  return __uint_as_float(b);
+  return b;
 }
 
 // The lane's values, rotated with HAD > 0, and the bits of their largest magnitude.
@@ -129,7 +136,10 @@ __device__ __forceinline__ uint32_t values(const Raw<DT>& w, float (&f)[8], int 
   flag_nonfinite(f, dbg);
   if constexpr (HAD > 0) {
     hadamard8<HAD>(f, lane);
-    return __float_as_uint(amax8(f));
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+    return m;
   } else {
     return amax_bits<DT>(w);
   }
@@ -158,8 +168,8 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(Fp8Params p) {
     const int r = u * 4 + wave;
     if (r >= live) continue;
     float f[8];
-    const float s = scale_of(lanes_max<16>(values<DT, HAD>(raw[u], f, lane, p.dbg)));
-    const bool fast = s >= 0x1p-100f;
+    const float s = scale_of(__uint_as_float(lanes_max<16>(values<DT, HAD>(raw[u], f, lane, p.dbg))));
+    const bool fast = fast_scale(s);
     if ((lane & 15) == 0) sc[lane >> 4][r] = s;
     if (c < p.cols)
       *reinterpret_cast<uint2*>(p.codes + (row0 + r) * p.ld_codes + c) = encode8(f, s, fast ? __builtin_amdgcn_rcpf(s) : 0.f, fast);
@@ -174,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_kernel(Fp8Params p) {
 // A workgroup takes one tile of 128 x 128, 16 rows at a time.
 template <int DT, int HAD>
 __global__ __launch_bounds__(kThreads) void quantize_fp8_tile_kernel(Fp8Params p) {
-  __shared__ float red[kThreads / 64];
+  __shared__ uint32_t red[kThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t bid = block_index();
   const uint32_t tr = bid / (uint32_t)p.col_groups, tc = bid % (uint32_t)p.col_groups;
@@ -191,12 +201,12 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_tile_kernel(Fp8Params p
     float f[8];
     bits = max(bits, values<DT, HAD>(raw[u], f, lane, p.dbg));
   }
-  const float m = lanes_max<64>(bits);
+  const uint32_t m = lanes_max<64>(bits);
   if (lane == 0) red[wave] = m;
   __syncthreads();
-  const float s = scale_of(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+  const float s = scale_of(__uint_as_float(max(max(red[0], red[1]), max(red[2], red[3]))));
   if (threadIdx.x == 0) *reinterpret_cast<float*>(p.scales + (int64_t)tr * p.ld_scales + (int64_t)tc * 4) = s;
-  const bool fast = s >= 0x1p-100f;
+  const bool fast = fast_scale(s);
   const float inv = fast ? __builtin_amdgcn_rcpf(s) : 0.f;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {

@@ -52,6 +52,8 @@
  *   INT8   s = RN_fp32(row amax / 127); q = clamp(RNE(x / s), -127, 127);
  *          s = 0 gives q = 0.
  *   FP8    s = RN_fp32(block amax / 448); q = RN_E4M3(x / s); s = 0 gives q = 0.
+ *          An infinite element makes its block's s infinite and is +-448, the
+ *          block's others 0; a NaN one makes s NaN.  No code is NaN.
  *
  * Storage (all device memory, row-major, K contiguous):
  *   codes   4-bit formats: [rows][K/2] bytes, element 2i in the low nibble

@@ -1,5 +1,5 @@
-"""NaN and infinities in the gated products and their gradients: what the formulas give,
-and nothing in rows and columns beside them."""
+"""NaN and infinities in the gated products, their gradients and the FP8
+quantize: what the formulas give, and nothing in rows and columns beside them."""
 import pytest
 import torch
 
@@ -81,3 +81,49 @@ def test_infinite_last_rows(m, n, k):
     assert same(dx, bf16(want)), "dx"
     assert same(dwg, with_infinite_row(dg.t(), xd, 3)), "dWg"
     assert same(dwu, with_infinite_row(du.t(), xd, 3)), "dWu"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", [mxq.FP8, mxq.FP8_TILE])
+def test_quantize_of_nonfinite_blocks(dtype, fmt):
+    """The scale of a block with an infinity is infinite, its elements 448 (the infinite
+    ones) and 0; that of a block with a NaN is NaN.  No code is NaN, and other blocks
+    are as without them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn((140, 416), generator=g, device="cuda").to(dtype)
+    clean, y = mxq.quantize(x, fmt), x.clone()
+    y[2, 140], y[129, 400], y[130, 30] = INF, -INF, NAN
+    q = mxq.quantize(y, fmt)
+    by_row = lambda t: t if fmt == mxq.FP8_TILE else t.t()   # noqa: E731
+    scales, first = by_row(q.scales), by_row(clean.scales)
+    hit = torch.zeros_like(scales, dtype=torch.bool)
+    row = lambda r: r // 128 if fmt == mxq.FP8_TILE else r   # noqa: E731
+    hit[row(2), 1] = hit[row(129), 3] = hit[row(130), 0] = True
+    assert torch.equal(scales[~hit], first[~hit])
+    assert scales[row(2), 1] == INF and scales[row(129), 3] == INF and bool(scales[row(130), 0].isnan())
+    spread = (hit.repeat_interleave(128, 0)[:140] if fmt == mxq.FP8_TILE else hit).repeat_interleave(128, 1)[:, :416]
+    assert torch.equal(q.codes[~spread], clean.codes[~spread])
+    assert not bool(((q.codes & 127) == 127).any())
+    infinite = spread & ~(scales.isnan().repeat_interleave(128, 0)[:140] if fmt == mxq.FP8_TILE
+                          else scales.isnan()).repeat_interleave(128, 1)[:, :416]
+    want = torch.where(y.isinf(), 126, 0).to(torch.uint8) | torch.where(torch.signbit(y), 128, 0).to(torch.uint8)
+    assert torch.equal(q.codes[infinite], want[infinite])
+
+
+@pytest.mark.parametrize("fmt", [mxq.FP8, mxq.FP8_TILE])
+@pytest.mark.parametrize("had", [16, 128])
+def test_quantize_rotates_a_nan_into_its_block(fmt, had):
+    """Sums with a NaN (or of opposite infinities) are NaN: so is their block's scale, and no code is."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x = torch.randn((140, 384), generator=g, device="cuda")
+    clean, y = mxq.quantize(x, fmt, hadamard=had), x.clone()
+    y[3, 200], y[135, 1], y[135, 2] = NAN, INF, -INF
+    q = mxq.quantize(y, fmt, hadamard=had)
+    scales, first = (t.scales if fmt == mxq.FP8_TILE else t.scales.t() for t in (q, clean))
+    hit = torch.zeros_like(scales, dtype=torch.bool)
+    row = lambda r: r // 128 if fmt == mxq.FP8_TILE else r   # noqa: E731
+    hit[row(3), 1] = hit[row(135), 0] = True
+    assert bool(scales[hit].isnan().all()) and torch.equal(scales[~hit], first[~hit])
+    assert not bool(((q.codes & 127) == 127).any())
