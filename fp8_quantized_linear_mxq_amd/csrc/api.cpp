@@ -73,6 +73,7 @@ mxq_status check_qtensor(const mxq_qtensor* t) {
 
 constexpr int64_t kMaxKInt8 = 1 << 17, kMaxLdInt8 = 1 << 24;
 constexpr int64_t kMaxLd = 1 << 24;   // bytes between rows, FP8 and the gated products
+constexpr int64_t kMaxRowsFp8 = INT32_MAX - 511;   // rows of the FP8 products: those past the end of a tile are counted in int32 too
 constexpr int32_t kMaxGroups = 1 << 16;
 constexpr int64_t kMaxNormCols = 1 << 26;
 
@@ -346,6 +347,7 @@ static mxq_status gemm_checks(const mxq_qtensor* a, const mxq_qtensor* w, const 
   // int8 sums stay within int32 up to K = 2**17
   if (f8 ? a->cols == 0 : i8 ? a->cols == 0 || a->cols > kMaxKInt8 : a->cols % 128 != 0) return MXQ_ERR_SHAPE;
   if (f8 && (a->ld_codes > kMaxLd || w->ld_codes > kMaxLd)) return MXQ_ERR_SHAPE;
+  if (f8 && (a->rows > kMaxRowsFp8 || w->rows > kMaxRowsFp8)) return MXQ_ERR_SHAPE;
   if (i8 && (a->ld_codes > kMaxLdInt8 || w->ld_codes > kMaxLdInt8)) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX || w->rows > INT32_MAX || a->cols > INT32_MAX || n_out > INT32_MAX)
     return MXQ_ERR_SHAPE;
@@ -482,7 +484,7 @@ mxq_status mxq_gemm_grouped(const mxq_qtensor* a, const mxq_qtensor* w, int32_t 
   if (f8 && n % 128) return MXQ_ERR_SHAPE;   // an expert's tiles are its own
   if (a->rows == 0 || n == 0) return MXQ_OK;
   if (a->cols == 0 || (i8 ? a->cols > kMaxKInt8 : !f8 && a->cols % 128 != 0)) return MXQ_ERR_SHAPE;
-  if (f8 && (a->ld_codes > kMaxLd || w->ld_codes > kMaxLd)) return MXQ_ERR_SHAPE;
+  if (f8 && (a->ld_codes > kMaxLd || w->ld_codes > kMaxLd || n > kMaxRowsFp8)) return MXQ_ERR_SHAPE;
   if (i8 && (a->ld_codes > kMaxLdInt8 || w->ld_codes > kMaxLdInt8)) return MXQ_ERR_SHAPE;
   if (a->rows > INT32_MAX / 2 || w->rows > INT32_MAX || a->cols > INT32_MAX) return MXQ_ERR_SHAPE;
   if (!offsets || !out || ld_out < n) return MXQ_ERR_INVALID_ARG;

@@ -320,7 +320,7 @@ mxq_status mxq_quantize_noalloc(const void* x, int32_t dtype, int64_t rows, int6
  *              route and with a low-rank branch, it is unused.
  * Requirements: a->cols == w->cols == K, K a multiple of 128; INT8: K a
  * multiple of 32, 32 .. 2**17, row strides at most 2**24 bytes; FP8: K a multiple
- * of 32, not 0, row strides at most 2**24 bytes.
+ * of 32, not 0, row strides at most 2**24 bytes, M and N at most 2**31 - 512.
  * M or N of 0 is a no-op.  Accumulation is fp32; long K is summed in slabs.
  */
 mxq_status mxq_gemm(const mxq_qtensor* a, const mxq_qtensor* w, const int32_t* w_out_col,
@@ -363,7 +363,7 @@ mxq_status mxq_gemm_mixed(const mxq_qtensor* a, const mxq_qtensor* w_groups, int
  *              access outside the operands.
  *  bias        optional device bf16 [n_groups][N].
  *  out         device bf16 [M][ld_out], N columns; 2-byte aligned.
- * K and row strides as in mxq_gemm, K not 0.  M = 0 or N = 0 is a no-op.
+ * K, N and row strides as in mxq_gemm, K not 0.  M = 0 or N = 0 is a no-op.
  * Error bound as in mxq_gemm; long K is summed in slabs here too.
  * The kernel is chosen by the sizes (few rows per expert, or few output tiles:
  * one that streams the weights of the experts hit), never by what offsets holds.

@@ -30,7 +30,7 @@ def weights(n, k):
     return mxq.fp8_operand(v.to(torch.float8_e4m3fn), torch.ones(((n + 127) // 128, 1), device="cuda"), tile=True), v.double()
 
 
-@pytest.mark.parametrize("m,n", [((1 << 30) + 30, 8)])
+@pytest.mark.parametrize("m,n", [((1 << 30) + 30, 8), ((1 << 31) - 512, 1)])
 def test_products_of_many_rows(m, n):
     """Every row has the scale of its own: the first tile is 2**30 rows and more from the last."""
     room(110)
@@ -41,3 +41,17 @@ def test_products_of_many_rows(m, n):
     same_blocks(y, want)
     rest = m % BLOCK
     assert torch.equal(y[m - rest:], want[:rest])
+
+
+def test_products_of_many_columns():
+    room(90)
+    n = (1 << 31) - 512
+    gu.say(f"fp8 1 x {n} x 32")
+    (w, wv), (a, av) = rows_of(n, 32), rows_of(1, 32)
+    tile = torch.exp2((torch.arange(-(-n // 128), device="cuda") % 8).float())   # BLOCK / 128 is a multiple of 8
+    y = mxq.gemm(a, mxq.fp8_operand(w.codes, tile[:, None], tile=True))
+    v = w.codes[:BLOCK].view(torch.float8_e4m3fn).double() * tile[:BLOCK // 128].double().repeat_interleave(128)[:, None]
+    want = (av[:1] @ v.t()).float().bfloat16()[0]
+    same_blocks(y[0], want)
+    rest = n % BLOCK
+    assert torch.equal(y[0, n - rest:], want[:rest])
