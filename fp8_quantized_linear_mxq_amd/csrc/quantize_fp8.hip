@@ -222,10 +222,10 @@ __global__ __launch_bounds__(kThreads) void quantize_fp8_tile_kernel(Fp8Params p
 template <int DT, int HAD>
 hipError_t go(Fp8Params p, bool tile, hipStream_t s) {
   if (tile) {
-    p.col_groups = (p.cols + 127) / 128;
+    p.col_groups = (int)((p.cols + (int64_t)127) / 128);
     quantize_fp8_tile_kernel<DT, HAD><<<grid_of((p.rows + 127) / 128 * p.col_groups), kThreads, 0, s>>>(p);
   } else {
-    p.col_groups = (p.cols + 511) / 512;
+    p.col_groups = (int)((p.cols + (int64_t)511) / 512);
     // one row to a wave while that leaves compute units idle, and of fp32 (4096 x 4096
     // 17.4 us, with two 19.0), else two
     if (DT == DT_F32 || (p.rows + 3) / 4 * p.col_groups <= 2048)

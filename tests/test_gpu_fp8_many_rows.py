@@ -55,3 +55,20 @@ def test_products_of_many_columns():
     same_blocks(y[0], want)
     rest = n % BLOCK
     assert torch.equal(y[0, n - rest:], want[:rest])
+
+
+@pytest.mark.parametrize("fmt", [mxq.FP8, mxq.FP8_TILE])
+def test_quantize_of_wide_rows(fmt):
+    """As many columns as an operand can have."""
+    room(30)
+    cols = (1 << 31) - 32
+    gu.say(f"fp8 quantize 1 x {cols}, format {fmt}")
+    block = torch.randn((1, BLOCK), device="cuda").bfloat16()
+    x = block.repeat(1, 1 << 11)[:, :cols]
+    q, want = mxq.quantize(x, fmt), mxq.quantize(block, fmt)
+    whole = cols // BLOCK
+    same_blocks(q.codes[0, :whole * BLOCK], want.codes[0])
+    same_blocks(q.scales.view(-1)[:whole * (BLOCK // 128)], want.scales.view(-1))
+    end = mxq.quantize(block[:, :cols % BLOCK], fmt)   # ends inside a K-block
+    assert torch.equal(q.codes[0, whole * BLOCK:], end.codes[0])
+    assert torch.equal(q.scales.view(-1)[whole * (BLOCK // 128):], end.scales.view(-1))
