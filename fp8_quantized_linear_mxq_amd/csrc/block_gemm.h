@@ -273,6 +273,15 @@ __device__ __forceinline__ void store_tile(int n_lim, int tid, At at, To to) {
   }
 }
 
+// Keeps the compiler from moving a wave's LDS accesses across this point, where its lanes
+// exchange values: the hardware keeps a wave's LDS accesses in order, but a lane's own
+// addresses do not tell the compiler of the others'.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <int EL, int AL, int WL, int EP, bool GRP, int TI, int TJ, int WM, int WN, int DEEP>
 __global__ __launch_bounds__(64 * WM * WN, (BlockGemm<EL, AL, WL, EP, GRP, TI, TJ, WM, WN, DEEP>::PER_EU))
 void block_gemm_kernel(BlockP p, int gm) {
@@ -728,6 +737,7 @@ void block_gemm_kernel(BlockP p, int gm) {
               for (int e = 0; e < 4; ++e) q[e] = side ? acc[i][j + OJ][4 * g + e] : acc[i][j][4 * g + e];
               *reinterpret_cast<v4f*>(own + rl * 144 + (8 * g + 4 * part) * 4) = q;
             }
+            wave_order();   // lanes read what others wrote
             // rows of the tile from the lane's first on, its columns among those that exist
             const bool vec = p.saved_vec;
             const int r0 = vec ? lane >> 3 : lane >> 5, c = vec ? (lane & 7) * 4 : lane & 31;
@@ -743,6 +753,7 @@ void block_gemm_kernel(BlockP p, int gm) {
               for (int t = 0; t < 16; ++t, o += 2 * p.ld_saved)
                 if (2 * t < rows) *o = *reinterpret_cast<const float*>(from + t * 2 * 144);
             }
+            wave_order();   // before the next tile's values take the place
           }
       }
     }
