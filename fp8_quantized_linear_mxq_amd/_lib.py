@@ -192,6 +192,16 @@ def act_format_for_step(table, n_layers: int, n_buckets: int, layer: int, step: 
     return int(lib.mxq_act_format_for_step(buf, n_layers, n_buckets, layer, step, num_steps))
 
 
+def _row_bytes(t, align: int) -> int:
+    """Bytes between rows.  A single row may have any stride in torch (that of a
+    transposed column is 1): one that the library would refuse is replaced."""
+    given = t.stride(0) * t.element_size()
+    if len(t) != 1:
+        return given
+    width = t.numel() * t.element_size()
+    return given if given >= width and given % align == 0 else (width + 15) // 16 * 16
+
+
 @dataclass
 class QTensor:
     """A quantized [rows, cols] operand in device memory (torch uint8 / fp32)."""
@@ -206,9 +216,9 @@ class QTensor:
         codes, scales, ts = self.codes, self.scales, self.tensor_scale
         return QTensorC(self.fmt, 0, self.rows, self.cols,
                         codes.data_ptr() if codes is not None else None,
-                        codes.stride(0) * codes.element_size() if codes is not None else 0,
+                        _row_bytes(codes, 16) if codes is not None else 0,
                         scales.data_ptr() if scales is not None else None,
-                        scales.stride(0) * scales.element_size() if scales is not None else 0,
+                        _row_bytes(scales, 16 if self.fmt == INT4 else 4) if scales is not None else 0,
                         ts.data_ptr() if ts is not None else None)
 
 
