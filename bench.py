@@ -30,6 +30,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -62,10 +63,28 @@ DEFAULT_WORKLOAD = "svdq_r32"
 CSRC = os.path.join(ROOT, "fp8_quantized_linear_mxq_amd", "csrc")
 
 
-def kernel_source_digest() -> str:
+# the sources of the kernels that the workloads run
+WORKLOAD_SOURCES = ("quantize.hip", "lowrank.hip", "gemm_mx.hip", "gemm_dq.hip", "gemm_dqp.hip")
+
+
+def kernel_sources(csrc: str = CSRC) -> list:
+    """Those and the headers they include, but for kernels.h, which declares the launch
+    functions of every operator: what another operator adds changes no kernel here."""
+    names, todo = set(), list(WORKLOAD_SOURCES)
+    while todo:
+        name = todo.pop()
+        if name in names or name == "kernels.h" or not os.path.exists(os.path.join(csrc, name)):
+            continue
+        names.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            todo += re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+    return sorted(names)
+
+
+def kernel_source_digest(csrc: str = CSRC) -> str:
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
-        with open(os.path.join(CSRC, name), "rb") as f:
+    for name in kernel_sources(csrc):
+        with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]
 
