@@ -31,11 +31,12 @@
 // under the MFMAs after it.
 // Converting the codes to bf16 would be exact at 2.4 times the MFMA time.
 //
-// Bound by the MFMAs under the power limit where large: FP8 8192^3 479 us, 2.30 PFLOP/s
-// (400 us on zeros; a loop of MFMAs on random codes in registers reaches 4.1 PFLOP/s, 3.5
-// with the blocks added; the library's product with one scale to a tensor takes 407);
-// bf16 8192 x 2048 x 5632 gated with its pre-activations 392 us, its dx 286 and dW 331,
-// where the library's plain products take 403, 295 and 365.  Small ones wait for memory: a
+// Large ones: FP8 8192^3 479 .. 505 us with the card, 2.18 .. 2.30 PFLOP/s, the MFMAs busy 55% of
+// the time and LDS bank conflicts as long as the other LDS work (400 us on zeros; a loop of
+// MFMAs on random codes in registers reaches 4.1 PFLOP/s, 3.5 with the blocks added; the library's
+// product with one scale to a tensor takes 407 .. 420); bound by the MFMAs under the power limit,
+// bf16 8192 x 2048 x 5632 gated with its pre-activations 354 .. 398 us, its dx 286 .. 303 and dW
+// 331 .. 348, where the library's plain products take 400, 297 and 364.  Small ones wait for memory: a
 // lone workgroup takes 0.84 us to a K-tile of 128 x 128, against 0.2 of MFMAs.
 #pragma once
 

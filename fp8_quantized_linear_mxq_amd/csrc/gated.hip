@@ -12,8 +12,9 @@
 // Backward: one pass over dy, g and u forms P = [dg | du] in bf16, its halves
 // padded with zeros to whole K-tiles of 64 columns and its rows to 64, so that dx is
 // one product over 2 N and both weight gradients are one product over the rows of
-// x, and neither has a K-tile cut short.  8192 x 2048 x 5632: forward 392 us, the pass
-// 102 (bound by memory: 14 bytes to an element, 6.3 TB/s), dx 286, dW 331.
+// x, and neither has a K-tile cut short.  8192 x 2048 x 5632: forward 354 .. 398 us with
+// the card, the pass 102 (bound by memory: 14 bytes to an element, 6.3 TB/s), dx 286 .. 303, dW
+// 331 .. 348.
 #include "block_gemm.h"
 
 #include <algorithm>

@@ -1,8 +1,9 @@
 // Products of E4M3 codes with fp32 block scales (block_gemm.h): the FP8 layer
 //   y[m][n] = RN_bf16(sum over K-blocks b of sa[b][m] sw[n / 128][b] sum_{k in b} a[m][k] w[n][k] + bias[n]),
-// the same grouped by expert, and the gated pair of projections.  8192^3 takes 479 us
-// (2.30 PFLOP/s), 4096 x 4096 x 11008 gated 375 (1.97: 5.4 rounds of tiles take six), 777 x
-// 1184 x 1001 7.8.
+// the same grouped by expert, and the gated pair of projections.  8192^3 takes 479 .. 505 us
+// with the card (2.18 .. 2.30 PFLOP/s), 4096 x 4096 x 11008 gated 376 .. 384 (1.92 .. 1.97: 5.4
+// rounds of tiles take six), 777 x 1184 x 1001 7.7 .. 8.1; 16384 rows of 32 experts, K 2048, N
+// 4096, 170 even (1.62 PFLOP/s) and 225 with half of them one expert's.
 #include "block_gemm.h"
 
 namespace mxq {

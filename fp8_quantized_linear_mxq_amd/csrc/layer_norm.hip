@@ -8,7 +8,7 @@
 // difference of two sums would lose a row whose mean is large.
 //
 // Bound by memory.  Forward: a row is held in registers, one wave to a row while
-// it fits, else four (16384 x 4096 bf16 54 us, 5.0 TB/s; one row of 1152 3.5).
+// it fits, else four (16384 x 4096 bf16 54 .. 58 us, 4.8 TB/s, fp32 107; one row of 1152 3.5).
 // Backward: a persistent grid; a workgroup walks over rows with x and dy of a row in
 // registers and keeps its share of dw and db there too, so both inputs are read once
 // (8192 x 4096 bf16 44 us, 4.6 TB/s).  Each workgroup writes its sums to a row of the

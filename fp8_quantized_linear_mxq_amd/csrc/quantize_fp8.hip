@@ -21,8 +21,10 @@
 // block is held in registers between its maximum and its codes.  A lane takes 8
 // consecutive elements, 16 lanes a row's block, and the maxima are those of the bit
 // patterns, two bf16 to an integer instruction.  Measured: 16384 x 4608 bf16 49 us, 4.7
-// TB/s (57 with inputs from HBM only), 2048 x 4608 in 8.9, 37 x 1184 in 3.3; with a
-// division per block and float64 near ties 62, 15.2 and 11.2.
+// TB/s (57 .. 59 with inputs from HBM only), 2048 x 4608 in 8.9, 37 x 1184 in 3.2 .. 4.0; with a
+// division per block and float64 near ties 62, 15.2 and 11.2.  Tiles: 11008 x 4096 bf16 34 us
+// from HBM, 4.0 TB/s.  Rotations add float64 sums: 16384 x 4608 by 16, 32 and 128 59, 65 and 76
+// us, tiles, which form them twice, 11008 x 4096 by 16 and 128 74 and 138.
 #include "device_common.h"
 #include "kernels.h"
 #include "rows8.h"
