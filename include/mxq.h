@@ -444,6 +444,8 @@ mxq_status mxq_gemm_gated(const mxq_qtensor* x, const mxq_qtensor* w_gate, const
  *              fp32 sums of products with few output tiles, whose K is then split
  *              over more workgroups and added in a fixed order; results are
  *              deterministic for a given workspace size.
+ * The gradients overlap neither an operand nor each other: the weights' are formed
+ * from x after dx is written.
  * Without terms (N = 0 for dx, M = 0 for the weights) a gradient is zero.  A
  * padded row's gradients are zero where its dy is zero, provided its x, g and u
  * are finite.

@@ -1,11 +1,11 @@
-"""NaN and infinities in the gated products, their gradients and the FP8
-quantize: what the formulas give, and nothing in rows and columns beside them."""
+"""NaN and infinities in the FP8 layer, the gated products, their gradients and the layer
+norm: what the formulas give, and nothing in rows and columns beside them."""
 import pytest
 import torch
 
 import fp8_quantized_linear_mxq_amd as mxq
 from tests import gpu_util as gu
-from tests.test_gpu_fp8 import bf16
+from tests.test_gpu_fp8 import bf16, gen, whole
 from tests.test_gpu_gated import exact_case
 
 pytestmark = pytest.mark.gpu
@@ -127,3 +127,43 @@ def test_quantize_rotates_a_nan_into_its_block(fmt, had):
     hit[row(3), 1] = hit[row(135), 0] = True
     assert bool(scales[hit].isnan().all()) and torch.equal(scales[~hit], first[~hit])
     assert not bool(((q.codes & 127) == 127).any())
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 300, 160), (200, 700, 1184), (2100, 2050, 288)])   # few rows, small and large tiles
+def test_fp8_products_keep_nonfinite_scales_to_their_rows_and_tiles(m, n, k):
+    """A NaN or infinite scale reaches its row of outputs, or its tile's columns, alone:
+    also from the last rows, which tiles past the end read again."""
+    gu.say(f"fp8 {m}x{n}x{k}, non-finite scales")
+    g = gen(m + n)
+    (a, av), (w, wv) = whole(g, m, k, False), whole(g, n, k, True)
+    want = bf16(av @ wv.t())
+    a.scales[0, m - 1], w.scales[0, 0] = NAN, INF
+    y = mxq.gemm(a, w)
+    assert bool(y[m - 1].isnan().all()) and not bool(y[:, :min(128, n)].isfinite().any())
+    assert torch.equal(y[:m - 1, 128:], want[:m - 1, 128:])
+    a.scales[0, m - 1], w.scales[0, 0], w.scales[-1, -1] = 1, 1, NAN
+    y, first = mxq.gemm(a, w), (n - 1) // 128 * 128
+    assert bool(y[:, first:].isnan().all()) and bool(y[:, :first].isfinite().all())
+
+
+@pytest.mark.parametrize("cols", [100, 264, 1030, 2048, 16392, 16401])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_layer_norm_keeps_nonfinite_rows_to_themselves(cols, bad):
+    """Also the last row, which groups of waves without a row of their own read."""
+    rows = 37
+    g = torch.Generator(device="cuda")
+    g.manual_seed(cols)
+    x, dy = (torch.randn((rows, cols), generator=g, device="cuda").bfloat16() for _ in range(2))
+    stats = torch.empty((rows, 2), device="cuda")
+    y = mxq.layer_norm(x, stats=stats)
+    dx, dw, _ = mxq.layer_norm_backward(dy, x, stats)
+    z = x.clone()
+    z[5, cols // 2] = z[rows - 1, cols - 1] = bad
+    other = torch.ones(rows, dtype=torch.bool, device="cuda")
+    other[5] = other[rows - 1] = False
+    got = mxq.layer_norm(z, stats=stats)
+    assert torch.equal(got[other], y[other]) and bool(got[~other].isnan().all())
+    gx, gw, _ = mxq.layer_norm_backward(dy, z, stats)
+    assert torch.equal(gx[other], dx[other]) and bool(gx[~other].isnan().all()) and bool(gw.isnan().all())
+    clean = torch.where(other[:, None], dy, torch.zeros_like(dy))   # a padded row's dy is zero: its NaN still is one
+    assert torch.equal(mxq.layer_norm_backward(clean, z, stats)[0][other], dx[other])
